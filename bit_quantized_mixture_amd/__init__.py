@@ -17,6 +17,7 @@ __all__ = [
     "E4B_ROUTE_RENORMALIZE", "E4B_ACT_CLAMPED_GLU", "E4B_GU_INTERLEAVED", "E4B_MXFP4_SCALED", "E4B_MXFP4_FP16", "E4B_COMBINE_ATOMIC", "lib_path", "e4b_version", "e4b_status_string", "e4b_pack_nf4",
     "e4b_pack_mxfp4", "e4b_route_workspace_bytes", "e4b_route_permute", "e4b_moe_workspace_bytes",
     "e4b_moe_forward", "e4b_moe_forward_noalloc", "e4b_noalloc_scratch_bytes", "e4b_stream_probe", "e4b_decode_workspace_bytes", "e4b_moe_decode_step", "MoeArgs", "e4b_dgrad_workspace_bytes", "e4b_grouped_dgrad", "DgradArgs",
+    "e4b_permute_tokens", "e4b_combine_workspace_bytes", "e4b_combine_tokens", "e4b_combine_tokens_backward",
 ]
 
 E4B_FMT_NF4, E4B_FMT_MXFP4 = 0, 1
@@ -26,6 +27,7 @@ E4B_ROUTE_RENORMALIZE = 1
 E4B_ACT_CLAMPED_GLU, E4B_GU_INTERLEAVED = 0x10, 0x20
 E4B_MXFP4_SCALED, E4B_MXFP4_FP16 = 0x40, 0x80
 E4B_COMBINE_ATOMIC = 0x100
+E4B_DT_BF16, E4B_DT_F32 = 0, 1
 _FMT = {"nf4": E4B_FMT_NF4, "mxfp4": E4B_FMT_MXFP4, E4B_FMT_NF4: E4B_FMT_NF4, E4B_FMT_MXFP4: E4B_FMT_MXFP4}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -107,6 +109,11 @@ _c_pack_int4 = _decl("e4b_pack_int4_b32", [_vp, _i64, _i64, _i64, _vp, _vp, _vp]
 _c_quant_act = _decl("e4b_quantize_act_int8", [_vp, _i64, _i64, _vp, _vp, _vp])
 _c_int4_ws = _decl("e4b_int4_gemv_workspace_bytes", [ctypes.POINTER(Int4GemvArgs), ctypes.POINTER(_sz)])
 _c_int4_gemv = _decl("e4b_gemv_int4_b32", [ctypes.POINTER(Int4GemvArgs), _vp])
+_c_permute = _decl("e4b_permute_tokens", [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp])
+_c_combine_ws = _decl("e4b_combine_workspace_bytes", [_i64, _i32, ctypes.POINTER(_sz)])
+_c_combine = _decl("e4b_combine_tokens", [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp, _i32, _vp, _sz, _vp])
+_c_combine_bwd = _decl("e4b_combine_tokens_backward", [_vp, _i32, _vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp,
+                                                       _i32, _vp, _vp, _sz, _vp])
 
 
 class E4BError(RuntimeError):
@@ -187,6 +194,43 @@ def _need(t, name, dtypes, shape=None, device=None):
 
 
 _BF16 = (torch.bfloat16, torch.uint16, torch.int16)
+_ROWS = {torch.bfloat16: E4B_DT_BF16, torch.float32: E4B_DT_F32}
+
+
+class _on_device:
+    """Context of the calls below: the tensors' device made the current one (a launch goes to the
+    current device) and, inside it, the stream of the call: the given one or the device's
+    current one.  A torch stream of another device is refused."""
+
+    def __init__(self, dev, stream):
+        if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
+        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+        self.on = _on_stream(stream)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.on.__enter__()
+
+    def __exit__(self, *exc):
+        self.on.__exit__(*exc)
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+        return False
+
+
+def _rows_dtype(dtype, name):
+    if dtype not in _ROWS:
+        raise ValueError(f"{name} must be torch.bfloat16 or torch.float32, not {dtype}")
+    return _ROWS[dtype]
+
+
+def _need_rows(t, name, shape=None, device=None):
+    _need(t, name, tuple(_ROWS), shape, device)
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got shape {tuple(t.shape)}")
+    return _ROWS[t.dtype]
 
 
 def e4b_pack_nf4(w, packed=None, absmax=None, stream=None):
@@ -631,3 +675,102 @@ def e4b_moe_decode_step(fmt, logits, x, w_gu, s_gu, w_dn, s_dn, k: int, renormal
     a.ws, a.ws_bytes = ws.data_ptr(), ws.numel() * ws.element_size()
     _check("e4b_moe_decode_step", _c_decode_step(ctypes.byref(a), _stream(stream)))
     return out, out_f32, route_out
+
+
+def e4b_permute_tokens(x, sorted_slots, k: int, out=None, stream=None):
+    """The routed copies of the token rows in expert order: out[p] = x[sorted_slots[p] // k].
+
+    x [T, H] bf16 or float32; sorted_slots [T*k] int32 from e4b_route_permute.  Returns out
+    [T*k, H] of x's dtype.  The gradient of x is e4b_combine_tokens(g_out, sorted_slots, k).
+    """
+    dt = _need_rows(x, "x")
+    T, H = x.shape
+    dev = x.device
+    _need(sorted_slots, "sorted_slots", (torch.int32,), (T * k,), dev)
+    with _on_device(dev, stream) as st:
+        if out is None:
+            out = st.alloc((T * k, H), dtype=x.dtype, device=dev)
+        else:
+            _need(out, "out", (x.dtype,), (T * k, H), dev)
+        _check("e4b_permute_tokens", _c_permute(x.data_ptr(), dt, T, H, k, sorted_slots.data_ptr(), out.data_ptr(),
+                                                _stream(stream)))
+    return out
+
+
+def e4b_combine_workspace_bytes(T: int, k: int) -> int:
+    n = _sz(0)
+    _check("e4b_combine_workspace_bytes", _c_combine_ws(T, k, ctypes.byref(n)))
+    return n.value
+
+
+def _combine_ws(st, T, k, ws, dev):
+    """(workspace tensor or None, its address, its bytes) of a combine call."""
+    if ws is None:
+        need = e4b_combine_workspace_bytes(T, k)
+        if not need:
+            return None, None, 0
+        ws = st.alloc((need,), dtype=torch.uint8, device=dev)
+    _need(ws, "ws", (torch.uint8,), device=dev)
+    return ws, ws.data_ptr(), ws.numel()
+
+
+def _tokens_of(rows, k):
+    if k < 1 or rows.shape[0] % k:
+        raise ValueError(f"{rows.shape[0]} rows are not k = {k} rows for each token")
+    return rows.shape[0] // k
+
+
+def e4b_combine_tokens(rows, sorted_slots, k: int, topk_w=None, out=None, dtype=torch.bfloat16, ws=None,
+                       stream=None):
+    """Rows in expert order back to tokens: out[t] = sum_j topk_w[t, j] * (row of slot t*k + j).
+
+    rows [T*k, H] bf16 or float32; sorted_slots [T*k] int32; topk_w [T, k] float32, or None for
+    all weights 1 (the gradient of e4b_permute_tokens).  Returns out [T, H] of `dtype` (bf16 or
+    float32; the dtype of `out` where that is given).  Sums are float32 in the order of j.
+    """
+    rdt = _need_rows(rows, "rows")
+    T, H, dev = _tokens_of(rows, k), rows.shape[1], rows.device
+    _need(sorted_slots, "sorted_slots", (torch.int32,), (T * k,), dev)
+    if topk_w is not None:
+        _need(topk_w, "topk_w", (torch.float32,), (T, k), dev)
+    odt = _rows_dtype(dtype, "dtype") if out is None else _need_rows(out, "out", (T, H), dev)
+    with _on_device(dev, stream) as st:
+        if out is None:
+            out = st.alloc((T, H), dtype=dtype, device=dev)
+        ws, wp, wn = _combine_ws(st, T, k, ws, dev)
+        _check("e4b_combine_tokens", _c_combine(
+            rows.data_ptr(), rdt, T, H, k, sorted_slots.data_ptr(), None if topk_w is None else topk_w.data_ptr(),
+            out.data_ptr(), odt, wp, wn, _stream(stream)))
+    return out
+
+
+def e4b_combine_tokens_backward(g_out, rows, sorted_slots, k: int, topk_w, g_rows=None, g_w=None,
+                                dtype=torch.bfloat16, ws=None, stream=None):
+    """Gradients of e4b_combine_tokens: (g_rows [T*k, H], g_w [T, k] float32).
+
+    g_out [T, H] bf16 or float32; rows, sorted_slots, topk_w as given to the forward call.  g_rows
+    is of `dtype` (or the dtype of `g_rows` where that is given).  rows=None: the router is frozen,
+    g_w is not computed and None is returned for it.
+    """
+    gdt = _need_rows(g_out, "g_out")
+    T, H = g_out.shape
+    dev = g_out.device
+    _need(sorted_slots, "sorted_slots", (torch.int32,), (T * k,), dev)
+    _need(topk_w, "topk_w", (torch.float32,), (T, k), dev)
+    rdt = E4B_DT_BF16 if rows is None else _need_rows(rows, "rows", (T * k, H), dev)
+    if rows is None and g_w is not None:
+        raise ValueError("g_w needs rows")
+    if g_w is not None:
+        _need(g_w, "g_w", (torch.float32,), (T, k), dev)
+    ddt = _rows_dtype(dtype, "dtype") if g_rows is None else _need_rows(g_rows, "g_rows", (T * k, H), dev)
+    with _on_device(dev, stream) as st:
+        if g_rows is None:
+            g_rows = st.alloc((T * k, H), dtype=dtype, device=dev)
+        if g_w is None and rows is not None:
+            g_w = st.alloc((T, k), dtype=torch.float32, device=dev)
+        ws, wp, wn = _combine_ws(st, T, k, ws, dev)
+        _check("e4b_combine_tokens_backward", _c_combine_bwd(
+            g_out.data_ptr(), gdt, None if rows is None else rows.data_ptr(), rdt, T, H, k,
+            sorted_slots.data_ptr(), topk_w.data_ptr(), g_rows.data_ptr(), ddt,
+            None if g_w is None else g_w.data_ptr(), wp, wn, _stream(stream)))
+    return g_rows, g_w

@@ -227,9 +227,108 @@ int int4_check(const e4b_int4_gemv_args* a, int64_t* max_tiles) {
   return E4B_OK;
 }
 
+bool dtype_ok(int32_t d) { return d == E4B_DT_BF16 || d == E4B_DT_F32; }
+
+// Sizes of the token permutation calls: T tokens, k slots each, rows of H elements.
+int check_tokens(int64_t T, int64_t H, int32_t k) {
+  if (T < 0 || H <= 0 || k < 1) return E4B_ERR_ARG;
+  if (k > 64) return E4B_ERR_SHAPE;
+  const int64_t lim = int64_t(1) << 31;
+  if (T >= lim || T * k >= lim || H >= lim) return E4B_ERR_OVERFLOW;
+  // byte offsets are 64-bit; the row blocks have to fit a grid
+  if (T * k > (int64_t(1) << 50) / H || e4b::combine_blocks(T, H, k) >= lim ||
+      e4b::permute_blocks(T * k, 2 * H) >= lim)
+    return E4B_ERR_OVERFLOW;
+  return E4B_OK;
+}
+
+size_t combine_ws_bytes(int64_t T, int32_t k) { return align_up(size_t(e4b::combine_inv_slots(T * k)) * 4); }
+
 }  // namespace
 
 extern "C" {
+
+int e4b_permute_tokens(const void* x, int32_t dtype, int64_t T, int64_t H, int32_t k,
+                       const int32_t* sorted_slots, void* rows, void* stream) {
+  if (!dtype_ok(dtype)) return E4B_ERR_ARG;
+  int st = check_tokens(T, H, k);
+  if (st != E4B_OK) return st;
+  if (T == 0) return check_device();
+  if (!x || !sorted_slots || !rows) return E4B_ERR_ARG;
+  if (!aligned16(x) || !aligned16(sorted_slots) || !aligned16(rows)) return E4B_ERR_ALIGN;
+  if ((st = check_device()) != E4B_OK) return st;
+  return launched(e4b::launch_permute(x, dtype == E4B_DT_F32 ? 2 : 1, T * k, H, k, sorted_slots, rows,
+                                      (hipStream_t)stream));
+}
+
+int e4b_combine_workspace_bytes(int64_t T, int32_t k, size_t* bytes) {
+  if (!bytes) return E4B_ERR_ARG;
+  const int st = check_tokens(T, 1, k);
+  if (st != E4B_OK) return st;
+  *bytes = combine_ws_bytes(T, k);
+  return E4B_OK;
+}
+
+int e4b_combine_tokens(const void* rows, int32_t rows_dtype, int64_t T, int64_t H, int32_t k,
+                       const int32_t* sorted_slots, const float* topk_w, void* out, int32_t out_dtype,
+                       void* ws, size_t ws_bytes, void* stream) {
+  if (!dtype_ok(rows_dtype) || !dtype_ok(out_dtype)) return E4B_ERR_ARG;
+  int st = check_tokens(T, H, k);
+  if (st != E4B_OK) return st;
+  if (T == 0) return check_device();
+  if (!rows || !sorted_slots || !out) return E4B_ERR_ARG;
+  const void* ptrs[] = {rows, sorted_slots, topk_w, out, ws};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return E4B_ERR_ALIGN;
+  const size_t need = combine_ws_bytes(T, k);
+  if (need && (!ws || ws_bytes < need)) return E4B_ERR_WORKSPACE;
+  if ((st = check_device()) != E4B_OK) return st;
+  e4b::CombineLaunch L{};
+  L.T = T;
+  L.H = H;
+  L.k = k;
+  L.rows_dtype = rows_dtype;
+  L.out_dtype = out_dtype;
+  L.rows = rows;
+  L.slots = sorted_slots;
+  L.w = topk_w;
+  L.out = out;
+  L.inv = static_cast<int32_t*>(ws);
+  return launched(e4b::launch_combine(L, (hipStream_t)stream));
+}
+
+int e4b_combine_tokens_backward(const void* g_out, int32_t g_dtype, const void* rows, int32_t rows_dtype,
+                                int64_t T, int64_t H, int32_t k, const int32_t* sorted_slots,
+                                const float* topk_w, void* g_rows, int32_t g_rows_dtype, float* g_w,
+                                void* ws, size_t ws_bytes, void* stream) {
+  if (!dtype_ok(g_dtype) || !dtype_ok(rows_dtype) || !dtype_ok(g_rows_dtype)) return E4B_ERR_ARG;
+  int st = check_tokens(T, H, k);
+  if (st != E4B_OK) return st;
+  if (T == 0) return check_device();
+  if (!g_out || !sorted_slots || !topk_w || !g_rows) return E4B_ERR_ARG;
+  if (g_w && !rows) return E4B_ERR_ARG;  // the weights' gradient needs the rows
+  const void* ptrs[] = {g_out, rows, sorted_slots, topk_w, g_rows, g_w, ws};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return E4B_ERR_ALIGN;
+  const size_t need = combine_ws_bytes(T, k);
+  if (need && (!ws || ws_bytes < need)) return E4B_ERR_WORKSPACE;
+  if ((st = check_device()) != E4B_OK) return st;
+  e4b::CombineBackwardLaunch L{};
+  L.T = T;
+  L.H = H;
+  L.k = k;
+  L.g_dtype = g_dtype;
+  L.rows_dtype = rows_dtype;
+  L.g_rows_dtype = g_rows_dtype;
+  L.g_out = g_out;
+  L.rows = rows;
+  L.slots = sorted_slots;
+  L.w = topk_w;
+  L.g_rows = g_rows;
+  L.g_w = g_w;
+  L.inv = static_cast<int32_t*>(ws);
+  return launched(e4b::launch_combine_backward(L, (hipStream_t)stream));
+}
 
 int e4b_pack_int4_b32(const uint16_t* w, int64_t E, int64_t N, int64_t K, uint8_t* packed,
                       uint16_t* scales, void* stream) {

@@ -161,6 +161,35 @@ struct DecodeLaunch {
 size_t decode_ctl_bytes(int64_t H);
 hipError_t launch_decode_step(const DecodeLaunch& L, hipStream_t stream);
 
+// Token rows to expert order and back (tokens.hip).  Element types are e4b_dtype values.
+hipError_t launch_permute(const void* x, int elem_halves, int64_t S, int64_t H, int k, const int32_t* slots,
+                          void* rows, hipStream_t stream);
+struct CombineLaunch {
+  int64_t T, H;
+  int k, rows_dtype, out_dtype;
+  const void* rows;
+  const int32_t* slots;
+  const float* w;       // nullable: all weights 1
+  void* out;
+  int32_t* inv;         // workspace [combine_inv_slots(T * k)]
+};
+hipError_t launch_combine(const CombineLaunch& L, hipStream_t stream);
+struct CombineBackwardLaunch {
+  int64_t T, H;
+  int k, g_dtype, rows_dtype, g_rows_dtype;
+  const void* g_out;
+  const void* rows;     // read only for g_w
+  const int32_t* slots;
+  const float* w;
+  void* g_rows;
+  float* g_w;           // nullable
+  int32_t* inv;         // workspace, as above
+};
+hipError_t launch_combine_backward(const CombineBackwardLaunch& L, hipStream_t stream);
+int64_t combine_inv_slots(int64_t S);  // 0: the kernels find the rows themselves
+int64_t permute_blocks(int64_t S, int64_t halves);
+int64_t combine_blocks(int64_t T, int64_t H, int k);
+
 // Streaming read (mode 0; dst: NULL or a 4-byte sink that is never written in practice) or
 // copy (mode 1) of `bytes` (a multiple of 16) with cus * 8 workgroups.
 hipError_t launch_stream_probe(const void* src, void* dst, int64_t bytes, int mode, int cus,

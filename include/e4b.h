@@ -77,6 +77,9 @@ typedef enum e4b_status {
   E4B_ERR_TOO_LARGE = -8    /* more workspace than e4b_moe_forward_noalloc's fixed scratch */
 } e4b_status;
 
+/* Element type of a row matrix in the calls that take either. */
+typedef enum e4b_dtype { E4B_DT_BF16 = 0, E4B_DT_F32 = 1 } e4b_dtype;
+
 typedef enum e4b_fmt { E4B_FMT_NF4 = 0, E4B_FMT_MXFP4 = 1 } e4b_fmt;
 
 /* e4b_route_permute flags */
@@ -181,6 +184,50 @@ int e4b_route_workspace_bytes(int64_t T, int64_t E, int32_t k, size_t* bytes);
 int e4b_route_permute(const float* logits, int64_t T, int64_t E, int32_t k, int32_t flags,
                       int32_t* topk_ids, float* topk_w, int32_t* expert_offsets,
                       int32_t* sorted_slots, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * e4b_permute_tokens — the routed copies of the token rows in expert order, the input of the
+ * grouped products: rows[p] = x[sorted_slots[p] / k].
+ *   x             [T, H] of `dtype` (an e4b_dtype).  Any H >= 1.  1 <= k <= 64, T*k < 2^31.
+ *   sorted_slots  [T*k] int32 from e4b_route_permute: a permutation of 0 .. T*k - 1.
+ *   rows          [T*k, H] of `dtype` out: bit copies.
+ * A slot outside [0, T*k) leaves a row of zeros.  The gradient of x is e4b_combine_tokens of the
+ * rows' gradients with topk_w = NULL.
+ */
+int e4b_permute_tokens(const void* x, int32_t dtype, int64_t T, int64_t H, int32_t k,
+                       const int32_t* sorted_slots, void* rows, void* stream);
+
+/* Workspace bytes of e4b_combine_tokens and e4b_combine_tokens_backward (0 for small batches:
+ * ws may then be NULL). */
+int e4b_combine_workspace_bytes(int64_t T, int32_t k, size_t* bytes);
+
+/*
+ * e4b_combine_tokens — rows in expert order back to tokens, with the routing weights applied:
+ * out[t] = sum_j topk_w[t, j] * rows[p_j], p_j the row with sorted_slots[p_j] = t*k + j
+ * (grouped-nf4-gemm 0.25.0 project description, opening section: the combine).
+ *   rows       [T*k, H] of rows_dtype; out [T, H] of out_dtype.  Any H >= 1, k <= 64.
+ *   topk_w     [T, k] float32, or NULL: all weights 1 (the gradient of e4b_permute_tokens).
+ *   ws         device workspace of at least e4b_combine_workspace_bytes().
+ * Products and sums are float32 in the order of j, rounded once to out_dtype: deterministic.  A
+ * slot that no row names adds nothing; where two rows name one slot the higher row counts.
+ */
+int e4b_combine_tokens(const void* rows, int32_t rows_dtype, int64_t T, int64_t H, int32_t k,
+                       const int32_t* sorted_slots, const float* topk_w, void* out, int32_t out_dtype,
+                       void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * e4b_combine_tokens_backward — the gradients of e4b_combine_tokens:
+ *   g_rows[p_j] = topk_w[t, j] * g_out[t],   g_w[t, j] = sum_h g_out[t, h] * rows[p_j, h].
+ *   g_out   [T, H] of g_dtype; rows [T*k, H] of rows_dtype, as given to the forward call.
+ *   g_rows  [T*k, H] of g_rows_dtype out (bf16 is what e4b_grouped_dgrad takes).
+ *   g_w     [T, k] float32 out, or NULL (frozen router; rows may then be NULL).
+ * Sums are float32 in a fixed order.  A slot that no row names gets g_w = 0; a row that names no
+ * slot is left as it was.
+ */
+int e4b_combine_tokens_backward(const void* g_out, int32_t g_dtype, const void* rows, int32_t rows_dtype,
+                                int64_t T, int64_t H, int32_t k, const int32_t* sorted_slots,
+                                const float* topk_w, void* g_rows, int32_t g_rows_dtype, float* g_w,
+                                void* ws, size_t ws_bytes, void* stream);
 
 /* Arguments of e4b_moe_forward.  Sizes: H % 64 == 0, I % 64 == 0 (both formats); T*H,
  * T*k*I and I*H below 2^31 (E4B_ERR_OVERFLOW otherwise). */
