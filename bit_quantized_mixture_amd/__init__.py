@@ -18,6 +18,8 @@ __all__ = [
     "e4b_pack_mxfp4", "e4b_route_workspace_bytes", "e4b_route_permute", "e4b_moe_workspace_bytes",
     "e4b_moe_forward", "e4b_moe_forward_noalloc", "e4b_noalloc_scratch_bytes", "e4b_stream_probe", "e4b_decode_workspace_bytes", "e4b_moe_decode_step", "MoeArgs", "e4b_dgrad_workspace_bytes", "e4b_grouped_dgrad", "DgradArgs",
     "e4b_permute_tokens", "e4b_combine_workspace_bytes", "e4b_combine_tokens", "e4b_combine_tokens_backward",
+    "LoraArgs", "LoraBackwardArgs", "e4b_lora_workspace_bytes", "e4b_grouped_lora",
+    "e4b_lora_backward_workspace_bytes", "e4b_grouped_lora_backward",
 ]
 
 E4B_FMT_NF4, E4B_FMT_MXFP4 = 0, 1
@@ -83,6 +85,26 @@ class Int4GemvArgs(ctypes.Structure):
     ]
 
 
+class LoraArgs(ctypes.Structure):
+    """Mirror of struct e4b_lora_args."""
+    _fields_ = [
+        ("r", _i32), ("out_dtype", _i32), ("S", _i64), ("K", _i64), ("N", _i64), ("groups", _i64),
+        ("adapters", _i64), ("x", _vp), ("a", _vp), ("b", _vp), ("scale", _vp), ("group_offsets", _vp),
+        ("group_adapter", _vp), ("y", _vp), ("out", _vp), ("z", _vp), ("ws", _vp), ("ws_bytes", _sz),
+        ("reserved", _i64),
+    ]
+
+
+class LoraBackwardArgs(ctypes.Structure):
+    """Mirror of struct e4b_lora_backward_args."""
+    _fields_ = [
+        ("r", _i32), ("gx_dtype", _i32), ("S", _i64), ("K", _i64), ("N", _i64), ("groups", _i64),
+        ("adapters", _i64), ("g", _vp), ("x", _vp), ("z", _vp), ("a", _vp), ("b", _vp), ("scale", _vp),
+        ("group_offsets", _vp), ("group_adapter", _vp), ("gx_base", _vp), ("gx", _vp), ("ga", _vp),
+        ("gb", _vp), ("ws", _vp), ("ws_bytes", _sz), ("reserved", _i64),
+    ]
+
+
 def _decl(name, argtypes, restype=ctypes.c_int):
     fn = getattr(_lib, name)
     fn.argtypes = argtypes
@@ -114,6 +136,10 @@ _c_combine_ws = _decl("e4b_combine_workspace_bytes", [_i64, _i32, ctypes.POINTER
 _c_combine = _decl("e4b_combine_tokens", [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp, _i32, _vp, _sz, _vp])
 _c_combine_bwd = _decl("e4b_combine_tokens_backward", [_vp, _i32, _vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp,
                                                        _i32, _vp, _vp, _sz, _vp])
+_c_lora_ws = _decl("e4b_lora_workspace_bytes", [ctypes.POINTER(LoraArgs), ctypes.POINTER(_sz)])
+_c_lora = _decl("e4b_grouped_lora", [ctypes.POINTER(LoraArgs), _vp])
+_c_lora_bwd_ws = _decl("e4b_lora_backward_workspace_bytes", [ctypes.POINTER(LoraBackwardArgs), ctypes.POINTER(_sz)])
+_c_lora_bwd = _decl("e4b_grouped_lora_backward", [ctypes.POINTER(LoraBackwardArgs), _vp])
 
 
 class E4BError(RuntimeError):
@@ -774,3 +800,162 @@ def e4b_combine_tokens_backward(g_out, rows, sorted_slots, k: int, topk_w, g_row
             sorted_slots.data_ptr(), topk_w.data_ptr(), g_rows.data_ptr(), ddt,
             None if g_w is None else g_w.data_ptr(), wp, wn, _stream(stream)))
     return g_rows, g_w
+
+
+def _lora_common(args, a, b, scale, group_offsets, group_adapter, S, K, N, dev):
+    """Checks the adapters and the groups and fills the fields both adapter calls share."""
+    _need(a, "a", _BF16, device=dev)
+    _need(b, "b", _BF16, device=dev)
+    if a.dim() != 3:
+        raise ValueError(f"a must be [adapters, r, K], got shape {tuple(a.shape)}")
+    n, r = a.shape[0], a.shape[1]
+    if a.shape[2] != K:
+        raise ValueError(f"a has {a.shape[2]} columns, x has {K}")
+    if tuple(b.shape) != (n, N, r):
+        raise ValueError(f"b has shape {tuple(b.shape)}, expected {(n, N, r)}")
+    if scale is not None:
+        _need(scale, "scale", (torch.float32,), (n,), dev)
+        args.scale = scale.data_ptr()
+    _need(group_offsets, "group_offsets", (torch.int32,), device=dev)
+    if group_offsets.dim() != 1 or group_offsets.numel() < 2:
+        raise ValueError("group_offsets must be [groups + 1] with groups >= 1")
+    G = group_offsets.numel() - 1
+    if group_adapter is not None:
+        _need(group_adapter, "group_adapter", (torch.int32,), (G,), dev)
+        args.group_adapter = group_adapter.data_ptr()
+    args.r, args.S, args.K, args.N, args.groups, args.adapters = r, S, K, N, G, n
+    args.a, args.b, args.group_offsets = a.data_ptr(), b.data_ptr(), group_offsets.data_ptr()
+
+
+def _ws_of(query, name, args):
+    n = _sz(0)
+    _check(name, query(ctypes.byref(args), ctypes.byref(n)))
+    return n.value
+
+
+def _give_ws(st, ws, need, args, dev):
+    """Puts the workspace (allocated where ws is None) into args; returns the tensor to keep."""
+    if ws is None:
+        ws = st.alloc((max(need, 256),), dtype=torch.uint8, device=dev)
+    _need(ws, "ws", (torch.uint8,), device=dev)
+    args.ws, args.ws_bytes = ws.data_ptr(), ws.numel()
+    return ws
+
+
+def e4b_lora_workspace_bytes(S: int, K: int, N: int, r: int, groups: int, adapters: int) -> int:
+    a = LoraArgs()
+    a.S, a.K, a.N, a.r, a.groups, a.adapters = S, K, N, r, groups, adapters
+    return _ws_of(_c_lora_ws, "e4b_lora_workspace_bytes", a)
+
+
+def e4b_grouped_lora(x, a, b, scale, group_offsets, group_adapter=None, y=None, out=None, dtype=torch.float32,
+                     z=None, ws=None, stream=None):
+    """Low-rank adapters on grouped rows: out[p] = y[p] + scale[i] * (x[p] @ a[i].T) @ b[i].T for
+    the rows p of a group with adapter i.
+
+    x [S, K] bf16; a [adapters, r, K] and b [adapters, N, r] bf16; scale [adapters] float32 or None;
+    group_offsets [groups+1] int32 (expert_offsets of e4b_route_permute, or a batch's row offsets);
+    group_adapter [groups] int32 (-1: no adapter) or None (group g uses adapter g); y [S, N] bf16 or
+    float32 (the shared projection's output) or None.  out may be y (in place); it is allocated in
+    y's dtype, else `dtype`.  z: True to get x @ a.T [S, r] float32 for the backward call, a tensor
+    to fill, or None.  Returns (out, z or None).  r % 8 == K % 8 == N % 8 == 0, r <= 128.
+    """
+    _need(x, "x", _BF16)
+    if x.dim() != 2:
+        raise ValueError(f"x must be [S, K], got shape {tuple(x.shape)}")
+    S, K = x.shape
+    dev = x.device
+    N = b.shape[1] if isinstance(b, torch.Tensor) and b.dim() == 3 else 0
+    args = LoraArgs()
+    _lora_common(args, a, b, scale, group_offsets, group_adapter, S, K, N, dev)
+    if y is not None:
+        dtype = y.dtype
+        _need_rows(y, "y", (S, N), dev)
+        args.y = y.data_ptr()
+    if out is not None:
+        _need_rows(out, "out", (S, N), dev)
+        if y is not None and out.dtype != dtype:
+            raise ValueError(f"out has dtype {out.dtype}, y has {dtype}")
+        dtype = out.dtype
+    args.out_dtype = _rows_dtype(dtype, "dtype")
+    with _on_device(dev, stream) as st:
+        if out is None:
+            out = st.alloc((S, N), dtype=dtype, device=dev)
+        if z is True:
+            z = st.alloc((S, args.r), dtype=torch.float32, device=dev)
+        if z is not None:
+            _need(z, "z", (torch.float32,), (S, args.r), dev)
+            args.z = z.data_ptr()
+        args.x, args.out = x.data_ptr(), out.data_ptr()
+        need = _ws_of(_c_lora_ws, "e4b_lora_workspace_bytes", args) if ws is None else 0
+        ws = _give_ws(st, ws, need, args, dev)
+        _check("e4b_grouped_lora", _c_lora(ctypes.byref(args), _stream(stream)))
+    return out, z
+
+
+def e4b_lora_backward_workspace_bytes(S: int, K: int, N: int, r: int, groups: int, adapters: int,
+                                      group_adapter: bool = False, gx: bool = True, ga: bool = True,
+                                      gb: bool = True) -> int:
+    """group_adapter: whether the call passes one; gx, ga, gb: whether it wants them."""
+    a = LoraBackwardArgs()
+    a.S, a.K, a.N, a.r, a.groups, a.adapters = S, K, N, r, groups, adapters
+    for name, given in (("group_adapter", group_adapter), ("gx", gx), ("ga", ga), ("gb", gb)):
+        setattr(a, name, 16 if given else None)  # only whether it is NULL counts
+    return _ws_of(_c_lora_bwd_ws, "e4b_lora_backward_workspace_bytes", a)
+
+
+def e4b_grouped_lora_backward(g, x, z, a, b, scale, group_offsets, group_adapter=None, gx_base=None, gx=None,
+                              ga=None, gb=None, dtype=torch.float32, ws=None, stream=None):
+    """Gradients of e4b_grouped_lora: (gx [S, K], ga [adapters, r, K], gb [adapters, N, r]).
+
+    g [S, N] bf16: the gradient of out; x, a, b, scale, group_offsets, group_adapter as given to the
+    forward call and z as it returned.  gx_base [S, K] bf16 or float32 (the base projection's
+    gradient, e.g. of e4b_grouped_dgrad) is added to gx, which may be gx_base itself; gx is
+    allocated in its dtype, else `dtype`.  gx, ga, gb: a tensor to fill, None to allocate it, False
+    where it is not wanted (x may be None without ga, z without gb).  ga and gb are float32.
+    """
+    _need(g, "g", _BF16)
+    if g.dim() != 2:
+        raise ValueError(f"g must be [S, N], got shape {tuple(g.shape)}")
+    S, N = g.shape
+    dev = g.device
+    K = a.shape[2] if isinstance(a, torch.Tensor) and a.dim() == 3 else 0
+    args = LoraBackwardArgs()
+    _lora_common(args, a, b, scale, group_offsets, group_adapter, S, K, N, dev)
+    r, n = args.r, args.adapters
+    if gx is False and gx_base is not None:
+        raise ValueError("gx_base is only for gx")
+    if ga is not False:
+        _need(x, "x", _BF16, (S, K), dev)
+        args.x = x.data_ptr()
+    if gb is not False:
+        _need(z, "z", (torch.float32,), (S, r), dev)
+        args.z = z.data_ptr()
+    if gx_base is not None:
+        dtype = gx_base.dtype
+        _need_rows(gx_base, "gx_base", (S, K), dev)
+        args.gx_base = gx_base.data_ptr()
+    if isinstance(gx, torch.Tensor):
+        _need_rows(gx, "gx", (S, K), dev)
+        if gx_base is not None and gx.dtype != dtype:
+            raise ValueError(f"gx has dtype {gx.dtype}, gx_base has {dtype}")
+        dtype = gx.dtype
+    args.gx_dtype = _rows_dtype(dtype, "dtype")
+    with _on_device(dev, stream) as st:
+        outs = []
+        for name, t, shape, dt in (("gx", gx, (S, K), dtype), ("ga", ga, (n, r, K), torch.float32),
+                                   ("gb", gb, (n, N, r), torch.float32)):
+            if t is False:
+                outs.append(None)
+                continue
+            if t is None:
+                t = st.alloc(shape, dtype=dt, device=dev)
+            else:
+                _need(t, name, (dt,), shape, dev)
+            setattr(args, name, t.data_ptr())
+            outs.append(t)
+        args.g = g.data_ptr()
+        need = _ws_of(_c_lora_bwd_ws, "e4b_lora_backward_workspace_bytes", args) if ws is None else 0
+        ws = _give_ws(st, ws, need, args, dev)
+        _check("e4b_grouped_lora_backward", _c_lora_bwd(ctypes.byref(args), _stream(stream)))
+    return tuple(outs)

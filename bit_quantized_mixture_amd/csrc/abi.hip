@@ -244,9 +244,116 @@ int check_tokens(int64_t T, int64_t H, int32_t k) {
 
 size_t combine_ws_bytes(int64_t T, int32_t k) { return align_up(size_t(e4b::combine_inv_slots(T * k)) * 4); }
 
+// Sizes common to the adapter calls.
+int check_lora(int32_t r, int64_t S, int64_t K, int64_t N, int64_t groups, int64_t adapters,
+               const int32_t* offsets, const int32_t* ids, e4b::LoraGroups* q) {
+  if (S < 0 || K <= 0 || N <= 0 || groups <= 0 || adapters <= 0 || r <= 0) return E4B_ERR_ARG;
+  if (r % 8 || r > 128 || K % 8 || N % 8) return E4B_ERR_SHAPE;
+  const int64_t lim = int64_t(1) << 31, big = int64_t(1) << 48;
+  const int64_t wide = K > N ? K : N;
+  if (S >= lim || wide >= lim || groups >= lim || adapters >= lim || S > big / wide ||
+      adapters > big / (wide * r))
+    return E4B_ERR_OVERFLOW;
+  q->S = S;
+  q->K = K;
+  q->N = N;
+  q->G = groups;
+  q->n = adapters;
+  q->r = r;
+  q->offsets = offsets;
+  q->ids = ids;
+  return e4b::lora_blocks(*q) >= lim ? E4B_ERR_OVERFLOW : E4B_OK;
+}
+
+int lora_launch_of(const e4b_lora_args* a, e4b::LoraLaunch* L) {
+  if (!a || a->reserved != 0 || !dtype_ok(a->out_dtype)) return E4B_ERR_ARG;
+  *L = e4b::LoraLaunch{};
+  const int st = check_lora(a->r, a->S, a->K, a->N, a->groups, a->adapters, a->group_offsets, a->group_adapter, &L->q);
+  if (st != E4B_OK) return st;
+  L->out_dtype = a->out_dtype;
+  L->x = a->x;
+  L->a = a->a;
+  L->b = a->b;
+  L->scale = a->scale;
+  L->y = a->y;
+  L->out = a->out;
+  L->z = a->z;
+  L->ws = a->ws;
+  return E4B_OK;
+}
+
+int lora_backward_launch_of(const e4b_lora_backward_args* a, e4b::LoraBackwardLaunch* L) {
+  if (!a || a->reserved != 0 || !dtype_ok(a->gx_dtype)) return E4B_ERR_ARG;
+  *L = e4b::LoraBackwardLaunch{};
+  const int st = check_lora(a->r, a->S, a->K, a->N, a->groups, a->adapters, a->group_offsets, a->group_adapter, &L->q);
+  if (st != E4B_OK) return st;
+  L->gx_dtype = a->gx_dtype;
+  L->g = a->g;
+  L->x = a->x;
+  L->z = a->z;
+  L->a = a->a;
+  L->b = a->b;
+  L->scale = a->scale;
+  L->gx_base = a->gx_base;
+  L->gx = a->gx;
+  L->ga = a->ga;
+  L->gb = a->gb;
+  L->ws = a->ws;
+  return E4B_OK;
+}
+
 }  // namespace
 
 extern "C" {
+
+int e4b_lora_workspace_bytes(const e4b_lora_args* a, size_t* bytes) {
+  if (!bytes) return E4B_ERR_ARG;
+  e4b::LoraLaunch L;
+  const int st = lora_launch_of(a, &L);
+  if (st != E4B_OK) return st;
+  *bytes = e4b::lora_ws_bytes(L);
+  return E4B_OK;
+}
+
+int e4b_grouped_lora(const e4b_lora_args* a, void* stream) {
+  e4b::LoraLaunch L;
+  int st = lora_launch_of(a, &L);
+  if (st != E4B_OK) return st;
+  if (a->S == 0) return check_device();
+  if (!a->x || !a->a || !a->b || !a->group_offsets || !a->out || !a->ws) return E4B_ERR_ARG;
+  const void* ptrs[] = {a->x, a->a, a->b, a->scale, a->group_offsets, a->group_adapter, a->y, a->out, a->z, a->ws};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return E4B_ERR_ALIGN;
+  if (a->ws_bytes < e4b::lora_ws_bytes(L)) return E4B_ERR_WORKSPACE;
+  if ((st = check_device()) != E4B_OK) return st;
+  return launched(e4b::launch_lora(L, (hipStream_t)stream));
+}
+
+int e4b_lora_backward_workspace_bytes(const e4b_lora_backward_args* a, size_t* bytes) {
+  if (!bytes) return E4B_ERR_ARG;
+  e4b::LoraBackwardLaunch L;
+  const int st = lora_backward_launch_of(a, &L);
+  if (st != E4B_OK) return st;
+  *bytes = e4b::lora_backward_ws_bytes(L);
+  return E4B_OK;
+}
+
+int e4b_grouped_lora_backward(const e4b_lora_backward_args* a, void* stream) {
+  e4b::LoraBackwardLaunch L;
+  int st = lora_backward_launch_of(a, &L);
+  if (st != E4B_OK) return st;
+  if (!a->gx && !a->ga && !a->gb) return E4B_ERR_ARG;
+  // without rows the inputs may be empty; the adapters' gradients are still written (zeros)
+  if (!a->group_offsets || !a->a || !a->b) return E4B_ERR_ARG;
+  if (a->S > 0 && (!a->g || !a->ws || (a->ga && !a->x) || (a->gb && !a->z))) return E4B_ERR_ARG;
+  const void* ptrs[] = {a->g, a->x, a->z, a->a, a->b, a->scale, a->group_offsets, a->group_adapter,
+                        a->gx_base, a->gx, a->ga, a->gb, a->ws};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return E4B_ERR_ALIGN;
+  if (a->S > 0 && a->ws_bytes < e4b::lora_backward_ws_bytes(L)) return E4B_ERR_WORKSPACE;
+  if ((st = check_device()) != E4B_OK) return st;
+  return launched(e4b::launch_lora_backward(L, (hipStream_t)stream));
+}
 
 int e4b_permute_tokens(const void* x, int32_t dtype, int64_t T, int64_t H, int32_t k,
                        const int32_t* sorted_slots, void* rows, void* stream) {

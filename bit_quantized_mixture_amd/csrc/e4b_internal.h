@@ -190,6 +190,47 @@ int64_t combine_inv_slots(int64_t S);  // 0: the kernels find the rows themselve
 int64_t permute_blocks(int64_t S, int64_t halves);
 int64_t combine_blocks(int64_t T, int64_t H, int k);
 
+// Low-rank adapters on grouped rows (lora.hip).
+struct LoraGroups {
+  int64_t S, K, N, G, n;   // rows, x columns, out columns, groups, adapters
+  int r;
+  const int32_t* offsets;  // [G + 1]
+  const int32_t* ids;      // nullable [G]
+};
+struct LoraLaunch {
+  LoraGroups q;
+  int out_dtype;
+  const uint16_t* x;
+  const uint16_t* a;
+  const uint16_t* b;
+  const float* scale;      // nullable
+  const void* y;           // nullable
+  void* out;
+  float* z;                // nullable
+  void* ws;
+};
+struct LoraBackwardLaunch {
+  LoraGroups q;
+  int gx_dtype;
+  const uint16_t* g;
+  const uint16_t* x;
+  const float* z;
+  const uint16_t* a;
+  const uint16_t* b;
+  const float* scale;
+  const void* gx_base;     // nullable
+  void* gx;                // nullable, as are ga and gb
+  float* ga;
+  float* gb;
+  void* ws;
+};
+// Workspace sizes go by q's sizes and ids and by which outputs are set.
+size_t lora_ws_bytes(const LoraLaunch& L);
+size_t lora_backward_ws_bytes(const LoraBackwardLaunch& L);
+int64_t lora_blocks(const LoraGroups& q);
+hipError_t launch_lora(const LoraLaunch& L, hipStream_t stream);
+hipError_t launch_lora_backward(const LoraBackwardLaunch& L, hipStream_t stream);
+
 // Streaming read (mode 0; dst: NULL or a 4-byte sink that is never written in practice) or
 // copy (mode 1) of `bytes` (a multiple of 16) with cus * 8 workgroups.
 hipError_t launch_stream_probe(const void* src, void* dst, int64_t bytes, int mode, int cus,

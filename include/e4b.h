@@ -378,6 +378,83 @@ int e4b_dgrad_workspace_bytes(const e4b_dgrad_args* a, size_t* bytes);
  */
 int e4b_grouped_dgrad(const e4b_dgrad_args* a, void* stream);
 
+/* Arguments of e4b_grouped_lora.  Sizes: K % 8 == 0, N % 8 == 0, r % 8 == 0, 8 <= r <= 128;
+ * S, K, N, groups and adapters below 2^31.  Smaller or mixed ranks: pad A and B with zeros. */
+typedef struct e4b_lora_args {
+  int32_t r;              /* rank */
+  int32_t out_dtype;      /* e4b_dtype of y and out */
+  int64_t S, K, N;        /* grouped rows, columns of x, columns of out */
+  int64_t groups, adapters;
+  const uint16_t* x;      /* [S, K] bf16 bits */
+  const uint16_t* a;      /* [adapters, r, K] bf16 bits */
+  const uint16_t* b;      /* [adapters, N, r] bf16 bits */
+  const float* scale;     /* [adapters] float32, or NULL: all 1 */
+  const int32_t* group_offsets; /* [groups+1]: rows of group g are offsets[g] .. offsets[g+1]-1
+                           * (experts: expert_offsets of e4b_route_permute; requests: the
+                           * batch's row offsets), ascending; clamped to [0, S] */
+  const int32_t* group_adapter; /* [groups] adapter of each group, a value outside
+                           * [0, adapters) (e.g. -1) for none; or NULL: group g uses adapter g */
+  const void* y;          /* [S, N] of out_dtype: what the shared projection gave, or NULL: zeros */
+  void* out;              /* [S, N] of out_dtype out; may be y */
+  float* z;               /* [S, r] float32 out, or NULL: x A^T, kept for the backward call */
+  void* ws;               /* device workspace of at least e4b_lora_workspace_bytes() */
+  size_t ws_bytes;
+  int64_t reserved;       /* must be 0 */
+} e4b_lora_args;
+
+/* Workspace bytes e4b_grouped_lora needs for the sizes in `a`. */
+int e4b_lora_workspace_bytes(const e4b_lora_args* a, size_t* bytes);
+
+/*
+ * e4b_grouped_lora — low-rank adapters of many experts or requests at once, beside a shared
+ * projection (grouped-nf4-gemm 0.25.0 and experts4bit-qlora 0.35.0 project descriptions: the
+ * per-expert adapters of QLoRA training).  For every row p of group g with adapter a:
+ *   z[p] = x[p] A_a^T,   out[p] = y[p] + scale[a] * z[p] B_a^T.
+ * Rows of a group without an adapter get out = y and z = 0; rows outside every group are left as
+ * they were.  z is the float32 sum of exact products, and enters the second product unrounded;
+ * out is rounded once.  Deterministic.  A and B are finite.  Apart from y == out the outputs and
+ * the workspace overlap no other argument.  Synchronous errors as e4b_moe_forward.
+ */
+int e4b_grouped_lora(const e4b_lora_args* a, void* stream);
+
+/* Arguments of e4b_grouped_lora_backward; sizes as for e4b_lora_args. */
+typedef struct e4b_lora_backward_args {
+  int32_t r;
+  int32_t gx_dtype;       /* e4b_dtype of gx_base and gx */
+  int64_t S, K, N;
+  int64_t groups, adapters;
+  const uint16_t* g;      /* [S, N] bf16 bits: gradient of out */
+  const uint16_t* x;      /* [S, K] bf16 bits (read for ga) */
+  const float* z;         /* [S, r] float32 from the forward call (read for gb) */
+  const uint16_t* a;      /* [adapters, r, K] bf16 bits */
+  const uint16_t* b;      /* [adapters, N, r] bf16 bits */
+  const float* scale;     /* [adapters] or NULL */
+  const int32_t* group_offsets;
+  const int32_t* group_adapter; /* or NULL */
+  const void* gx_base;    /* [S, K] of gx_dtype: the base projection's part (e4b_grouped_dgrad),
+                           * or NULL: zeros */
+  void* gx;               /* [S, K] of gx_dtype out, may be gx_base; or NULL: not wanted */
+  float* ga;              /* [adapters, r, K] float32 out, or NULL */
+  float* gb;              /* [adapters, N, r] float32 out, or NULL */
+  void* ws;               /* device workspace of at least e4b_lora_backward_workspace_bytes() */
+  size_t ws_bytes;
+  int64_t reserved;       /* must be 0 */
+} e4b_lora_backward_args;
+
+/* Workspace bytes e4b_grouped_lora_backward needs: by the sizes in `a`, by which of gx, ga and
+ * gb are set and by whether group_adapter is (the pointers are not followed). */
+int e4b_lora_backward_workspace_bytes(const e4b_lora_backward_args* a, size_t* bytes);
+
+/*
+ * e4b_grouped_lora_backward — the gradients of e4b_grouped_lora, with u[p] = scale[a] g[p] B_a:
+ *   gx[p] = gx_base[p] + u[p] A_a,   ga[a] = sum_p u[p]^T x[p],   gb[a] = scale[a] sum_p g[p]^T z[p],
+ * the sums over the rows of every group that uses adapter a (0 for an adapter without rows).
+ * Rows of a group without an adapter get gx = gx_base; rows outside every group are left as they
+ * were.  Float32 sums in a fixed order: deterministic.  ga and gb are overwritten.  At least one
+ * of gx, ga, gb is given.  Synchronous errors as e4b_moe_forward.
+ */
+int e4b_grouped_lora_backward(const e4b_lora_backward_args* a, void* stream);
+
 /*
  * e4b_pack_int4_b32 — round-to-nearest int4-b32 packing of bf16 stacks (grouped-nf4-gemm
  * 0.25.0 project description, opening section: the int4-b32 decode GEMV and its packer; the
