@@ -836,7 +836,9 @@ def _ws_of(query, name, args):
 def _give_ws(st, ws, need, args, dev):
     """Puts the workspace (allocated where ws is None) into args; returns the tensor to keep."""
     if ws is None:
-        ws = st.alloc((max(need, 256),), dtype=torch.uint8, device=dev)
+        if not need:
+            return None
+        ws = st.alloc((need,), dtype=torch.uint8, device=dev)
     _need(ws, "ws", (torch.uint8,), device=dev)
     args.ws, args.ws_bytes = ws.data_ptr(), ws.numel()
     return ws

@@ -251,7 +251,8 @@ int check_lora(int32_t r, int64_t S, int64_t K, int64_t N, int64_t groups, int64
   if (r % 8 || r > 128 || K % 8 || N % 8) return E4B_ERR_SHAPE;
   const int64_t lim = int64_t(1) << 31, big = int64_t(1) << 48;
   const int64_t wide = K > N ? K : N;
-  if (S >= lim || wide >= lim || groups >= lim || adapters >= lim || S > big / wide ||
+  // a tile's rows and an adapter's matrix are addressed with 32-bit byte offsets
+  if (S >= lim || wide > (int64_t(1) << 23) || groups >= lim || adapters >= lim || S > big / wide ||
       adapters > big / (wide * r))
     return E4B_ERR_OVERFLOW;
   q->S = S;
@@ -320,11 +321,13 @@ int e4b_grouped_lora(const e4b_lora_args* a, void* stream) {
   int st = lora_launch_of(a, &L);
   if (st != E4B_OK) return st;
   if (a->S == 0) return check_device();
-  if (!a->x || !a->a || !a->b || !a->group_offsets || !a->out || !a->ws) return E4B_ERR_ARG;
+  if (!a->x || !a->a || !a->b || !a->group_offsets || !a->out) return E4B_ERR_ARG;
   const void* ptrs[] = {a->x, a->a, a->b, a->scale, a->group_offsets, a->group_adapter, a->y, a->out, a->z, a->ws};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return E4B_ERR_ALIGN;
-  if (a->ws_bytes < e4b::lora_ws_bytes(L)) return E4B_ERR_WORKSPACE;
+  const size_t need = e4b::lora_ws_bytes(L);
+  if (need && !a->ws) return E4B_ERR_ARG;
+  if (need && a->ws_bytes < need) return E4B_ERR_WORKSPACE;
   if ((st = check_device()) != E4B_OK) return st;
   return launched(e4b::launch_lora(L, (hipStream_t)stream));
 }
@@ -345,12 +348,14 @@ int e4b_grouped_lora_backward(const e4b_lora_backward_args* a, void* stream) {
   if (!a->gx && !a->ga && !a->gb) return E4B_ERR_ARG;
   // without rows the inputs may be empty; the adapters' gradients are still written (zeros)
   if (!a->group_offsets || !a->a || !a->b) return E4B_ERR_ARG;
-  if (a->S > 0 && (!a->g || !a->ws || (a->ga && !a->x) || (a->gb && !a->z))) return E4B_ERR_ARG;
+  if (a->S > 0 && (!a->g || (a->ga && !a->x) || (a->gb && !a->z))) return E4B_ERR_ARG;
   const void* ptrs[] = {a->g, a->x, a->z, a->a, a->b, a->scale, a->group_offsets, a->group_adapter,
                         a->gx_base, a->gx, a->ga, a->gb, a->ws};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return E4B_ERR_ALIGN;
-  if (a->S > 0 && a->ws_bytes < e4b::lora_backward_ws_bytes(L)) return E4B_ERR_WORKSPACE;
+  const size_t need = a->S > 0 ? e4b::lora_backward_ws_bytes(L) : 0;
+  if (need && !a->ws) return E4B_ERR_ARG;
+  if (need && a->ws_bytes < need) return E4B_ERR_WORKSPACE;
   if ((st = check_device()) != E4B_OK) return st;
   return launched(e4b::launch_lora_backward(L, (hipStream_t)stream));
 }

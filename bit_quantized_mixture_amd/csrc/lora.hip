@@ -29,52 +29,56 @@ struct RowTile {
   int group;
   int64_t row0;
   int rows;        // 1 .. bm; 0: no such tile
-  int64_t kept;    // index among the tiles of groups with more than one (find_tile's `single` false)
+  int kept;        // index among the tiles of groups with more than one (find_tile's `single` false)
 };
 
+// Inclusive sum over the wave's lanes in six steps of the vector unit: shifts by 1, 2, 4 and 8 in
+// each row of 16 lanes, then a row's last lane onto the next row, and lane 31 onto the upper half.
+__device__ __forceinline__ int wave_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
+  return x;
+}
+
+// Rows lo .. hi of group g, clamped to the S rows there are and to ascending order.
+__device__ __forceinline__ void group_rows(const int32_t* __restrict__ offsets, int g, int S, int* lo, int* hi) {
+  const int a = offsets[g], b = offsets[g + 1];
+  *lo = a < 0 ? 0 : (a > S ? S : a);
+  *hi = b < *lo ? *lo : (b > S ? S : b);
+}
+
 // Tile `tile` of the list that cuts every group into pieces of 1 << bm_log2 rows, found by each
-// wave from the offsets (64 groups a step).  Offsets are clamped to [0, S] and to ascending order,
-// so a tile never reaches a row outside the matrices.
-__device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offsets, int G, int64_t S, int bm_log2,
-                                             int64_t tile, bool single) {
+// wave from the offsets, 64 groups a step.
+__device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offsets, int G, int S, int bm_log2,
+                                             uint32_t tile, bool single) {
   const int lane = threadIdx.x & (kWave - 1);
-  int64_t base = 0, kbase = 0;
+  int base = 0, kbase = 0;
   for (int g0 = 0; g0 < G; g0 += kWave) {
-    const int g = g0 + lane;
-    int64_t lo = 0, hi = 0;
-    if (g < G) {
-      lo = offsets[g];
-      hi = offsets[g + 1];
-      lo = lo < 0 ? 0 : (lo > S ? S : lo);
-      hi = hi < lo ? lo : (hi > S ? S : hi);
-    }
-    const int n = int((hi - lo + (int64_t(1) << bm_log2) - 1) >> bm_log2);
+    int lo = 0, hi = 0;
+    if (g0 + lane < G) group_rows(offsets, g0 + lane, S, &lo, &hi);
+    const int n = int((int64_t(hi) - lo + (1 << bm_log2) - 1) >> bm_log2);
     const int k = single && n == 1 ? 0 : n;
-    int ni = n, ki = k;  // inclusive sums over the wave
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-      const int a = __shfl_up(ni, d, kWave), b = __shfl_up(ki, d, kWave);
-      if (lane >= d) {
-        ni += a;
-        ki += b;
-      }
-    }
-    const int total = __shfl(ni, kWave - 1, kWave);
-    if (tile < base + total) {
-      const uint64_t hit = __ballot(tile < base + ni);
-      const int l = __ffsll((unsigned long long)hit) - 1;
-      const int64_t at = tile - (base + __shfl(ni - n, l, kWave));
+    const int ni = wave_scan(n), ki = single ? wave_scan(k) : ni;
+    const int total = __builtin_amdgcn_readlane(ni, kWave - 1);
+    if (int(tile) - base < total) {
+      const int l = __ffsll((unsigned long long)__ballot(int(tile) - base < ni)) - 1;
+      const int nl = __builtin_amdgcn_readlane(n, l);
+      const int at = int(tile) - base - (__builtin_amdgcn_readlane(ni, l) - nl);
+      const int row0 = __builtin_amdgcn_readlane(lo, l) + (at << bm_log2);
+      const int left = __builtin_amdgcn_readlane(hi, l) - row0;
       RowTile t;
       t.group = g0 + l;
-      t.row0 = __shfl(int(lo), l, kWave) + (at << bm_log2);
-      const int64_t left = __shfl(int(hi), l, kWave) - t.row0;
-      t.rows = int(left < (int64_t(1) << bm_log2) ? left : (int64_t(1) << bm_log2));
-      t.kept = kbase + __shfl(ki - k, l, kWave) + at;
-      if (single && __shfl(n, l, kWave) == 1) t.kept = -1;
+      t.row0 = row0;
+      t.rows = left < (1 << bm_log2) ? left : (1 << bm_log2);
+      t.kept = single && nl == 1 ? -1 : kbase + __builtin_amdgcn_readlane(ki - k, l) + at;
       return t;
     }
     base += total;
-    kbase += __shfl(ki, kWave - 1, kWave);
+    kbase += __builtin_amdgcn_readlane(ki, kWave - 1);
   }
   return RowTile{0, 0, 0, 0};
 }
@@ -86,6 +90,103 @@ __device__ __forceinline__ int adapter_of(const int32_t* __restrict__ ids, int g
 
 __device__ __forceinline__ bf16x8 load8(const uint16_t* p) { return *reinterpret_cast<const bf16x8*>(p); }
 
+// Loads and stores go through buffers that end with the tile's rows or the adapter's matrix: a
+// lane's offset is fixed for the tile, the step's offset is scalar, and what lies past the end
+// reads as zero and is not written, with no test (the issue of address arithmetic, four cycles an
+// instruction and wave, was what bounded the small tiles: 27 us against 12 for 64 decoded tokens).
+__device__ __forceinline__ u32x4 buf_load(__amdgpu_buffer_rsrc_t r, uint32_t lane_off, uint32_t off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane_off, off, 0));
+}
+__device__ __forceinline__ bf16x8 buf_load8(__amdgpu_buffer_rsrc_t r, uint32_t lane_off, uint32_t off) {
+  return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(r, lane_off, off, 0));
+}
+constexpr uint32_t kNowhere = 0xFFFFFFF0u;  // past the end of every buffer
+
+// Sums of one wave over its units of the columns: acc[b][k] gets rows 16b .. of the tile by ranks
+// 16k .. .  A unit is U matrix steps, 64 U contiguous bytes of each row; a wave takes the units
+// first + wave, first + wave + waves, ... below `end`, the next one's loads in flight while it
+// multiplies.  The adapter is the matrix instruction's first operand, so a lane ends with 4 ranks
+// of one row.
+template <int RB, int RT, int U>
+__device__ __forceinline__ void shrink_sums(const uint16_t* __restrict__ m, const uint16_t* __restrict__ w, uint32_t C,
+                                            int r, int rows, int first, int end, int waves, f32x4 (&acc)[RB][RT]) {
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 15, q = lane >> 4;
+  const __amdgpu_buffer_rsrc_t mres = buffer_rsrc(m, uint32_t(rows) * C * 2u);
+  const __amdgpu_buffer_rsrc_t wres = buffer_rsrc(w, uint32_t(r) * C * 2u);
+  const uint32_t lane_off = uint32_t(c) * C * 2u + 16u * q, block = 32u * C;  // bytes of 16 rows
+  struct Unit {
+    bf16x8 m[U][RB], w[U][RT];
+  };
+  auto load = [&](int s, Unit& v) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t at = uint32_t(s) * (64u * U) + 64u * u;
+#pragma unroll
+      for (int b = 0; b < RB; ++b) v.m[u][b] = buf_load8(mres, lane_off, at + b * block);
+#pragma unroll
+      for (int k = 0; k < RT; ++k) v.w[u][k] = buf_load8(wres, lane_off, at + k * block);
+    }
+  };
+  auto mma = [&](const Unit& v) {
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int b = 0; b < RB; ++b)
+#pragma unroll
+        for (int k = 0; k < RT; ++k)
+          acc[b][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v.w[u][k], v.m[u][b], acc[b][k], 0, 0, 0);
+  };
+  const int full = int(C / (32u * U)), fend = end < full ? end : full;
+  int s = first + wave;
+  if (s < fend) {
+    Unit a, b;
+    load(s, a);
+    for (; s + waves < fend; s += 2 * waves) {
+      load(s + waves, b);
+      __builtin_amdgcn_sched_barrier(0);
+      mma(a);
+      __builtin_amdgcn_sched_barrier(0);
+      load(s + 2 * waves, a);  // past the piece: read for nothing, inside the buffers or zeros
+      __builtin_amdgcn_sched_barrier(0);
+      mma(b);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (s < fend) {
+      mma(a);
+      s += waves;
+    }
+  }
+  if (s < end) {  // the unit that holds the last columns: zeros past them
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t at = uint32_t(s) * (64u * U) + 64u * u;
+      const uint32_t off = at + 16u * q < 2u * C ? lane_off + at : kNowhere;
+      bf16x8 wv[RT];
+#pragma unroll
+      for (int k = 0; k < RT; ++k) wv[k] = buf_load8(wres, off == kNowhere ? kNowhere : off + k * block, 0);
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        const bf16x8 mv = buf_load8(mres, off == kNowhere ? kNowhere : off + b * block, 0);
+#pragma unroll
+        for (int k = 0; k < RT; ++k)
+          acc[b][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[k], mv, acc[b][k], 0, 0, 0);
+      }
+    }
+  }
+}
+
+// Matrix steps of a unit: two units of RB row and RT rank fragments fit the registers beside the sums.
+constexpr int shrink_steps(int rb, int rt) { return rb + rt <= 3 ? 4 : 2; }
+
+template <int RB, int RT>
+__device__ __forceinline__ void zero_sums(f32x4 (&acc)[RB][RT]) {
+#pragma unroll
+  for (int b = 0; b < RB; ++b)
+#pragma unroll
+    for (int k = 0; k < RT; ++k) acc[b][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+}
+
 struct ShrinkArgs {
   const uint16_t* m;      // [S, C]
   const uint16_t* w;      // [n, r, C]
@@ -93,84 +194,39 @@ struct ShrinkArgs {
   const int32_t* offsets;
   const int32_t* ids;     // nullable: group = adapter
   float* z;               // [ksplit, S, r]
-  int64_t S, C;
-  int G, n, r, bm_log2, ksplit;
+  int64_t C;
+  int S, G, n, r, bm_log2;
+  uint32_t ksplit;
+  int per;                // units of a piece
 };
 
-// A workgroup: up to 16 * RB rows of a group, one of ksplit pieces of the columns; its waves take
-// 32-column steps in turn (256 contiguous bytes of each row together) and their sums meet in LDS.
-// The adapter is the matrix instruction's first operand, so a lane ends with 4 ranks of one row.
+// A workgroup: up to 16 * RB rows of a group and one piece of the columns; its waves'
+// sums meet in LDS.
 template <int RB, int RT>
 __global__ void __launch_bounds__(kThreads) shrink_kernel(ShrinkArgs p) {
   __shared__ f32x4 part[kWaves][RB * RT][kWave];
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
   const int c = lane & 15, q = lane >> 4;
-  const int ks = int(blockIdx.x) % p.ksplit;
-  const RowTile t = find_tile(p.offsets, p.G, p.S, p.bm_log2, int64_t(blockIdx.x) / p.ksplit, false);
+  const uint32_t tile = blockIdx.x / p.ksplit;
+  const int ks = int(blockIdx.x - tile * p.ksplit);
+  const RowTile t = find_tile(p.offsets, p.G, p.S, p.bm_log2, tile, false);
   if (t.rows == 0) return;
   const int a = adapter_of(p.ids, t.group, p.n);
   f32x4 acc[RB][RT];
-#pragma unroll
-  for (int b = 0; b < RB; ++b)
-#pragma unroll
-    for (int k = 0; k < RT; ++k) acc[b][k] = f32x4{0.f, 0.f, 0.f, 0.f};
+  zero_sums(acc);
   if (a >= 0) {
-    const uint16_t* mp[RB];
-    const uint16_t* wp[RT];
-#pragma unroll
-    for (int b = 0; b < RB; ++b) {
-      const int row = 16 * b + c < t.rows ? 16 * b + c : t.rows - 1;  // a row past the tile repeats its last
-      mp[b] = p.m + (t.row0 + row) * p.C + 8 * q;
-    }
-#pragma unroll
-    for (int k = 0; k < RT; ++k) {
-      const int i = 16 * k + c < p.r ? 16 * k + c : p.r - 1;          // ranks past r are not stored
-      wp[k] = p.w + (int64_t(a) * p.r + i) * p.C + 8 * q;
-    }
-    const int64_t steps = (p.C + 31) >> 5, full = p.C >> 5;
-    const int64_t per = (steps + p.ksplit - 1) / p.ksplit;
-    const int64_t end = (ks + 1) * per < steps ? (ks + 1) * per : steps;
-    const int64_t fend = end < full ? end : full;
-    constexpr int U = RB * RT <= 4 ? 4 : 2;
-    int64_t s = ks * per + wave;
-    for (; s + (U - 1) * kWaves < fend; s += U * kWaves) {
-      bf16x8 mv[U][RB], wv[U][RT];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-#pragma unroll
-        for (int b = 0; b < RB; ++b) mv[u][b] = load8(mp[b] + 32 * (s + u * kWaves));
-#pragma unroll
-        for (int k = 0; k < RT; ++k) wv[u][k] = load8(wp[k] + 32 * (s + u * kWaves));
-      }
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-#pragma unroll
-        for (int b = 0; b < RB; ++b)
-#pragma unroll
-          for (int k = 0; k < RT; ++k)
-            acc[b][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[u][k], mv[u][b], acc[b][k], 0, 0, 0);
-    }
-    for (; s < end; s += kWaves) {
-      const bool in = 32 * s + 8 * q < p.C;  // the last step may hold fewer than 32 columns
-      const int64_t at = in ? 32 * s : 0;
-      bf16x8 wv[RT];
-#pragma unroll
-      for (int k = 0; k < RT; ++k) wv[k] = in ? load8(wp[k] + at) : bf16x8{};
-#pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        const bf16x8 mv = in ? load8(mp[b] + at) : bf16x8{};
-#pragma unroll
-        for (int k = 0; k < RT; ++k)
-          acc[b][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[k], mv, acc[b][k], 0, 0, 0);
-      }
-    }
+    constexpr int U = shrink_steps(RB, RT);
+    const int units = int((p.C + 32 * U - 1) / (32 * U));
+    const int end = (ks + 1) * p.per < units ? (ks + 1) * p.per : units;
+    shrink_sums<RB, RT, U>(p.m + t.row0 * p.C, p.w + int64_t(a) * p.r * p.C, uint32_t(p.C), p.r, t.rows, ks * p.per, end, kWaves,
+                        acc);
   }
 #pragma unroll
   for (int b = 0; b < RB; ++b)
 #pragma unroll
     for (int k = 0; k < RT; ++k) part[wave][b * RT + k][lane] = acc[b][k];
-  __syncthreads();
   const float sc = a >= 0 && p.scale ? p.scale[a] : 1.f;
+  __syncthreads();
   float* z = p.z + int64_t(ks) * p.S * p.r;
 #pragma unroll
   for (int i0 = 0; i0 < RB * RT; i0 += kWaves) {
@@ -184,6 +240,162 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(ShrinkArgs p) {
   }
 }
 
+// The three parts of v, v = hi + mid + lo exactly, each the 8 leading bits of what is left.  An
+// infinity or NaN stands in the first part alone.
+struct Parts {
+  uint32_t hi, mid, lo;  // bf16 in the upper half
+};
+__device__ __forceinline__ Parts split3(float v) {
+  const uint32_t b = __float_as_uint(v);
+  const bool finite = (b & 0x7F800000u) != 0x7F800000u;
+  const float r1 = v - __uint_as_float(b & 0xFFFF0000u);
+  const uint32_t b1 = __float_as_uint(r1);
+  const float r2 = r1 - __uint_as_float(b1 & 0xFFFF0000u);
+  Parts p;
+  p.hi = finite ? b : b | ((b & 0x007FFFFFu) ? 0x00400000u : 0u);
+  p.mid = finite ? b1 : 0u;
+  p.lo = finite ? __float_as_uint(r2) : 0u;
+  return p;
+}
+// The upper halves of two words as one (first in the low half).
+__device__ __forceinline__ uint32_t hi2(uint32_t first, uint32_t second) { return perm(second, first, 0x07060302u); }
+
+// Geometry of the second product at RP ranks (r rounded up to a power of two) and out type ODT: the
+// row's z stands as hi | mid | lo parts of RP ranks behind one another in the contraction; a wave
+// takes 128 bytes of every row at a time, kH matrix tiles whose rows are dealt out so that a lane
+// holds 32 consecutive bytes of one row.
+template <int RP, int ODT>
+struct Expand {
+  static constexpr int kSteps = (3 * RP + 31) / 32;      // 32-deep matrix steps over the three parts
+  static constexpr int kFrags = RP >= 32 ? RP / 32 : 1;  // distinct adapter fragments among them
+  static constexpr int kStride = 32 * kSteps + 8;        // LDS row in bf16 (16 rows hit distinct banks)
+  static constexpr int kH = ODT == 0 ? 4 : 2;
+  static constexpr int kLaneCols = 4 * kH, kCols = 16 * kH;
+  typedef row_elem<ODT> out_t;
+
+  // Ranks rank .. rank + 3 of one row into the LDS row zr.
+  static __device__ __forceinline__ void put(uint16_t* zr, int rank, f32x4 v) {
+    Parts s[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s[j] = split3(v[j]);
+    *reinterpret_cast<u32x2*>(zr + rank) = u32x2{hi2(s[0].hi, s[1].hi), hi2(s[2].hi, s[3].hi)};
+    *reinterpret_cast<u32x2*>(zr + RP + rank) = u32x2{hi2(s[0].mid, s[1].mid), hi2(s[2].mid, s[3].mid)};
+    *reinterpret_cast<u32x2*>(zr + 2 * RP + rank) = u32x2{hi2(s[0].lo, s[1].lo), hi2(s[2].lo, s[3].lo)};
+    if (3 * RP + rank < 32 * kSteps) *reinterpret_cast<u32x2*>(zr + 3 * RP + rank) = u32x2{0u, 0u};
+  }
+
+  // What a step of 128 bytes a row reads: the rows' bytes and the adapter's fragments.
+  template <int RB>
+  struct Step {
+    u32x4 y[RB][2];
+    bf16x8 w[kH][kFrags];
+  };
+  static constexpr uint32_t kSize = sizeof(out_t);
+
+  // The rows of a tile (row 0 at base and out) and the adapter's [C, r].
+  template <int RB>
+  struct Rows {
+    __amdgpu_buffer_rsrc_t base, out, w;
+    uint32_t C, r, row_off, w_off[kFrags];
+    bool adapter;
+
+    __device__ __forceinline__ Rows(const out_t* base_, out_t* out_, const uint16_t* w_, uint32_t C_, int r_, int rows,
+                                    bool adapter_)
+        : base(buffer_rsrc(base_, base_ ? uint32_t(rows) * C_ * kSize : 0u)),  // no base: all of it reads as zero
+          out(buffer_rsrc(out_, uint32_t(rows) * C_ * kSize)),
+          w(buffer_rsrc(w_, C_ * uint32_t(r_) * 2u)), C(C_), r(uint32_t(r_)), adapter(adapter_) {
+      const uint32_t lane = threadIdx.x & (kWave - 1), c = lane & 15, q = lane >> 4;
+      row_off = (c * C + kLaneCols * q) * kSize;
+#pragma unroll
+      for (int f = 0; f < kFrags; ++f) {
+        const uint32_t rank = (32u * f + 8u * q) % RP;  // ranks past r meet zeros of z
+        w_off[f] = ((kLaneCols * (c >> 2) + (c & 3)) * r + (rank < r ? rank : 0u)) * 2u;
+      }
+    }
+
+    // The lane's offset of its 16-byte piece e of a row in step s, apart from the row block's.
+    __device__ __forceinline__ uint32_t piece(uint32_t s, int e) const {
+      const uint32_t q = (threadIdx.x & (kWave - 1)) >> 4;
+      const uint32_t col = kCols * s + kLaneCols * q + (16 / kSize) * e;
+      return col < C ? row_off + kCols * kSize * s + 16u * e : kNowhere;
+    }
+
+    __device__ __forceinline__ void load(uint32_t s, Step<RB>& t) const {
+      const bool whole = kCols * (s + 1) <= C;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (whole) {
+#pragma unroll
+          for (int b = 0; b < RB; ++b)
+            t.y[b][e] = buf_load(base, row_off, kCols * kSize * s + 16u * e + b * 16u * C * kSize);
+        } else {
+          const uint32_t at = piece(s, e);
+#pragma unroll
+          for (int b = 0; b < RB; ++b)
+            t.y[b][e] = buf_load(base, at == kNowhere ? kNowhere : at + b * 16u * C * kSize, 0);
+        }
+      }
+      if (adapter) {
+#pragma unroll
+        for (int h = 0; h < kH; ++h)
+#pragma unroll
+          for (int f = 0; f < kFrags; ++f) t.w[h][f] = buf_load8(w, w_off[f], (kCols * s + 4u * h) * r * 2u);
+      }
+    }
+
+    __device__ __forceinline__ void finish(uint32_t s, const Step<RB>& t, const bf16x8 (&zf)[RB][kSteps]) const {
+      const bool whole = kCols * (s + 1) <= C;
+#pragma unroll
+      for (int b = 0; b < RB; ++b) {
+        f32x4 d[kH];
+#pragma unroll
+        for (int h = 0; h < kH; ++h) d[h] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (adapter) {
+#pragma unroll
+          for (int k = 0; k < kSteps; ++k)
+#pragma unroll
+            for (int h = 0; h < kH; ++h)
+              d[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t.w[h][k % kFrags], zf[b][k], d[h], 0, 0, 0);
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          u32x4 o;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (ODT == 1) {
+              o[j] = __float_as_uint(__uint_as_float(t.y[b][e][j]) + d[e][j]);
+            } else {
+              const int i = 8 * e + 2 * j;
+              o[j] = bf16_rne2(__uint_as_float(t.y[b][e][j] << 16) + d[i >> 2][i & 3],
+                               __uint_as_float(t.y[b][e][j] & 0xFFFF0000u) + d[i >> 2][(i & 3) + 1]);
+            }
+          }
+          const uint32_t blk = b * 16u * C * kSize;
+          if (whole) {
+            __builtin_amdgcn_raw_buffer_store_b128(o, out, row_off, kCols * kSize * s + 16u * e + blk, 0);
+          } else {
+            const uint32_t at = piece(s, e);
+            __builtin_amdgcn_raw_buffer_store_b128(o, out, at == kNowhere ? kNowhere : at + blk, 0, 0);
+          }
+        }
+      }
+    }
+  };
+
+  template <int RB>
+  static __device__ __forceinline__ void fragments(const uint16_t* zs, bf16x8 (&zf)[RB][kSteps]) {
+    const int lane = threadIdx.x & (kWave - 1), c = lane & 15, q = lane >> 4;
+#pragma unroll
+    for (int b = 0; b < RB; ++b)
+#pragma unroll
+      for (int k = 0; k < kSteps; ++k)
+        zf[b][k] = *reinterpret_cast<const bf16x8*>(zs + (16 * b + c) * kStride + 32 * k + 8 * q);
+  }
+
+  // Steps whose loads a wave has in flight together.
+  static constexpr int ahead(int rb) { return rb == 1 ? (RP <= 32 ? 4 : 2) : (rb == 2 && RP <= 32 ? 2 : 1); }
+};
+
 struct ExpandArgs {
   const float* z;         // [ksplit, S, r]: the sum over ksplit is taken here
   const uint16_t* w;      // [n, C, r]
@@ -193,126 +405,147 @@ struct ExpandArgs {
   const void* base;       // nullable [S, C]
   void* out;              // [S, C]
   float* z_out;           // nullable [S, r]: the summed z
-  int64_t S, C;
-  int G, n, r, bm_log2, ksplit, chunks;
+  int64_t C;
+  int S, G, n, r, bm_log2, ksplit;
+  uint32_t chunks;
+  int per;                // column steps of a chunk
 };
 
-// v = hi + mid + lo exactly: each part the 8 leading bits of what is left.  An infinity or NaN
-// stands in the first part alone.
-__device__ __forceinline__ void split3(float v, uint16_t (&h)[3]) {
-  const uint32_t b = __float_as_uint(v);
-  h[0] = uint16_t(b >> 16);
-  if ((b & 0x7F800000u) == 0x7F800000u) {
-    if ((b & 0x007FFFFFu) != 0) h[0] |= 0x40;
-    h[1] = h[2] = 0;
-    return;
-  }
-  const float r1 = v - __uint_as_float(b & 0xFFFF0000u);
-  const uint32_t b1 = __float_as_uint(r1);
-  h[1] = uint16_t(b1 >> 16);
-  h[2] = uint16_t(__float_as_uint(r1 - __uint_as_float(b1 & 0xFFFF0000u)) >> 16);
-}
-
-// A workgroup: up to 16 * RB rows of a group and one of `chunks` pieces of the columns.  The rows'
-// z stands in registers as hi | mid | lo parts of RP (r rounded up to a power of two) ranks each;
-// waves take 32 columns at a time: two matrix tiles whose rows are dealt out so that a lane holds
-// 8 consecutive columns of one row.
+// A workgroup: up to 16 * RB rows of a group and one piece of the columns.
 template <int RB, int RP, int ODT>
 __global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs p) {
-  constexpr int kSteps = (3 * RP + 31) / 32;           // 32-deep matrix steps over the three parts
-  constexpr int kFrags = RP >= 32 ? RP / 32 : 1;       // distinct adapter fragments among them
-  constexpr int kStride = 32 * kSteps + 8;             // LDS row in bf16 (16 rows hit distinct banks)
-  __shared__ __attribute__((aligned(16))) uint16_t zs[16 * RB * kStride];
-  typedef row_elem<ODT> out_t;
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
-  const int c = lane & 15, q = lane >> 4;
-  const int chunk = int(blockIdx.x) % p.chunks;
-  const RowTile t = find_tile(p.offsets, p.G, p.S, p.bm_log2, int64_t(blockIdx.x) / p.chunks, false);
+  typedef Expand<RP, ODT> X;
+  __shared__ __attribute__((aligned(16))) uint16_t zs[16 * RB * X::kStride];
+  const uint32_t tile = blockIdx.x / p.chunks;
+  const int chunk = int(blockIdx.x - tile * p.chunks);
+  const RowTile t = find_tile(p.offsets, p.G, p.S, p.bm_log2, tile, false);
   if (t.rows == 0) return;
   const int a = adapter_of(p.ids, t.group, p.n);
-  if (a < 0 && p.base == p.out && !(p.z_out && chunk == 0)) return;  // these rows stay as they are
+  const bool z_out = p.z_out && chunk == 0;
+  if (a < 0 && p.base == p.out && !z_out) return;  // these rows stay as they are
 
   const float sc = a >= 0 && p.scale ? p.scale[a] : 1.f;
-  for (int i = threadIdx.x; i < 16 * RB * 4 * kSteps; i += kThreads) {
-    const int row = i / (4 * kSteps), ch = i % (4 * kSteps);  // 8 positions of the contraction
-    const int part = 8 * ch / RP, rank = 8 * ch % RP;
-    uint16_t h[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    if (part < 3 && row < t.rows && rank < p.r && a >= 0) {
-      const float* zp = p.z + (t.row0 + row) * p.r + rank;
-      float v[8];
-      load_vec<8>(zp, v);
-      for (int k = 1; k < p.ksplit; ++k) {
-        float o[8];
-        load_vec<8>(zp + int64_t(k) * p.S * p.r, o);
+  for (int i = threadIdx.x; i < 16 * RB * (RP / 4); i += kThreads) {  // 4 ranks of a row
+    const int row = i / (RP / 4), rank = 4 * (i % (RP / 4));
+    f32x4 v = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (row < t.rows && rank < p.r) {
+      const int64_t at = (t.row0 + row) * p.r + rank;
+      if (a >= 0) {
+        const int64_t piece = int64_t(p.S) * p.r;
+        for (int k0 = 0; k0 < p.ksplit; k0 += 4) {  // the pieces, four loads in flight (the last repeated)
+          f32x4 o[4];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] += o[j];
-      }
-      if (p.z_out && chunk == 0 && part == 0) store_vec<8>(p.z_out + (t.row0 + row) * p.r + rank, v);
+          for (int k = 0; k < 4; ++k)
+            o[k] = *reinterpret_cast<const f32x4*>(p.z + (k0 + k < p.ksplit ? k0 + k : p.ksplit - 1) * piece + at);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        uint16_t s[3];
-        split3(v[j] * sc, s);
-        h[j] = s[part];
+          for (int k = 0; k < 4; ++k)
+            if (k0 + k < p.ksplit) v += o[k];
+        }
       }
-    } else if (p.z_out && chunk == 0 && part == 0 && row < t.rows && rank < p.r) {
-      const float zero[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      store_vec<8>(p.z_out + (t.row0 + row) * p.r + rank, zero);
+      if (z_out) *reinterpret_cast<f32x4*>(p.z_out + at) = v;
     }
-    u32x4 d;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) d[j] = uint32_t(h[2 * j]) | (uint32_t(h[2 * j + 1]) << 16);
-    *reinterpret_cast<u32x4*>(zs + row * kStride + 8 * ch) = d;
+    X::put(zs + row * X::kStride, rank, v * sc);
   }
   __syncthreads();
   if (a < 0 && p.base == p.out) return;
-  bf16x8 zf[RB][kSteps];
+  bf16x8 zf[RB][X::kSteps];
+  X::template fragments<RB>(zs, zf);
+  const int steps = int((p.C + X::kCols - 1) / X::kCols);
+  const int end = (chunk + 1) * p.per < steps ? (chunk + 1) * p.per : steps;
+  const typename X::out_t* base = static_cast<const typename X::out_t*>(p.base);
+  const typename X::template Rows<RB> rows(base ? base + t.row0 * p.C : nullptr,
+                                           static_cast<typename X::out_t*>(p.out) + t.row0 * p.C,
+                                           p.w + int64_t(a < 0 ? 0 : a) * p.C * p.r, uint32_t(p.C), p.r, t.rows, a >= 0);
+  constexpr int kAhead = X::ahead(RB);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  for (int s = chunk * p.per + wave; s < end; s += kAhead * kWaves) {
+    typename X::template Step<RB> st[kAhead];
 #pragma unroll
-  for (int b = 0; b < RB; ++b)
+    for (int i = 0; i < kAhead; ++i) rows.load(s + i * kWaves, st[i]);
 #pragma unroll
-    for (int k = 0; k < kSteps; ++k)
-      zf[b][k] = *reinterpret_cast<const bf16x8*>(zs + (16 * b + c) * kStride + 32 * k + 8 * q);
+    for (int i = 0; i < kAhead; ++i)
+      if (i == 0 || s + i * kWaves < end) rows.finish(s + i * kWaves, st[i], zf);
+  }
+}
 
-  const int64_t steps = (p.C + 31) >> 5, per = (steps + p.chunks - 1) / p.chunks;
-  const int64_t end = (chunk + 1) * per < steps ? (chunk + 1) * per : steps;
-  const out_t* base = static_cast<const out_t*>(p.base);
-  out_t* out = static_cast<out_t*>(p.out);
-  for (int64_t s = chunk * per + wave; s < end; s += kWaves) {
-    const int64_t col = 32 * s + 8 * q;
-    const bool in = col < p.C;
-    float y[RB][8];
+struct FusedArgs {
+  const uint16_t* x;      // [S, K]
+  const uint16_t* a;      // [n, r, K]
+  const uint16_t* b;      // [n, N, r]
+  const float* scale;
+  const int32_t* offsets;
+  const int32_t* ids;
+  const void* y;
+  void* out;
+  float* z;               // nullable
+  int64_t K, N;
+  int S, G, n, r;
+  uint32_t chunks;
+  int per;
+};
+
+constexpr int kFusedWaves = 16;
+
+// Both products in one launch for tiles of at most 16 rows (decoded tokens): every workgroup of a
+// tile computes the tile's z for itself, from the adapter's A in the L2 cache, instead of waiting
+// for another launch to do it.
+template <int RP, int ODT>
+__global__ void __launch_bounds__(kFusedWaves * kWave) fused_kernel(FusedArgs p) {
+  typedef Expand<RP, ODT> X;
+  constexpr int RT = (RP + 15) / 16;
+  __shared__ f32x4 part[kFusedWaves][RT][kWave];
+  __shared__ __attribute__((aligned(16))) uint16_t zs[16 * X::kStride];
+  const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t tile = blockIdx.x / p.chunks;
+  const int chunk = int(blockIdx.x - tile * p.chunks);
+  const RowTile t = find_tile(p.offsets, p.G, p.S, 4, tile, false);
+  if (t.rows == 0) return;
+  const int a = adapter_of(p.ids, t.group, p.n);
+  const bool z_out = p.z && chunk == 0;
+  if (a < 0 && p.y == p.out && !z_out) return;
+  const float sc = a >= 0 && p.scale ? p.scale[a] : 1.f;
+  const int steps = int((p.N + X::kCols - 1) / X::kCols);
+  const int end = (chunk + 1) * p.per < steps ? (chunk + 1) * p.per : steps;
+  const typename X::out_t* y = static_cast<const typename X::out_t*>(p.y);
+  const typename X::template Rows<1> rows(y ? y + t.row0 * p.N : nullptr,
+                                          static_cast<typename X::out_t*>(p.out) + t.row0 * p.N,
+                                          p.b + int64_t(a < 0 ? 0 : a) * p.N * p.r, uint32_t(p.N), p.r, t.rows, a >= 0);
+  constexpr int kAhead = ODT == 1 && RP <= 16 ? 2 : 1;  // 128 registers a lane
+  int s = chunk * p.per + wave;
+  typename X::template Step<1> st[kAhead];  // the first steps' loads go out before z is computed
 #pragma unroll
-    for (int b = 0; b < RB; ++b) {
+  for (int i = 0; i < kAhead; ++i) rows.load(s + i * kFusedWaves, st[i]);
+  f32x4 acc[1][RT];
+  zero_sums(acc);
+  if (a >= 0) {
+    constexpr int U = RT == 1 ? 4 : (RT == 2 ? 2 : 1);
+    shrink_sums<1, RT, U>(p.x + t.row0 * p.K, p.a + int64_t(a) * p.r * p.K, uint32_t(p.K), p.r, t.rows, 0,
+                          int((p.K + 32 * U - 1) / (32 * U)), kFusedWaves, acc);
+  }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[b][j] = 0.f;
-      if (base && in && 16 * b + c < t.rows) load_vec<8>(base + (t.row0 + 16 * b + c) * p.C + col, y[b]);
-    }
-    if (a >= 0) {
-      bf16x8 wf[2][kFrags];
+  for (int k = 0; k < RT; ++k) part[wave][k][lane] = acc[0][k];
+  __syncthreads();
+  if (wave < RT) {
+    f32x4 v = part[0][wave][lane];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        int64_t n = 32 * s + 8 * (c >> 2) + 4 * h + (c & 3);
-        n = n < p.C ? n : p.C - 1;                    // columns past C are not stored
+    for (int w = 1; w < kFusedWaves; ++w) v += part[w][wave][lane];
+    const int row = lane & 15, rank = 16 * wave + 4 * (lane >> 4);
+    if (rank >= p.r) v = f32x4{0.f, 0.f, 0.f, 0.f};  // repeated ranks
+    if (z_out && row < t.rows && rank < p.r) *reinterpret_cast<f32x4*>(p.z + (t.row0 + row) * p.r + rank) = v;
+    if (rank < RP) X::put(zs + row * X::kStride, rank, v * sc);
+  }
+  __syncthreads();
+  if (a < 0 && p.y == p.out) return;
+  bf16x8 zf[1][X::kSteps];
+  X::template fragments<1>(zs, zf);
+  while (s < end) {
 #pragma unroll
-        for (int f = 0; f < kFrags; ++f) {
-          const int rank = (32 * f + 8 * q) % RP;     // ranks past r meet zeros of z: no garbage there
-          wf[h][f] = rank < p.r ? load8(p.w + (int64_t(a) * p.C + n) * p.r + rank) : bf16x8{};
-        }
-      }
+    for (int i = 0; i < kAhead; ++i)
+      if (s + i * kFusedWaves < end) rows.finish(s + i * kFusedWaves, st[i], zf);
+    s += kAhead * kFusedWaves;
+    if (s >= end) break;
 #pragma unroll
-      for (int b = 0; b < RB; ++b)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          f32x4 d = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int k = 0; k < kSteps; ++k)
-            d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf[h][k % kFrags], zf[b][k], d, 0, 0, 0);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) y[b][4 * h + j] += d[j];
-        }
-    }
-#pragma unroll
-    for (int b = 0; b < RB; ++b)
-      if (in && 16 * b + c < t.rows) store_vec<8>(out + (t.row0 + 16 * b + c) * p.C + col, y[b]);
+    for (int i = 0; i < kAhead; ++i) rows.load(s + i * kFusedWaves, st[i]);
   }
 }
 
@@ -324,8 +557,9 @@ struct WgradArgs {
   const int32_t* ids;
   float* grad;            // [n, r, C], or [n, C, r] (by_column)
   float* parts;           // [tiles, r, C] (or [tiles, C, r])
-  int64_t S, C, parts_cap;  // parts there is room for (offsets that are not ascending ask for more)
-  int G, n, r, bm_log2, chunks, by_column;
+  int64_t C, parts_cap;   // parts there is room for (offsets that are not ascending ask for more)
+  int S, G, n, r, bm_log2, by_column;
+  uint32_t chunks;
 };
 
 constexpr int kWgradCols = 128 * kWaves;
@@ -338,10 +572,10 @@ template <int RT>
 __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradArgs p) {
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
   const int c = lane & 15, q = lane >> 4;
-  const int chunk = int(blockIdx.x) % p.chunks;
+  const uint32_t tile = blockIdx.x / p.chunks;
+  const int chunk = int(blockIdx.x - tile * p.chunks);
   const int rank0 = 16 * RT * int(blockIdx.y);
-  const bool single = p.ids == nullptr;
-  const RowTile t = find_tile(p.offsets, p.G, p.S, p.bm_log2, int64_t(blockIdx.x) / p.chunks, single);
+  const RowTile t = find_tile(p.offsets, p.G, p.S, p.bm_log2, tile, p.ids == nullptr);
   if (t.rows == 0) return;
   const int a = adapter_of(p.ids, t.group, p.n);
   if (a < 0) return;
@@ -396,7 +630,7 @@ __global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradArgs p) {
   }
   if (!in || t.kept >= p.parts_cap) return;
   const float sc = p.scale ? p.scale[a] : 1.f;
-  float* dst = t.kept < 0 ? p.grad + int64_t(a) * p.r * p.C : p.parts + t.kept * p.r * p.C;
+  float* dst = t.kept < 0 ? p.grad + int64_t(a) * p.r * p.C : p.parts + int64_t(t.kept) * p.r * p.C;
 #pragma unroll
   for (int k = 0; k < RT; ++k) {
     const int i = rank0 + 16 * k + 4 * q;
@@ -422,50 +656,41 @@ struct ReduceArgs {
   const int32_t* offsets;
   const int32_t* ids;
   float* grad;            // [n, len]
-  int64_t S, len, parts_cap;
-  int G, n, bm_log2, chunks;
+  int64_t len, parts_cap;
+  int S, G, n, bm_log2;
+  uint32_t chunks;
 };
 
 // grad[a] = the sum of the parts of a's groups in order (0 without rows); a group of one tile
 // under ids == NULL has written its adapter's gradient itself.
 __global__ void __launch_bounds__(kThreads) wgrad_reduce_kernel(ReduceArgs p) {
   const int lane = threadIdx.x & (kWave - 1);
-  const int a = int(int64_t(blockIdx.x) / p.chunks);
-  const int64_t e = (int64_t(int(blockIdx.x) % p.chunks) * kThreads + threadIdx.x) * 4;
+  const int a = int(blockIdx.x / p.chunks);
+  const int64_t e = (int64_t(blockIdx.x - a * p.chunks) * kThreads + threadIdx.x) * 4;
   const bool single = p.ids == nullptr;
   f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
-  int64_t kbase = 0;
+  int kbase = 0;
   for (int g0 = 0; g0 < p.G; g0 += kWave) {
-    const int g = g0 + lane;
-    int64_t lo = 0, hi = 0;
-    int id = -1;
-    if (g < p.G) {
-      lo = p.offsets[g];
-      hi = p.offsets[g + 1];
-      lo = lo < 0 ? 0 : (lo > p.S ? p.S : lo);
-      hi = hi < lo ? lo : (hi > p.S ? p.S : hi);
-      id = adapter_of(p.ids, g, p.n);
+    int lo = 0, hi = 0, id = -1;
+    if (g0 + lane < p.G) {
+      group_rows(p.offsets, g0 + lane, p.S, &lo, &hi);
+      id = adapter_of(p.ids, g0 + lane, p.n);
     }
-    const int n = int((hi - lo + (int64_t(1) << p.bm_log2) - 1) >> p.bm_log2);
+    const int n = int((int64_t(hi) - lo + (1 << p.bm_log2) - 1) >> p.bm_log2);
     const int k = single && n == 1 ? 0 : n;
-    int ki = k;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) {
-      const int b = __shfl_up(ki, d, kWave);
-      if (lane >= d) ki += b;
-    }
-    if (single && a >= g0 && a < g0 + kWave && __shfl(n, a - g0, kWave) == 1) return;
+    const int ki = wave_scan(k);
+    if (single && a >= g0 && a < g0 + kWave && __builtin_amdgcn_readlane(n, a - g0) == 1) return;
     uint64_t mine = __ballot(id == a && k > 0);
     while (mine) {
       const int l = __ffsll((unsigned long long)mine) - 1;
       mine &= mine - 1;
-      const int cnt = __shfl(k, l, kWave);
-      const int64_t first = kbase + __shfl(ki - k, l, kWave);
+      const int cnt = __builtin_amdgcn_readlane(k, l);
+      const int64_t first = kbase + __builtin_amdgcn_readlane(ki - k, l);
       if (e < p.len)
         for (int i = 0; i < cnt && first + i < p.parts_cap; ++i)
           sum += *reinterpret_cast<const f32x4*>(p.parts + (first + i) * p.len + e);
     }
-    kbase += __shfl(ki, kWave - 1, kWave);
+    kbase += __builtin_amdgcn_readlane(ki, kWave - 1);
   }
   if (e < p.len) *reinterpret_cast<f32x4*>(p.grad + int64_t(a) * p.len + e) = sum;
 }
@@ -505,10 +730,10 @@ int log2_up(int64_t v) {
 // 32 at ranks over 64, whose parts fill the registers.
 int row_tile_log2(int64_t S, int64_t G, int r) { return S <= 16 * G ? 4 : (r > 64 ? 5 : 6); }
 
-// Pieces the columns of a shrink are cut into: enough workgroups for two on every CU, no piece
-// under 512 columns (four 32-column steps a wave).
+// Pieces the columns of a shrink are cut into: enough workgroups for four on every CU, no piece
+// under 512 columns (a unit of 128 for each wave).
 int shrink_pieces(int64_t tiles, int64_t C) {
-  const int64_t want = div_up(512, tiles > 0 ? tiles : 1), most = C / 512;
+  const int64_t want = div_up(1024, tiles > 0 ? tiles : 1), most = C / 512;
   const int64_t k = want < most ? want : most;
   return int(k < 1 ? 1 : (k > 16 ? 16 : k));
 }
@@ -529,16 +754,23 @@ int64_t parts_bound(int64_t S, int64_t G, int bm_log2, bool ids) {
 }
 
 template <int RB>
-void shrink_rb(const ShrinkArgs& a, unsigned grid, hipStream_t s) {
-  if (a.r <= 16) hipLaunchKernelGGL((shrink_kernel<RB, 1>), dim3(grid), dim3(kThreads), 0, s, a);
-  else if (a.r <= 32) hipLaunchKernelGGL((shrink_kernel<RB, 2>), dim3(grid), dim3(kThreads), 0, s, a);
-  else if (a.r <= 64) hipLaunchKernelGGL((shrink_kernel<RB, 4>), dim3(grid), dim3(kThreads), 0, s, a);
-  else if constexpr (RB <= 2) hipLaunchKernelGGL((shrink_kernel<RB, 8>), dim3(grid), dim3(kThreads), 0, s, a);
+void shrink_rb(const ShrinkArgs& a, dim3 grid, hipStream_t s) {
+  if (a.r <= 16) hipLaunchKernelGGL((shrink_kernel<RB, 1>), grid, dim3(kThreads), 0, s, a);
+  else if (a.r <= 32) hipLaunchKernelGGL((shrink_kernel<RB, 2>), grid, dim3(kThreads), 0, s, a);
+  else if (a.r <= 64) hipLaunchKernelGGL((shrink_kernel<RB, 4>), grid, dim3(kThreads), 0, s, a);
+  else if constexpr (RB <= 2) hipLaunchKernelGGL((shrink_kernel<RB, 8>), grid, dim3(kThreads), 0, s, a);
 }
 
-hipError_t shrink(const ShrinkArgs& a, int64_t tiles, hipStream_t s) {
-  const unsigned grid = unsigned(tiles * a.ksplit);
-  if (grid == 0) return hipSuccess;
+hipError_t shrink(const LoraGroups& q, const uint16_t* m, const uint16_t* w, const float* scale, int64_t C, float* z,
+                  int pieces, hipStream_t s) {
+  const int bm = row_tile_log2(q.S, q.G, q.r);
+  ShrinkArgs a{m, w, scale, q.offsets, q.ids, z, C, int(q.S), int(q.G), int(q.n), q.r, bm, uint32_t(pieces), 0};
+  // the unit of the variant that shrink_rb picks
+  const int rt = q.r <= 16 ? 1 : (q.r <= 32 ? 2 : (q.r <= 64 ? 4 : 8));
+  const int unit = 32 * shrink_steps(1 << (bm - 4), rt);
+  a.per = int(div_up(div_up(C, unit), pieces));
+  const dim3 grid(unsigned(tiles_bound(q.S, q.G, bm) * pieces));
+  if (grid.x == 0) return hipSuccess;
   if (a.bm_log2 == 4) shrink_rb<1>(a, grid, s);
   else if (a.bm_log2 == 5) shrink_rb<2>(a, grid, s);
   else shrink_rb<4>(a, grid, s);
@@ -546,29 +778,35 @@ hipError_t shrink(const ShrinkArgs& a, int64_t tiles, hipStream_t s) {
 }
 
 template <int RB, int ODT>
-void expand_rb(const ExpandArgs& a, unsigned grid, hipStream_t s) {
-  if (a.r <= 8) hipLaunchKernelGGL((expand_kernel<RB, 8, ODT>), dim3(grid), dim3(kThreads), 0, s, a);
-  else if (a.r <= 16) hipLaunchKernelGGL((expand_kernel<RB, 16, ODT>), dim3(grid), dim3(kThreads), 0, s, a);
-  else if (a.r <= 32) hipLaunchKernelGGL((expand_kernel<RB, 32, ODT>), dim3(grid), dim3(kThreads), 0, s, a);
-  else if (a.r <= 64) hipLaunchKernelGGL((expand_kernel<RB, 64, ODT>), dim3(grid), dim3(kThreads), 0, s, a);
-  else if constexpr (RB <= 2) hipLaunchKernelGGL((expand_kernel<RB, 128, ODT>), dim3(grid), dim3(kThreads), 0, s, a);
+void expand_rb(const ExpandArgs& a, dim3 grid, hipStream_t s) {
+  if (a.r <= 8) hipLaunchKernelGGL((expand_kernel<RB, 8, ODT>), grid, dim3(kThreads), 0, s, a);
+  else if (a.r <= 16) hipLaunchKernelGGL((expand_kernel<RB, 16, ODT>), grid, dim3(kThreads), 0, s, a);
+  else if (a.r <= 32) hipLaunchKernelGGL((expand_kernel<RB, 32, ODT>), grid, dim3(kThreads), 0, s, a);
+  else if (a.r <= 64) hipLaunchKernelGGL((expand_kernel<RB, 64, ODT>), grid, dim3(kThreads), 0, s, a);
+  else if constexpr (RB <= 2) hipLaunchKernelGGL((expand_kernel<RB, 128, ODT>), grid, dim3(kThreads), 0, s, a);
 }
 
 template <int ODT>
-void expand_dt(const ExpandArgs& a, unsigned grid, hipStream_t s) {
+void expand_dt(const ExpandArgs& a, dim3 grid, hipStream_t s) {
   if (a.bm_log2 == 4) expand_rb<1, ODT>(a, grid, s);
   else if (a.bm_log2 == 5) expand_rb<2, ODT>(a, grid, s);
   else expand_rb<4, ODT>(a, grid, s);
 }
 
-int expand_chunks(int64_t tiles, int64_t C) {
-  const int64_t most = div_up(div_up(C, 32), kWaves), want = div_up(1024, tiles > 0 ? tiles : 1);
+int expand_chunks(int64_t tiles, int64_t C, int odt, int waves, int groups_wanted) {
+  const int64_t most = div_up(div_up(C, odt == 0 ? 64 : 32), waves), want = div_up(groups_wanted, tiles > 0 ? tiles : 1);
   return int(want < most ? want : most);
 }
 
-hipError_t expand(const ExpandArgs& a, int odt, int64_t tiles, hipStream_t s) {
-  const unsigned grid = unsigned(tiles * a.chunks);
-  if (grid == 0) return hipSuccess;
+hipError_t expand(const LoraGroups& q, const float* z, int pieces, const uint16_t* w, const float* scale, int64_t C,
+                  const void* base, void* out, int odt, float* z_out, hipStream_t s) {
+  const int bm = row_tile_log2(q.S, q.G, q.r);
+  const int64_t tiles = tiles_bound(q.S, q.G, bm);
+  const int chunks = expand_chunks(tiles, C, odt, kWaves, 1024);
+  ExpandArgs a{z, w, scale, q.offsets, q.ids, base, out, z_out, C, int(q.S), int(q.G), int(q.n), q.r, bm, pieces,
+               uint32_t(chunks), int(div_up(div_up(C, odt == 0 ? 64 : 32), chunks))};
+  const dim3 grid(unsigned(tiles * chunks));
+  if (grid.x == 0) return hipSuccess;
   if (odt == 0) expand_dt<0>(a, grid, s);
   else expand_dt<1>(a, grid, s);
   return hipGetLastError();
@@ -591,13 +829,13 @@ hipError_t wgrad(const LoraGroups& q, const float* v, const uint16_t* m, const f
   a.ids = q.ids;
   a.grad = grad;
   a.parts = parts;
-  a.S = q.S;
+  a.S = int(q.S);
   a.C = C;
   a.G = int(q.G);
   a.n = int(q.n);
   a.r = q.r;
   a.bm_log2 = wgrad_tile_log2(q.S, C);
-  a.chunks = int(div_up(C, kWgradCols));
+  a.chunks = uint32_t(div_up(C, kWgradCols));
   a.by_column = by_column ? 1 : 0;
   a.parts_cap = parts_bound(q.S, q.G, a.bm_log2, q.ids != nullptr);
   const unsigned grid = unsigned(tiles_bound(q.S, q.G, a.bm_log2) * a.chunks);
@@ -611,13 +849,13 @@ hipError_t wgrad(const LoraGroups& q, const float* v, const uint16_t* m, const f
   d.offsets = q.offsets;
   d.ids = q.ids;
   d.grad = grad;
-  d.S = q.S;
+  d.S = int(q.S);
   d.len = q.r * C;
   d.parts_cap = a.parts_cap;
   d.G = a.G;
   d.n = a.n;
   d.bm_log2 = a.bm_log2;
-  d.chunks = int(div_up(d.len, 4 * kThreads));
+  d.chunks = uint32_t(div_up(d.len, 4 * kThreads));
   hipLaunchKernelGGL(wgrad_reduce_kernel, dim3(unsigned(q.n * d.chunks)), dim3(kThreads), 0, s, d);
   return hipGetLastError();
 }
@@ -656,8 +894,15 @@ BackwardLayout backward_layout(const LoraBackwardLaunch& L) {
 
 }  // namespace
 
+// Whether the forward call runs as one launch: tiles of at most 16 rows, and an A that a CU reads
+// from the L2 cache in a few microseconds, about what the second launch would cost.
+bool lora_fused(const LoraGroups& q) {
+  return row_tile_log2(q.S, q.G, q.r) == 4 && q.r <= 64 && int64_t(q.r) * q.K <= (1 << 17);
+}
+
 size_t lora_ws_bytes(const LoraLaunch& L) {
   const LoraGroups& q = L.q;
+  if (lora_fused(q)) return 0;
   const int64_t tiles = tiles_bound(q.S, q.G, row_tile_log2(q.S, q.G, q.r));
   return align256(size_t(shrink_pieces(tiles, q.K)) * q.S * q.r * 4);
 }
@@ -675,25 +920,38 @@ int64_t lora_blocks(const LoraGroups& q) {
   return most;
 }
 
+template <int ODT>
+void fused_dt(const FusedArgs& a, dim3 grid, hipStream_t s) {
+  const dim3 threads(kFusedWaves * kWave);
+  if (a.r <= 8) hipLaunchKernelGGL((fused_kernel<8, ODT>), grid, threads, 0, s, a);
+  else if (a.r <= 16) hipLaunchKernelGGL((fused_kernel<16, ODT>), grid, threads, 0, s, a);
+  else if (a.r <= 32) hipLaunchKernelGGL((fused_kernel<32, ODT>), grid, threads, 0, s, a);
+  else hipLaunchKernelGGL((fused_kernel<64, ODT>), grid, threads, 0, s, a);
+}
+
 hipError_t launch_lora(const LoraLaunch& L, hipStream_t stream) {
   const LoraGroups& q = L.q;
-  const int bm = row_tile_log2(q.S, q.G, q.r);
-  const int64_t tiles = tiles_bound(q.S, q.G, bm);
+  if (lora_fused(q)) {
+    const int64_t tiles = tiles_bound(q.S, q.G, 4);
+    const int chunks = expand_chunks(tiles, q.N, L.out_dtype, kFusedWaves, 256);
+    FusedArgs a{L.x, L.a, L.b, L.scale, q.offsets, q.ids, L.y, L.out, L.z, q.K, q.N, int(q.S), int(q.G), int(q.n),
+                q.r, uint32_t(chunks), int(div_up(div_up(q.N, L.out_dtype == 0 ? 64 : 32), chunks))};
+    const dim3 grid(unsigned(tiles * chunks));
+    if (L.out_dtype == 0) fused_dt<0>(a, grid, stream);
+    else fused_dt<1>(a, grid, stream);
+    return hipGetLastError();
+  }
+  const int64_t tiles = tiles_bound(q.S, q.G, row_tile_log2(q.S, q.G, q.r));
   const int pieces = shrink_pieces(tiles, q.K);
   float* z = pieces == 1 && L.z ? L.z : reinterpret_cast<float*>(L.ws);
-  ShrinkArgs a{L.x, L.a, nullptr, q.offsets, q.ids, z, q.S, q.K, int(q.G), int(q.n), q.r, bm, pieces};
-  if (hipError_t e = shrink(a, tiles, stream); e != hipSuccess) return e;
-  ExpandArgs b{z, L.b, L.scale, q.offsets, q.ids, L.y, L.out, pieces > 1 ? L.z : nullptr, q.S, q.N,
-               int(q.G), int(q.n), q.r, bm, pieces, expand_chunks(tiles, q.N)};
-  return expand(b, L.out_dtype, tiles, stream);
+  if (hipError_t e = shrink(q, L.x, L.a, nullptr, q.K, z, pieces, stream); e != hipSuccess) return e;
+  return expand(q, z, pieces, L.b, L.scale, q.N, L.y, L.out, L.out_dtype, pieces > 1 ? L.z : nullptr, stream);
 }
 
 hipError_t launch_lora_backward(const LoraBackwardLaunch& L, hipStream_t stream) {
   const LoraGroups& q = L.q;
   const BackwardLayout w = backward_layout(L);
   char* ws = reinterpret_cast<char*>(L.ws);
-  const int bm = row_tile_log2(q.S, q.G, q.r);
-  const int64_t tiles = tiles_bound(q.S, q.G, bm);
   float* u = reinterpret_cast<float*>(ws + w.u);
   float* parts = reinterpret_cast<float*>(ws + w.parts);
   hipError_t e = hipSuccess;
@@ -701,14 +959,12 @@ hipError_t launch_lora_backward(const LoraBackwardLaunch& L, hipStream_t stream)
     uint16_t* bt = reinterpret_cast<uint16_t*>(ws + w.bt);
     if ((e = transpose(L.b, q.n, q.N, q.r, bt, stream)) != hipSuccess) return e;
     float* to = w.pieces > 1 ? reinterpret_cast<float*>(ws + w.upart) : u;
-    ShrinkArgs a{L.g, bt, L.scale, q.offsets, q.ids, to, q.S, q.N, int(q.G), int(q.n), q.r, bm, w.pieces};
-    if ((e = shrink(a, tiles, stream)) != hipSuccess) return e;
+    if ((e = shrink(q, L.g, bt, L.scale, q.N, to, w.pieces, stream)) != hipSuccess) return e;
     if (L.gx) {
       uint16_t* at = reinterpret_cast<uint16_t*>(ws + w.at);
       if ((e = transpose(L.a, q.n, q.r, q.K, at, stream)) != hipSuccess) return e;
-      ExpandArgs b{to, at, nullptr, q.offsets, q.ids, L.gx_base, L.gx, w.pieces > 1 ? u : nullptr, q.S, q.K,
-                   int(q.G), int(q.n), q.r, bm, w.pieces, expand_chunks(tiles, q.K)};
-      if ((e = expand(b, L.gx_dtype, tiles, stream)) != hipSuccess) return e;
+      e = expand(q, to, w.pieces, at, nullptr, q.K, L.gx_base, L.gx, L.gx_dtype, w.pieces > 1 ? u : nullptr, stream);
+      if (e != hipSuccess) return e;
     }
   }
   if (L.ga && (e = wgrad(q, u, L.x, nullptr, q.K, false, L.ga, parts, stream)) != hipSuccess) return e;

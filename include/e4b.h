@@ -379,7 +379,7 @@ int e4b_dgrad_workspace_bytes(const e4b_dgrad_args* a, size_t* bytes);
 int e4b_grouped_dgrad(const e4b_dgrad_args* a, void* stream);
 
 /* Arguments of e4b_grouped_lora.  Sizes: K % 8 == 0, N % 8 == 0, r % 8 == 0, 8 <= r <= 128;
- * S, K, N, groups and adapters below 2^31.  Smaller or mixed ranks: pad A and B with zeros. */
+ * K, N <= 2^23; S, groups and adapters below 2^31.  Smaller or mixed ranks: pad A and B with zeros. */
 typedef struct e4b_lora_args {
   int32_t r;              /* rank */
   int32_t out_dtype;      /* e4b_dtype of y and out */
@@ -397,7 +397,8 @@ typedef struct e4b_lora_args {
   const void* y;          /* [S, N] of out_dtype: what the shared projection gave, or NULL: zeros */
   void* out;              /* [S, N] of out_dtype out; may be y */
   float* z;               /* [S, r] float32 out, or NULL: x A^T, kept for the backward call */
-  void* ws;               /* device workspace of at least e4b_lora_workspace_bytes() */
+  void* ws;               /* device workspace of at least e4b_lora_workspace_bytes() (0: may be
+                           * NULL) */
   size_t ws_bytes;
   int64_t reserved;       /* must be 0 */
 } e4b_lora_args;
