@@ -6,13 +6,13 @@
 // with A_a [r, K], B_a [N, r] bf16, r = 8 .. 128.  About 2r / b flop for each byte moved (b the
 // bytes of an element read and written): bound by memory at every rank taken here, so the kernels
 // are three streaming passes with the matrix unit beside them:
-//   shrink   [rows, C] x [r, C]^T -> [rows, r]     (z from x and A; u from g and B^T)
+//   shrink   [rows, C] x [r, C]^T -> [rows, r]     (z from x and A)
 //   expand   [rows, r] x [C, r]^T added to [rows, C]   (out from z and B; gx from u and A^T)
-//   wgrad    [rows, r]^T x [rows, C] -> [r, C]     (gA from u and x; gB from z and g)
+//   grad     [rows, r]^T x [rows, C] -> [r, C]     (gA from u and x; gB from z and g, with u in the same pass)
 // Products of bf16 values go through the bf16 matrix instruction exactly, with float32 sums.  z
 // and u are float32 all the way: in expand each is cut into three bf16 parts (8 + 8 + 8 bits of
-// its 24-bit significand: no rounding) that stand behind one another in the contraction, in wgrad
-// they enter the float32 matrix instruction.
+// its 24-bit significand: no rounding) that stand behind one another in the contraction, and so in
+// grad.
 #include "e4b_internal.h"
 #include "e4b_rows.h"
 
@@ -29,7 +29,6 @@ struct RowTile {
   int group;
   int64_t row0;
   int rows;        // 1 .. bm; 0: no such tile
-  int kept;        // index among the tiles of groups with more than one (find_tile's `single` false)
 };
 
 // Inclusive sum over the wave's lanes in six steps of the vector unit: shifts by 1, 2, 4 and 8 in
@@ -54,33 +53,25 @@ __device__ __forceinline__ void group_rows(const int32_t* __restrict__ offsets, 
 // Tile `tile` of the list that cuts every group into pieces of 1 << bm_log2 rows, found by each
 // wave from the offsets, 64 groups a step.
 __device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offsets, int G, int S, int bm_log2,
-                                             uint32_t tile, bool single) {
+                                             uint32_t tile) {
   const int lane = threadIdx.x & (kWave - 1);
-  int base = 0, kbase = 0;
+  int base = 0;
   for (int g0 = 0; g0 < G; g0 += kWave) {
     int lo = 0, hi = 0;
     if (g0 + lane < G) group_rows(offsets, g0 + lane, S, &lo, &hi);
     const int n = int((int64_t(hi) - lo + (1 << bm_log2) - 1) >> bm_log2);
-    const int k = single && n == 1 ? 0 : n;
-    const int ni = wave_scan(n), ki = single ? wave_scan(k) : ni;
+    const int ni = wave_scan(n);
     const int total = __builtin_amdgcn_readlane(ni, kWave - 1);
     if (int(tile) - base < total) {
       const int l = __ffsll((unsigned long long)__ballot(int(tile) - base < ni)) - 1;
-      const int nl = __builtin_amdgcn_readlane(n, l);
-      const int at = int(tile) - base - (__builtin_amdgcn_readlane(ni, l) - nl);
+      const int at = int(tile) - base - (__builtin_amdgcn_readlane(ni, l) - __builtin_amdgcn_readlane(n, l));
       const int row0 = __builtin_amdgcn_readlane(lo, l) + (at << bm_log2);
       const int left = __builtin_amdgcn_readlane(hi, l) - row0;
-      RowTile t;
-      t.group = g0 + l;
-      t.row0 = row0;
-      t.rows = left < (1 << bm_log2) ? left : (1 << bm_log2);
-      t.kept = single && nl == 1 ? -1 : kbase + __builtin_amdgcn_readlane(ki - k, l) + at;
-      return t;
+      return RowTile{g0 + l, row0, left < (1 << bm_log2) ? left : (1 << bm_log2)};
     }
     base += total;
-    kbase += __builtin_amdgcn_readlane(ki, kWave - 1);
   }
-  return RowTile{0, 0, 0, 0};
+  return RowTile{0, 0, 0};
 }
 
 __device__ __forceinline__ int adapter_of(const int32_t* __restrict__ ids, int group, int n) {
@@ -100,7 +91,7 @@ __device__ __forceinline__ u32x4 buf_load(__amdgpu_buffer_rsrc_t r, uint32_t lan
 __device__ __forceinline__ bf16x8 buf_load8(__amdgpu_buffer_rsrc_t r, uint32_t lane_off, uint32_t off) {
   return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(r, lane_off, off, 0));
 }
-constexpr uint32_t kNowhere = 0xFFFFFFF0u;  // past the end of every buffer
+constexpr uint32_t kNowhere = 0x80000000u;  // past the end of every buffer (of 2^31 bytes at most)
 
 // Sums of one wave over its units of the columns: acc[b][k] gets rows 16b .. of the tile by ranks
 // 16k .. .  A unit is U matrix steps, 64 U contiguous bytes of each row; a wave takes the units
@@ -209,7 +200,7 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(ShrinkArgs p) {
   const int c = lane & 15, q = lane >> 4;
   const uint32_t tile = blockIdx.x / p.ksplit;
   const int ks = int(blockIdx.x - tile * p.ksplit);
-  const RowTile t = find_tile(p.offsets, p.G, p.S, p.bm_log2, tile, false);
+  const RowTile t = find_tile(p.offsets, p.G, p.S, p.bm_log2, tile);
   if (t.rows == 0) return;
   const int a = adapter_of(p.ids, t.group, p.n);
   f32x4 acc[RB][RT];
@@ -418,7 +409,7 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs p) {
   __shared__ __attribute__((aligned(16))) uint16_t zs[16 * RB * X::kStride];
   const uint32_t tile = blockIdx.x / p.chunks;
   const int chunk = int(blockIdx.x - tile * p.chunks);
-  const RowTile t = find_tile(p.offsets, p.G, p.S, p.bm_log2, tile, false);
+  const RowTile t = find_tile(p.offsets, p.G, p.S, p.bm_log2, tile);
   if (t.rows == 0) return;
   const int a = adapter_of(p.ids, t.group, p.n);
   const bool z_out = p.z_out && chunk == 0;
@@ -498,7 +489,7 @@ __global__ void __launch_bounds__(kFusedWaves * kWave) fused_kernel(FusedArgs p)
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t tile = blockIdx.x / p.chunks;
   const int chunk = int(blockIdx.x - tile * p.chunks);
-  const RowTile t = find_tile(p.offsets, p.G, p.S, 4, tile, false);
+  const RowTile t = find_tile(p.offsets, p.G, p.S, 4, tile);
   if (t.rows == 0) return;
   const int a = adapter_of(p.ids, t.group, p.n);
   const bool z_out = p.z && chunk == 0;
@@ -549,121 +540,281 @@ __global__ void __launch_bounds__(kFusedWaves * kWave) fused_kernel(FusedArgs p)
   }
 }
 
-struct WgradArgs {
-  const float* v;         // [S, r]
-  const uint16_t* m;      // [S, C]
-  const float* scale;     // nullable: 1
+// A tile of the gradient pass: group g's rows cut evenly into ceil(rows / most) pieces of a multiple
+// of 64 rows (the last ones may hold fewer, or none).
+struct GradTile {
+  int group, row0, rows;
+  int kept;        // index among the tiles that write parts; -1: the group's only tile
+  bool valid;
+};
+
+__device__ __forceinline__ int grad_tiles(int rows, int most) {
+  return int((uint32_t(rows) + uint32_t(most) - 1u) / uint32_t(most));
+}
+
+// As find_tile.  `single`: a group of one tile is not counted among the kept ones.
+__device__ __forceinline__ GradTile find_grad_tile(const int32_t* __restrict__ offsets, int G, int S, int most,
+                                                   uint32_t tile, bool single) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int base = 0, kbase = 0;
+  for (int g0 = 0; g0 < G; g0 += kWave) {
+    int lo = 0, hi = 0;
+    if (g0 + lane < G) group_rows(offsets, g0 + lane, S, &lo, &hi);
+    const int n = grad_tiles(hi - lo, most);
+    const int k = single && n == 1 ? 0 : n;
+    const int ni = wave_scan(n), ki = wave_scan(k);
+    const int total = __builtin_amdgcn_readlane(ni, kWave - 1);
+    if (int(tile) - base < total) {
+      const int l = __ffsll((unsigned long long)__ballot(int(tile) - base < ni)) - 1;
+      const int nl = __builtin_amdgcn_readlane(n, l), lol = __builtin_amdgcn_readlane(lo, l);
+      const int rows = __builtin_amdgcn_readlane(hi, l) - lol;
+      const int at = int(tile) - base - (__builtin_amdgcn_readlane(ni, l) - nl);
+      const int per = (grad_tiles(rows, nl) + 63) & ~63;
+      const int64_t first = int64_t(at) * per;
+      GradTile t;
+      t.group = g0 + l;
+      t.rows = int(rows - first < 0 ? 0 : (rows - first < per ? rows - first : per));
+      t.row0 = lol + (t.rows > 0 ? int(first) : 0);
+      t.kept = single && nl == 1 ? -1 : kbase + __builtin_amdgcn_readlane(ki - k, l) + at;
+      t.valid = true;
+      return t;
+    }
+    base += total;
+    kbase += __builtin_amdgcn_readlane(ki, kWave - 1);
+  }
+  return GradTile{0, 0, 0, 0, false};
+}
+
+struct GradArgs {
+  const float* v;         // [S, r]: z or u (read for grad)
+  const uint16_t* m;      // [S, C]: g or x
+  const uint16_t* w;      // [n, C, r]: B, for u
+  const float* scale;     // nullable: 1; of grad and of u
   const int32_t* offsets;
   const int32_t* ids;
-  float* grad;            // [n, r, C], or [n, C, r] (by_column)
-  float* parts;           // [tiles, r, C] (or [tiles, C, r])
-  int64_t C, parts_cap;   // parts there is room for (offsets that are not ascending ask for more)
-  int S, G, n, r, bm_log2, by_column;
+  float* grad;            // nullable [n, r, C], or [n, C, r] (BYCOL)
+  float* parts;           // [parts_cap][r, C] (or [C, r])
+  float* upart;           // nullable [chunks, S, r]: m B, summed over a chunk's columns
+  int64_t parts_cap;      // parts there is room for (offsets that are not ascending ask for more)
+  uint32_t C;
+  int S, G, n, r, most;
   uint32_t chunks;
 };
 
-constexpr int kWgradCols = 128 * kWaves;
+constexpr int kGradRows = 64, kGradCols = 256;  // a block in LDS: 64 rows of 512 bytes
 
-// A workgroup: the rows of one tile and 512 columns, a wave 128 of them (8 a lane, 16 bytes of a
-// row) by up to 16 * RT ranks.  Four rows feed one float32 matrix instruction for each of a lane's
-// 8 columns, no transposition: the instruction's column index is the lane, and its 8 tiles are the
-// lanes' 8 columns.
-template <int RT>
-__global__ void __launch_bounds__(kThreads) wgrad_kernel(WgradArgs p) {
-  const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
+// LDS byte of the 16-byte piece `piece` of row `row` of a block.  Rows are 512 bytes; the 32-byte
+// units of a row and the halves of a unit are exchanged by the row so that the 16-byte reads of 16
+// rows and the transposing reads (4 rows by 32 bytes for each 16 lanes) spread over all 64 banks.
+__device__ __forceinline__ uint32_t block_at(int row, int piece) {
+  const uint32_t f = (row & 3) | ((row >> 1) & 4), h = (row >> 2) & 1;
+  return 512u * row + ((uint32_t(piece >> 1) ^ f) * 32u) + ((uint32_t(piece & 1) ^ h) * 16u);
+}
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+// Transposing LDS read: the 16 lanes of a group give the addresses of 4 rows by 16 columns (lane i:
+// row i / 4, columns 4 (i % 4) .. + 3); lane i gets column i of the 4 rows.
+__device__ __forceinline__ s16x4 lds_read_tr(const uint8_t* at) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)at);
+#else
+  return s16x4{};
+#endif
+}
+
+// One pass over m for both products it enters: grad = v^T m over the tile's rows, and (with UP)
+// u = m B over a chunk's columns.  A workgroup takes the rows of one tile and 256 * NSUB columns, in
+// blocks of 64 rows by 256 columns that come in whole lines through registers (the next block's
+// loads in flight) into LDS.  grad: a wave has 64 of the block's columns; the contraction runs over
+// the rows, so m is read transposed, and v stands in LDS transposed in its three parts.  u: a wave
+// has 16 of the block's rows and all its columns; B stands in LDS transposed.
+// Bound: HBM.  One pass instead of two (u on its own, grad on its own) reads m once: the gradients
+// of the 8-expert gate_up adapters took 387 us in separate passes over float32 matrix instructions.
+template <int RT, int NSUB, bool UP, bool BYCOL>
+__global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
+  constexpr int kVStride = kGradRows + 8;               // v^T row in bf16
+  constexpr int kWCols = kGradCols * NSUB, kWStride = kWCols + 8;
+  constexpr uint32_t kBlock = kGradRows * kGradCols * 2;
+  constexpr uint32_t kV = 3 * 16 * RT * kVStride * 2;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kBlock + kV + (UP ? 16 * RT * kWStride * 2 : 0)];
+  uint16_t* vt = reinterpret_cast<uint16_t*>(lds + kBlock);          // [3][16 RT][kVStride]
+  uint16_t* wt = reinterpret_cast<uint16_t*>(lds + kBlock + kV);     // [16 RT][kWStride]
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, q = lane >> 4;
   const uint32_t tile = blockIdx.x / p.chunks;
   const int chunk = int(blockIdx.x - tile * p.chunks);
-  const int rank0 = 16 * RT * int(blockIdx.y);
-  const RowTile t = find_tile(p.offsets, p.G, p.S, p.bm_log2, tile, p.ids == nullptr);
-  if (t.rows == 0) return;
+  const GradTile t = find_grad_tile(p.offsets, p.G, p.S, p.most, tile, p.ids == nullptr);
+  if (!t.valid) return;
   const int a = adapter_of(p.ids, t.group, p.n);
   if (a < 0) return;
-  const int64_t col = int64_t(chunk) * kWgradCols + 128 * wave + 8 * c;
-  const bool in = col < p.C;
-  const uint16_t* mp = p.m + t.row0 * p.C + (in ? col : 0);
-  const float* vp = p.v + t.row0 * p.r;
-  f32x4 acc[RT][8];
+  const uint32_t col0 = uint32_t(chunk) * kWCols;
+  const bool grad = p.grad != nullptr;
+
+  if (UP) {  // B^T of the chunk: 8 ranks of a column a thread and turn
+    const int per = p.r >> 3;
+    for (int i = tid; i < kWCols * per; i += kThreads) {
+      const int n = i / per, k = 8 * (i - n * per);
+      u32x4 b = u32x4{0u, 0u, 0u, 0u};
+      if (col0 + n < p.C) b = *reinterpret_cast<const u32x4*>(p.w + (int64_t(a) * p.C + col0 + n) * p.r + k);
 #pragma unroll
-  for (int k = 0; k < RT; ++k)
+      for (int j = 0; j < 8; ++j) wt[(k + j) * kWStride + n] = uint16_t(j & 1 ? b[j >> 1] >> 16 : b[j >> 1] & 0xFFFFu);
+    }
+  }
+
+  f32x4 acc[NSUB][4][RT];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) acc[k][j] = f32x4{0.f, 0.f, 0.f, 0.f};
-  auto fma_rows = [&](const u32x4& mv, const float (&vv)[RT]) {
+  for (int s = 0; s < NSUB; ++s) zero_sums(acc[s]);
+
+  // The block's loads: thread i of row i / 32 takes piece i % 32 of every 8th row.  Offsets are
+  // taken from the block's first row, so they stay small however long the tile is.
+  const int prow = tid >> 5, piece = tid & 31;
+  auto load_block = [&](int row, int sub, u32x4 (&v)[8]) {
+    const uint16_t* at = p.m + (int64_t(t.row0) + row) * p.C;
+    const int left = t.rows - row;
+    const __amdgpu_buffer_rsrc_t res =
+        buffer_rsrc(at, left > 0 ? uint32_t(left < kGradRows ? left : kGradRows) * p.C * 2u : 0u);
+    const uint32_t col = col0 + kGradCols * sub + 8 * piece;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float mf = __uint_as_float(j & 1 ? mv[j >> 1] & 0xFFFF0000u : mv[j >> 1] << 16);
+    for (int j = 0; j < 8; ++j)
+      v[j] = buf_load(res, col < p.C ? (prow * p.C + col) * 2u : kNowhere, 16u * j * p.C);
+  };
+  // v of a block: two rows of one rank a thread and turn.
+  constexpr int kVTurns = kGradRows / 2 * 16 * RT / kThreads;
+  auto load_v = [&](int row, float (&v)[kVTurns][2]) {
+    const int left = t.rows - row;
+    const __amdgpu_buffer_rsrc_t res =
+        buffer_rsrc(p.v + (int64_t(t.row0) + row) * p.r, grad && left > 0 ? uint32_t(left < kGradRows ? left : kGradRows) * p.r * 4u : 0u);
 #pragma unroll
-      for (int k = 0; k < RT; ++k) acc[k][j] = __builtin_amdgcn_mfma_f32_16x16x4f32(vv[k], mf, acc[k][j], 0, 0, 0);
+    for (int j = 0; j < kVTurns; ++j) {
+      const int i = tid + j * kThreads, rank = i % (16 * RT), pair = i / (16 * RT);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        v[j][h] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+            res, rank < p.r ? uint32_t(((2 * pair + h) * p.r + rank) * 4) : kNowhere, 0, 0));
     }
   };
-  constexpr int U = RT <= 2 ? 8 : 4;
-  int row = q;
-  for (; row - q + 4 * U <= t.rows; row += 4 * U) {
-    u32x4 mv[U];
-    float vv[U][RT];
+
+  u32x4 mv[8];
+  float vv[kVTurns][2];
+  load_block(0, 0, mv);
+  load_v(0, vv);
+  f32x4 us[RT];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      mv[u] = *reinterpret_cast<const u32x4*>(mp + int64_t(row + 4 * u) * p.C);
+  for (int k = 0; k < RT; ++k) us[k] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int row = 0; row < t.rows; row += kGradRows) {
 #pragma unroll
-      for (int k = 0; k < RT; ++k) {
-        const int i = rank0 + 16 * k + c;
-        vv[u][k] = vp[int64_t(row + 4 * u) * p.r + (i < p.r ? i : 0)];
+    for (int sub = 0; sub < NSUB; ++sub) {
+      __syncthreads();  // the last block has been read
+#pragma unroll
+      for (int j = 0; j < 8; ++j) *reinterpret_cast<u32x4*>(lds + block_at(prow + 8 * j, piece)) = mv[j];
+      if (sub == 0 && grad) {
+#pragma unroll
+        for (int j = 0; j < kVTurns; ++j) {
+          const int i = tid + j * kThreads, rank = i % (16 * RT), pair = i / (16 * RT);
+          const Parts x = split3(vv[j][0]), y = split3(vv[j][1]);
+          uint32_t* at = reinterpret_cast<uint32_t*>(vt + rank * kVStride) + pair;
+          at[0] = hi2(x.hi, y.hi);
+          at[16 * RT * kVStride / 2] = hi2(x.mid, y.mid);
+          at[2 * (16 * RT * kVStride / 2)] = hi2(x.lo, y.lo);
+        }
+      }
+      __syncthreads();
+      if (sub + 1 < NSUB) {
+        load_block(row, sub + 1, mv);
+      } else {
+        load_block(row + kGradRows, 0, mv);  // past the tile: zeros, unused
+        load_v(row + kGradRows, vv);
+      }
+      if (grad) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          bf16x8 mf[4];
+#pragma unroll
+          for (int ct = 0; ct < 4; ++ct) {
+            s16x8 mt;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int r4 = 32 * ks + 8 * q + 4 * h + (c >> 2), u = 4 * wave + ct;
+              const s16x4 x = lds_read_tr(lds + block_at(r4, 2 * u + ((c >> 1) & 1)) + 8 * (c & 1));
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mt[4 * h + j] = x[j];
+            }
+            mf[ct] = __builtin_bit_cast(bf16x8, mt);
+          }
+#pragma unroll
+          for (int k = 0; k < RT; ++k)
+#pragma unroll
+            for (int h = 0; h < 3; ++h) {
+              const bf16x8 vf =
+                  *reinterpret_cast<const bf16x8*>(vt + (16 * RT * h + 16 * k + c) * kVStride + 32 * ks + 8 * q);
+#pragma unroll
+              for (int ct = 0; ct < 4; ++ct)
+                acc[sub][ct][k] = BYCOL ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, mf[ct], acc[sub][ct][k], 0, 0, 0)
+                                        : __builtin_amdgcn_mfma_f32_16x16x32_bf16(mf[ct], vf, acc[sub][ct][k], 0, 0, 0);
+            }
+        }
+      }
+      if (UP) {
+#pragma unroll
+        for (int s = 0; s < kGradCols / 32; ++s) {
+          const bf16x8 mf = *reinterpret_cast<const bf16x8*>(lds + block_at(16 * wave + c, 4 * s + q));
+#pragma unroll
+          for (int k = 0; k < RT; ++k) {
+            const bf16x8 wf = *reinterpret_cast<const bf16x8*>(wt + (16 * k + c) * kWStride + kGradCols * sub + 32 * s + 8 * q);
+            us[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, mf, us[k], 0, 0, 0);
+          }
+        }
       }
     }
-#pragma unroll
-    for (int u = 0; u < U; ++u) fma_rows(mv[u], vv[u]);
-  }
-  for (; row - q < t.rows; row += 4) {  // rows past the tile enter as zeros
-    u32x4 mv = u32x4{0, 0, 0, 0};
-    float vv[RT];
-#pragma unroll
-    for (int k = 0; k < RT; ++k) vv[k] = 0.f;
-    if (row < t.rows) {
-      mv = *reinterpret_cast<const u32x4*>(mp + int64_t(row) * p.C);
+    if (UP) {
+      const int at = row + 16 * wave + c;
 #pragma unroll
       for (int k = 0; k < RT; ++k) {
-        const int i = rank0 + 16 * k + c;
-        vv[k] = vp[int64_t(row) * p.r + (i < p.r ? i : 0)];
+        const int rank = 16 * k + 4 * q;
+        if (at < t.rows && rank < p.r)
+          *reinterpret_cast<f32x4*>(p.upart + (int64_t(chunk) * p.S + t.row0 + at) * p.r + rank) = us[k];
+        us[k] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
     }
-    fma_rows(mv, vv);
   }
-  if (!in || t.kept >= p.parts_cap) return;
+  if (!grad || t.kept >= p.parts_cap) return;
   const float sc = p.scale ? p.scale[a] : 1.f;
   float* dst = t.kept < 0 ? p.grad + int64_t(a) * p.r * p.C : p.parts + int64_t(t.kept) * p.r * p.C;
 #pragma unroll
-  for (int k = 0; k < RT; ++k) {
-    const int i = rank0 + 16 * k + 4 * q;
-    if (i >= p.r) continue;
-    if (p.by_column) {
+  for (int sub = 0; sub < NSUB; ++sub)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) *reinterpret_cast<f32x4*>(dst + (col + j) * p.r + i) = acc[k][j] * sc;
-    } else {
+    for (int ct = 0; ct < 4; ++ct)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float* d = dst + int64_t(i + e) * p.C + col;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-          *reinterpret_cast<f32x4*>(d + 4 * h) =
-              f32x4{acc[k][4 * h][e], acc[k][4 * h + 1][e], acc[k][4 * h + 2][e], acc[k][4 * h + 3][e]} * sc;
+      for (int k = 0; k < RT; ++k) {
+        const uint32_t cc = col0 + kGradCols * sub + 64 * wave + 16 * ct;
+        if (BYCOL) {
+          const int rank = 16 * k + 4 * q;
+          if (cc + c < p.C && rank < p.r)
+            *reinterpret_cast<f32x4*>(dst + int64_t(cc + c) * p.r + rank) = acc[sub][ct][k] * sc;
+        } else {
+          const int rank = 16 * k + c;
+          if (cc + 4 * q < p.C && rank < p.r)
+            *reinterpret_cast<f32x4*>(dst + int64_t(rank) * p.C + cc + 4 * q) = acc[sub][ct][k] * sc;
+        }
       }
-    }
-  }
 }
 
 struct ReduceArgs {
-  const float* parts;     // [tiles, len]
+  const float* parts;     // [parts_cap, len]
   const int32_t* offsets;
   const int32_t* ids;
   float* grad;            // [n, len]
   int64_t len, parts_cap;
-  int S, G, n, bm_log2;
+  int S, G, n, most;
   uint32_t chunks;
 };
 
 // grad[a] = the sum of the parts of a's groups in order (0 without rows); a group of one tile
 // under ids == NULL has written its adapter's gradient itself.
-__global__ void __launch_bounds__(kThreads) wgrad_reduce_kernel(ReduceArgs p) {
+__global__ void __launch_bounds__(kThreads) grad_reduce_kernel(ReduceArgs p) {
   const int lane = threadIdx.x & (kWave - 1);
   const int a = int(blockIdx.x / p.chunks);
   const int64_t e = (int64_t(blockIdx.x - a * p.chunks) * kThreads + threadIdx.x) * 4;
@@ -676,7 +827,7 @@ __global__ void __launch_bounds__(kThreads) wgrad_reduce_kernel(ReduceArgs p) {
       group_rows(p.offsets, g0 + lane, p.S, &lo, &hi);
       id = adapter_of(p.ids, g0 + lane, p.n);
     }
-    const int n = int((int64_t(hi) - lo + (1 << p.bm_log2) - 1) >> p.bm_log2);
+    const int n = grad_tiles(hi - lo, p.most);
     const int k = single && n == 1 ? 0 : n;
     const int ki = wave_scan(k);
     if (single && a >= g0 && a < g0 + kWave && __builtin_amdgcn_readlane(n, a - g0) == 1) return;
@@ -684,15 +835,55 @@ __global__ void __launch_bounds__(kThreads) wgrad_reduce_kernel(ReduceArgs p) {
     while (mine) {
       const int l = __ffsll((unsigned long long)mine) - 1;
       mine &= mine - 1;
-      const int cnt = __builtin_amdgcn_readlane(k, l);
       const int64_t first = kbase + __builtin_amdgcn_readlane(ki - k, l);
+      int64_t cnt = __builtin_amdgcn_readlane(k, l);
+      if (cnt > p.parts_cap - first) cnt = p.parts_cap - first;
       if (e < p.len)
-        for (int i = 0; i < cnt && first + i < p.parts_cap; ++i)
-          sum += *reinterpret_cast<const f32x4*>(p.parts + (first + i) * p.len + e);
+        for (int64_t i = 0; i < cnt; ++i) sum += *reinterpret_cast<const f32x4*>(p.parts + (first + i) * p.len + e);
     }
     kbase += __builtin_amdgcn_readlane(ki, kWave - 1);
   }
   if (e < p.len) *reinterpret_cast<f32x4*>(p.grad + int64_t(a) * p.len + e) = sum;
+}
+
+// u[p] = scale of p's adapter * the sum of its chunks in order.  A thread has 4 ranks of a row; the
+// row's group is found by bisection.
+struct SumUArgs {
+  const float* upart;     // [chunks, S, r]
+  const float* scale;     // nullable: 1
+  const int32_t* offsets;
+  const int32_t* ids;
+  float* u;               // [S, r]
+  int S, G, n, r, chunks;
+};
+__global__ void __launch_bounds__(kThreads) sum_u_kernel(SumUArgs p) {
+  const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
+  const int per = p.r >> 2;
+  const int64_t row = i / per;
+  if (row >= p.S) return;
+  int lo = 0, hi = p.G;  // the last group that starts at or before the row: the one that holds it, if any does
+  while (lo + 1 < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (p.offsets[mid] <= row) lo = mid;
+    else hi = mid;
+  }
+  // a row outside every group, or of a group without an adapter, has no parts
+  if (p.offsets[lo] > row || p.offsets[lo + 1] <= row) return;
+  const int a = adapter_of(p.ids, lo, p.n);
+  if (a < 0) return;
+  const int64_t piece = int64_t(p.S) * p.r;
+  const float* src = p.upart + row * p.r + 4 * (i - row * per);
+  f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+  int k = 0;
+  for (; k + 4 <= p.chunks; k += 4) {
+    f32x4 o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = *reinterpret_cast<const f32x4*>(src + (k + j) * piece);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum += o[j];
+  }
+  for (; k < p.chunks; ++k) sum += *reinterpret_cast<const f32x4*>(src + k * piece);
+  *reinterpret_cast<f32x4*>(p.u + row * p.r + 4 * (i - row * per)) = sum * (p.scale ? p.scale[a] : 1.f);
 }
 
 // [n, R, C] -> [n, C, R] bf16, 64 x 64 tiles through LDS.
@@ -738,19 +929,30 @@ int shrink_pieces(int64_t tiles, int64_t C) {
   return int(k < 1 ? 1 : (k > 16 ? 16 : k));
 }
 
-// Rows of a wgrad tile: as many as leave four workgroups a CU, 64 at least (a tile costs one
+// Column blocks of 256 a workgroup of the gradient pass takes: with u more, so that u's partial
+// sums (r float32 for each row and workgroup) stay few beside m; as many as the registers hold.
+int grad_subs(int r, bool up) { return up ? (r <= 16 ? 4 : (r <= 32 ? 2 : 1)) : 1; }
+
+// Rows of a gradient tile at most: as many tiles as fill two workgroups on every CU (a tile costs a
 // float32 write and read of its [r, C] sums).
-int wgrad_tile_log2(int64_t S, int64_t C) {
-  const int64_t chunks = div_up(C, kWgradCols);
-  const int l = log2_up(div_up(S * chunks, 1024));
-  return l < 6 ? 6 : (l > 20 ? 20 : l);
+int grad_rows(const LoraGroups& q, int64_t C, bool up) {
+  const int64_t chunks = div_up(C, kGradCols * grad_subs(q.r, up));
+  const int64_t used = q.G < q.S ? q.G : q.S;
+  int64_t tiles = 512 / chunks - used / 2;  // about half a tile for each group is its rest
+  if (tiles < 1) tiles = 1;
+  int64_t most = (div_up(q.S, tiles) + 63) / 64 * 64;
+  return int(most < 128 ? 128 : (most > (1 << 20) ? 1 << 20 : most));
+}
+int64_t grad_tiles_bound(const LoraGroups& q, int most) {
+  const int64_t used = q.G < q.S ? q.G : q.S;
+  return (q.S + used * (most - 1)) / most;
 }
 
 // Tiles that write parts: all where adapters are shared by groups; without ids only those of
-// groups of several tiles, at most two for each full tile of rows.
-int64_t parts_bound(int64_t S, int64_t G, int bm_log2, bool ids) {
-  const int64_t all = tiles_bound(S, G, bm_log2), kept = (2 * S) >> bm_log2;
-  return ids || all < kept ? all : kept;
+// groups of several tiles, at most two for each `most` rows.
+int64_t parts_bound(const LoraGroups& q, int most) {
+  const int64_t all = grad_tiles_bound(q, most), kept = 2 * q.S / most;
+  return q.ids || all < kept ? all : kept;
 }
 
 template <int RB>
@@ -819,44 +1021,57 @@ hipError_t transpose(const uint16_t* src, int64_t n, int64_t R, int64_t C, uint1
   return hipGetLastError();
 }
 
-hipError_t wgrad(const LoraGroups& q, const float* v, const uint16_t* m, const float* scale, int64_t C, bool by_column,
-                 float* grad, float* parts, hipStream_t s) {
-  WgradArgs a{};
+template <bool UP, bool BYCOL>
+void grad_rt(const GradArgs& a, unsigned grid, hipStream_t s) {
+  if (a.r <= 16) hipLaunchKernelGGL((grad_kernel<1, UP ? 4 : 1, UP, BYCOL>), dim3(grid), dim3(kThreads), 0, s, a);
+  else if (a.r <= 32) hipLaunchKernelGGL((grad_kernel<2, UP ? 2 : 1, UP, BYCOL>), dim3(grid), dim3(kThreads), 0, s, a);
+  else if (a.r <= 64) hipLaunchKernelGGL((grad_kernel<4, 1, UP, BYCOL>), dim3(grid), dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((grad_kernel<8, 1, UP, BYCOL>), dim3(grid), dim3(kThreads), 0, s, a);
+}
+
+// The gradient pass over m: grad (nullable) from v, and with w also u.
+hipError_t grad_pass(const LoraGroups& q, const float* v, const uint16_t* m, const uint16_t* w, const float* scale,
+                     int64_t C, bool by_column, float* grad, float* parts, float* upart, hipStream_t s) {
+  const bool up = upart != nullptr;
+  GradArgs a{};
   a.v = v;
   a.m = m;
+  a.w = w;
   a.scale = scale;
   a.offsets = q.offsets;
   a.ids = q.ids;
   a.grad = grad;
   a.parts = parts;
+  a.upart = upart;
+  a.C = uint32_t(C);
   a.S = int(q.S);
-  a.C = C;
   a.G = int(q.G);
   a.n = int(q.n);
   a.r = q.r;
-  a.bm_log2 = wgrad_tile_log2(q.S, C);
-  a.chunks = uint32_t(div_up(C, kWgradCols));
-  a.by_column = by_column ? 1 : 0;
-  a.parts_cap = parts_bound(q.S, q.G, a.bm_log2, q.ids != nullptr);
-  const unsigned grid = unsigned(tiles_bound(q.S, q.G, a.bm_log2) * a.chunks);
-  if (grid == 0) ;  // no rows: the sums below are over nothing
-  else if (q.r <= 16) hipLaunchKernelGGL(wgrad_kernel<1>, dim3(grid), dim3(kThreads), 0, s, a);
-  else if (q.r <= 32) hipLaunchKernelGGL(wgrad_kernel<2>, dim3(grid), dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL(wgrad_kernel<4>, dim3(grid, q.r > 64 ? 2 : 1), dim3(kThreads), 0, s, a);
-  if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  a.most = grad_rows(q, C, up);
+  a.parts_cap = parts_bound(q, a.most);
+  a.chunks = uint32_t(div_up(C, kGradCols * grad_subs(q.r, up)));
+  const unsigned grid = unsigned(grad_tiles_bound(q, a.most) * a.chunks);
+  if (grid) {
+    if (up) grad_rt<true, true>(a, grid, s);
+    else if (by_column) grad_rt<false, true>(a, grid, s);
+    else grad_rt<false, false>(a, grid, s);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  if (!grad) return hipSuccess;
   ReduceArgs d{};
   d.parts = parts;
   d.offsets = q.offsets;
   d.ids = q.ids;
   d.grad = grad;
-  d.S = int(q.S);
+  d.S = a.S;
   d.len = q.r * C;
   d.parts_cap = a.parts_cap;
   d.G = a.G;
   d.n = a.n;
-  d.bm_log2 = a.bm_log2;
+  d.most = a.most;
   d.chunks = uint32_t(div_up(d.len, 4 * kThreads));
-  hipLaunchKernelGGL(wgrad_reduce_kernel, dim3(unsigned(q.n * d.chunks)), dim3(kThreads), 0, s, d);
+  hipLaunchKernelGGL(grad_reduce_kernel, dim3(unsigned(q.n * d.chunks)), dim3(kThreads), 0, s, d);
   return hipGetLastError();
 }
 
@@ -864,29 +1079,23 @@ size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Workspace of a backward call.
 struct BackwardLayout {
-  int pieces;
-  size_t u, upart, bt, at, parts, total;
+  size_t u, upart, at, parts, total;
 };
 BackwardLayout backward_layout(const LoraBackwardLaunch& L) {
   const LoraGroups& q = L.q;
   BackwardLayout w{};
-  const int64_t tiles = tiles_bound(q.S, q.G, row_tile_log2(q.S, q.G, q.r));
   const bool need_u = L.gx || L.ga;
-  // the pieces of u are summed where gx is expanded from them
-  w.pieces = L.gx ? shrink_pieces(tiles, q.N) : 1;
   size_t off = 0;
   w.u = off;
   if (need_u) off += align256(size_t(q.S) * q.r * 4);
   w.upart = off;
-  if (w.pieces > 1) off += align256(size_t(w.pieces) * q.S * q.r * 4);
-  w.bt = off;
-  if (need_u) off += align256(size_t(q.n) * q.r * q.N * 2);
+  if (need_u) off += align256(size_t(div_up(q.N, kGradCols * grad_subs(q.r, true))) * q.S * q.r * 4);
   w.at = off;
   if (L.gx) off += align256(size_t(q.n) * q.r * q.K * 2);
   w.parts = off;
   size_t pa = 0, pb = 0;  // one after the other in the same place
-  if (L.ga) pa = size_t(parts_bound(q.S, q.G, wgrad_tile_log2(q.S, q.K), q.ids != nullptr)) * q.r * q.K * 4;
-  if (L.gb) pb = size_t(parts_bound(q.S, q.G, wgrad_tile_log2(q.S, q.N), q.ids != nullptr)) * q.r * q.N * 4;
+  if (L.ga) pa = size_t(parts_bound(q, grad_rows(q, q.K, false))) * q.r * q.K * 4;
+  if (L.gb) pb = size_t(parts_bound(q, grad_rows(q, q.N, need_u))) * q.r * q.N * 4;
   off += align256(pa > pb ? pa : pb);
   w.total = off;
   return w;
@@ -911,11 +1120,17 @@ size_t lora_backward_ws_bytes(const LoraBackwardLaunch& L) { return backward_lay
 
 // Workgroups of the largest grid a call with these sizes starts.
 int64_t lora_blocks(const LoraGroups& q) {
-  const int64_t C = q.K > q.N ? q.K : q.N, c = q.K > q.N ? q.N : q.K;
+  const int64_t C = q.K > q.N ? q.K : q.N;
   const int64_t tiles = tiles_bound(q.S, q.G, row_tile_log2(q.S, q.G, q.r));
   int64_t most = tiles * 16;
-  const int64_t of[] = {tiles * div_up(C, 128), tiles_bound(q.S, q.G, wgrad_tile_log2(q.S, c)) * div_up(C, kWgradCols),
-                        q.n * div_up(int64_t(q.r) * C, 4 * kThreads), q.n * div_up(q.r, 64) * div_up(C, 64)};
+  int64_t grad = 0;
+  for (int64_t cols : {q.K, q.N})
+    for (bool up : {false, true}) {
+      const int64_t v = grad_tiles_bound(q, grad_rows(q, cols, up)) * div_up(cols, kGradCols);
+      grad = v > grad ? v : grad;
+    }
+  const int64_t of[] = {tiles * div_up(C, 128), grad, q.n * div_up(int64_t(q.r) * C, 4 * kThreads),
+                        q.n * div_up(q.r, 64) * div_up(C, 64), div_up(q.S * (q.r / 4), kThreads)};
   for (int64_t v : of) most = v > most ? v : most;
   return most;
 }
@@ -954,21 +1169,25 @@ hipError_t launch_lora_backward(const LoraBackwardLaunch& L, hipStream_t stream)
   char* ws = reinterpret_cast<char*>(L.ws);
   float* u = reinterpret_cast<float*>(ws + w.u);
   float* parts = reinterpret_cast<float*>(ws + w.parts);
+  const bool need_u = (L.gx || L.ga) && q.S > 0;
   hipError_t e = hipSuccess;
-  if ((L.gx || L.ga) && q.S > 0) {
-    uint16_t* bt = reinterpret_cast<uint16_t*>(ws + w.bt);
-    if ((e = transpose(L.b, q.n, q.N, q.r, bt, stream)) != hipSuccess) return e;
-    float* to = w.pieces > 1 ? reinterpret_cast<float*>(ws + w.upart) : u;
-    if ((e = shrink(q, L.g, bt, L.scale, q.N, to, w.pieces, stream)) != hipSuccess) return e;
-    if (L.gx) {
-      uint16_t* at = reinterpret_cast<uint16_t*>(ws + w.at);
-      if ((e = transpose(L.a, q.n, q.r, q.K, at, stream)) != hipSuccess) return e;
-      e = expand(q, to, w.pieces, at, nullptr, q.K, L.gx_base, L.gx, L.gx_dtype, w.pieces > 1 ? u : nullptr, stream);
-      if (e != hipSuccess) return e;
-    }
+  if (need_u || L.gb) {
+    float* upart = need_u ? reinterpret_cast<float*>(ws + w.upart) : nullptr;
+    if ((e = grad_pass(q, L.z, L.g, L.b, L.scale, q.N, true, L.gb, parts, upart, stream)) != hipSuccess) return e;
   }
-  if (L.ga && (e = wgrad(q, u, L.x, nullptr, q.K, false, L.ga, parts, stream)) != hipSuccess) return e;
-  if (L.gb && (e = wgrad(q, L.z, L.g, L.scale, q.N, true, L.gb, parts, stream)) != hipSuccess) return e;
+  if (need_u) {
+    SumUArgs a{reinterpret_cast<const float*>(ws + w.upart), L.scale, q.offsets, q.ids, u, int(q.S), int(q.G),
+               int(q.n), q.r, int(div_up(q.N, kGradCols * grad_subs(q.r, true)))};
+    hipLaunchKernelGGL(sum_u_kernel, dim3(unsigned(div_up(q.S * (q.r / 4), kThreads))), dim3(kThreads), 0, stream, a);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (L.gx && q.S > 0) {
+    uint16_t* at = reinterpret_cast<uint16_t*>(ws + w.at);
+    if ((e = transpose(L.a, q.n, q.r, q.K, at, stream)) != hipSuccess) return e;
+    e = expand(q, u, 1, at, nullptr, q.K, L.gx_base, L.gx, L.gx_dtype, nullptr, stream);
+    if (e != hipSuccess) return e;
+  }
+  if (L.ga) e = grad_pass(q, u, L.x, nullptr, nullptr, q.K, false, L.ga, parts, nullptr, stream);
   return e;
 }
 
