@@ -91,6 +91,14 @@ __device__ __forceinline__ u32x4 buf_load(__amdgpu_buffer_rsrc_t r, uint32_t lan
 __device__ __forceinline__ bf16x8 buf_load8(__amdgpu_buffer_rsrc_t r, uint32_t lane_off, uint32_t off) {
   return __builtin_bit_cast(bf16x8, __builtin_amdgcn_raw_buffer_load_b128(r, lane_off, off, 0));
 }
+// A buffer whose base and size are the same in every lane; said so, they stay in scalar registers
+// (else each access becomes a loop over the lanes' values).
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t wave_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(b)), hi = __builtin_amdgcn_readfirstlane(uint32_t(b >> 32));
+  return buffer_rsrc(reinterpret_cast<const void*>(uint64_t(lo) | (uint64_t(hi) << 32)),
+                     __builtin_amdgcn_readfirstlane(bytes));
+}
 constexpr uint32_t kNowhere = 0x80000000u;  // past the end of every buffer (of 2^31 bytes at most)
 
 // Sums of one wave over its units of the columns: acc[b][k] gets rows 16b .. of the tile by ranks
@@ -103,8 +111,8 @@ __device__ __forceinline__ void shrink_sums(const uint16_t* __restrict__ m, cons
                                             int r, int rows, int first, int end, int waves, f32x4 (&acc)[RB][RT]) {
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, q = lane >> 4;
-  const __amdgpu_buffer_rsrc_t mres = buffer_rsrc(m, uint32_t(rows) * C * 2u);
-  const __amdgpu_buffer_rsrc_t wres = buffer_rsrc(w, uint32_t(r) * C * 2u);
+  const __amdgpu_buffer_rsrc_t mres = wave_rsrc(m, uint32_t(rows) * C * 2u);
+  const __amdgpu_buffer_rsrc_t wres = wave_rsrc(w, uint32_t(r) * C * 2u);
   const uint32_t lane_off = uint32_t(c) * C * 2u + 16u * q, block = 32u * C;  // bytes of 16 rows
   struct Unit {
     bf16x8 m[U][RB], w[U][RT];
@@ -292,9 +300,9 @@ struct Expand {
 
     __device__ __forceinline__ Rows(const out_t* base_, out_t* out_, const uint16_t* w_, uint32_t C_, int r_, int rows,
                                     bool adapter_)
-        : base(buffer_rsrc(base_, base_ ? uint32_t(rows) * C_ * kSize : 0u)),  // no base: all of it reads as zero
-          out(buffer_rsrc(out_, uint32_t(rows) * C_ * kSize)),
-          w(buffer_rsrc(w_, C_ * uint32_t(r_) * 2u)), C(C_), r(uint32_t(r_)), adapter(adapter_) {
+        : base(wave_rsrc(base_, base_ ? uint32_t(rows) * C_ * kSize : 0u)),  // no base: all of it reads as zero
+          out(wave_rsrc(out_, uint32_t(rows) * C_ * kSize)),
+          w(wave_rsrc(w_, C_ * uint32_t(r_) * 2u)), C(C_), r(uint32_t(r_)), adapter(adapter_) {
       const uint32_t lane = threadIdx.x & (kWave - 1), c = lane & 15, q = lane >> 4;
       row_off = (c * C + kLaneCols * q) * kSize;
 #pragma unroll
@@ -675,7 +683,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
     const uint16_t* at = p.m + (int64_t(t.row0) + row) * p.C;
     const int left = t.rows - row;
     const __amdgpu_buffer_rsrc_t res =
-        buffer_rsrc(at, left > 0 ? uint32_t(left < kGradRows ? left : kGradRows) * p.C * 2u : 0u);
+        wave_rsrc(at, left > 0 ? uint32_t(left < kGradRows ? left : kGradRows) * p.C * 2u : 0u);
     const uint32_t col = col0 + kGradCols * sub + 8 * piece;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -686,7 +694,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
   auto load_v = [&](int row, float (&v)[kVTurns][2]) {
     const int left = t.rows - row;
     const __amdgpu_buffer_rsrc_t res =
-        buffer_rsrc(p.v + (int64_t(t.row0) + row) * p.r, grad && left > 0 ? uint32_t(left < kGradRows ? left : kGradRows) * p.r * 4u : 0u);
+        wave_rsrc(p.v + (int64_t(t.row0) + row) * p.r, grad && left > 0 ? uint32_t(left < kGradRows ? left : kGradRows) * p.r * 4u : 0u);
 #pragma unroll
     for (int j = 0; j < kVTurns; ++j) {
       const int i = tid + j * kThreads, rank = i % (16 * RT), pair = i / (16 * RT);
@@ -697,10 +705,33 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
     }
   };
 
+  // Fragments of a block.  m transposed: columns 64 wave + 16 ct + c, rows 32 ks + 8 q .. + 7.
+  auto m_columns = [&](int ks, int ct) {
+    s16x8 mt;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r4 = 32 * ks + 8 * q + 4 * h + (c >> 2), u = 4 * wave + ct;
+      const s16x4 x = lds_read_tr(lds + block_at(r4, 2 * u + ((c >> 1) & 1)) + 8 * (c & 1));
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mt[4 * h + j] = x[j];
+    }
+    return __builtin_bit_cast(bf16x8, mt);
+  };
+  auto v_ranks = [&](int ks, int k, int h) {
+    return *reinterpret_cast<const bf16x8*>(vt + (16 * RT * h + 16 * k + c) * kVStride + 32 * ks + 8 * q);
+  };
+  auto m_rows = [&](int s) {
+    return *reinterpret_cast<const bf16x8*>(lds + block_at(16 * wave + c, 4 * s + q));
+  };
+  auto w_ranks = [&](int sub, int s, int k) {
+    return *reinterpret_cast<const bf16x8*>(wt + (16 * k + c) * kWStride + kGradCols * sub + 32 * s + 8 * q);
+  };
+  constexpr int kUSteps = RT <= 2 ? 4 : (RT == 4 ? 2 : 1);  // steps of u whose fragments are read together
+
   u32x4 mv[8];
   float vv[kVTurns][2];
-  load_block(0, 0, mv);
   load_v(0, vv);
+  load_block(0, 0, mv);
   f32x4 us[RT];
 #pragma unroll
   for (int k = 0; k < RT; ++k) us[k] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -713,7 +744,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
       if (sub == 0 && grad) {
 #pragma unroll
         for (int j = 0; j < kVTurns; ++j) {
-          const int i = tid + j * kThreads, rank = i % (16 * RT), pair = i / (16 * RT);
+          const int e = tid + j * kThreads, rank = e % (16 * RT), pair = e / (16 * RT);
           const Parts x = split3(vv[j][0]), y = split3(vv[j][1]);
           uint32_t* at = reinterpret_cast<uint32_t*>(vt + rank * kVStride) + pair;
           at[0] = hi2(x.hi, y.hi);
@@ -724,59 +755,81 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
       __syncthreads();
       if (sub + 1 < NSUB) {
         load_block(row, sub + 1, mv);
-      } else {
-        load_block(row + kGradRows, 0, mv);  // past the tile: zeros, unused
+      } else {  // past the tile: zeros, unused
         load_v(row + kGradRows, vv);
+        load_block(row + kGradRows, 0, mv);
       }
-      if (grad) {
+      // Fragments are read from LDS a group ahead of the products that use them: two waves a SIMD do
+      // not hide the reads' latency (read where used, a block took twice as long).
+      bf16x8 um[kUSteps], uw[kUSteps][RT];
+      auto read_u = [&](int s0) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          bf16x8 mf[4];
+        for (int s = 0; s < kUSteps; ++s) {
+          um[s] = m_rows(s0 + s);
 #pragma unroll
-          for (int ct = 0; ct < 4; ++ct) {
-            s16x8 mt;
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int r4 = 32 * ks + 8 * q + 4 * h + (c >> 2), u = 4 * wave + ct;
-              const s16x4 x = lds_read_tr(lds + block_at(r4, 2 * u + ((c >> 1) & 1)) + 8 * (c & 1));
-#pragma unroll
-              for (int j = 0; j < 4; ++j) mt[4 * h + j] = x[j];
-            }
-            mf[ct] = __builtin_bit_cast(bf16x8, mt);
-          }
-#pragma unroll
-          for (int k = 0; k < RT; ++k)
-#pragma unroll
-            for (int h = 0; h < 3; ++h) {
-              const bf16x8 vf =
-                  *reinterpret_cast<const bf16x8*>(vt + (16 * RT * h + 16 * k + c) * kVStride + 32 * ks + 8 * q);
-#pragma unroll
-              for (int ct = 0; ct < 4; ++ct)
-                acc[sub][ct][k] = BYCOL ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf, mf[ct], acc[sub][ct][k], 0, 0, 0)
-                                        : __builtin_amdgcn_mfma_f32_16x16x32_bf16(mf[ct], vf, acc[sub][ct][k], 0, 0, 0);
-            }
+          for (int k = 0; k < RT; ++k) uw[s][k] = w_ranks(sub, s0 + s, k);
         }
+      };
+      if (grad) {
+        bf16x8 mf[2][4];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int ct = 0; ct < 4; ++ct) mf[ks][ct] = m_columns(ks, ct);
+        bf16x8 vf[3], vn[3];
+#pragma unroll
+        for (int h = 0; h < 3; ++h) vf[h] = v_ranks(0, 0, h);
+#pragma unroll
+        for (int g = 0; g < 2 * RT; ++g) {  // (ks, rank tile) in turn, the next one's v in flight
+          const int ks = g / RT, k = g % RT;
+          if (g + 1 < 2 * RT) {
+#pragma unroll
+            for (int h = 0; h < 3; ++h) vn[h] = v_ranks((g + 1) / RT, (g + 1) % RT, h);
+          } else if (UP) {
+            read_u(0);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int h = 0; h < 3; ++h)
+#pragma unroll
+            for (int ct = 0; ct < 4; ++ct)
+              acc[sub][ct][k] = BYCOL ? __builtin_amdgcn_mfma_f32_16x16x32_bf16(vf[h], mf[ks][ct], acc[sub][ct][k], 0, 0, 0)
+                                      : __builtin_amdgcn_mfma_f32_16x16x32_bf16(mf[ks][ct], vf[h], acc[sub][ct][k], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int h = 0; h < 3; ++h) vf[h] = vn[h];
+        }
+      } else if (UP) {
+        read_u(0);
       }
       if (UP) {
 #pragma unroll
-        for (int s = 0; s < kGradCols / 32; ++s) {
-          const bf16x8 mf = *reinterpret_cast<const bf16x8*>(lds + block_at(16 * wave + c, 4 * s + q));
+        for (int s0 = 0; s0 < kGradCols / 32; s0 += kUSteps) {
+          bf16x8 m0[kUSteps], w0[kUSteps][RT];
+#pragma unroll
+          for (int s = 0; s < kUSteps; ++s) {
+            m0[s] = um[s];
+#pragma unroll
+            for (int k = 0; k < RT; ++k) w0[s][k] = uw[s][k];
+          }
+          if (s0 + kUSteps < kGradCols / 32) read_u(s0 + kUSteps);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int s = 0; s < kUSteps; ++s)
+#pragma unroll
+            for (int k = 0; k < RT; ++k) us[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w0[s][k], m0[s], us[k], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        if (sub == NSUB - 1) {
+          const int at = row + 16 * wave + c;
 #pragma unroll
           for (int k = 0; k < RT; ++k) {
-            const bf16x8 wf = *reinterpret_cast<const bf16x8*>(wt + (16 * k + c) * kWStride + kGradCols * sub + 32 * s + 8 * q);
-            us[k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wf, mf, us[k], 0, 0, 0);
+            const int rank = 16 * k + 4 * q;
+            if (at < t.rows && rank < p.r)
+              *reinterpret_cast<f32x4*>(p.upart + (int64_t(chunk) * p.S + t.row0 + at) * p.r + rank) = us[k];
+            us[k] = f32x4{0.f, 0.f, 0.f, 0.f};
           }
         }
-      }
-    }
-    if (UP) {
-      const int at = row + 16 * wave + c;
-#pragma unroll
-      for (int k = 0; k < RT; ++k) {
-        const int rank = 16 * k + 4 * q;
-        if (at < t.rows && rank < p.r)
-          *reinterpret_cast<f32x4*>(p.upart + (int64_t(chunk) * p.S + t.row0 + at) * p.r + rank) = us[k];
-        us[k] = f32x4{0.f, 0.f, 0.f, 0.f};
       }
     }
   }
@@ -921,17 +974,25 @@ int log2_up(int64_t v) {
 // 32 at ranks over 64, whose parts fill the registers.
 int row_tile_log2(int64_t S, int64_t G, int r) { return S <= 16 * G ? 4 : (r > 64 ? 5 : 6); }
 
-// Pieces the columns of a shrink are cut into: enough workgroups for four on every CU, no piece
-// under 512 columns (a unit of 128 for each wave).
-int shrink_pieces(int64_t tiles, int64_t C) {
-  const int64_t want = div_up(1024, tiles > 0 ? tiles : 1), most = C / 512;
+// Rows of a shrink tile: 32 from rank 33 on, where the sums and fragments of 64 rows leave room for
+// one workgroup a CU.
+int shrink_tile_log2(const LoraGroups& q) {
+  const int l = row_tile_log2(q.S, q.G, q.r);
+  return q.r > 32 && l > 5 ? 5 : l;
+}
+
+// Pieces the columns of a shrink are cut into: as many workgroups as are resident together (three
+// or four on every CU), no piece under 512 columns (a unit of 128 for each wave).
+int shrink_pieces(const LoraGroups& q, int64_t C) {
+  const int64_t tiles = tiles_bound(q.S, q.G, shrink_tile_log2(q));
+  const int64_t want = div_up(q.r > 32 ? 768 : 1024, tiles > 0 ? tiles : 1), most = C / 512;
   const int64_t k = want < most ? want : most;
   return int(k < 1 ? 1 : (k > 16 ? 16 : k));
 }
 
 // Column blocks of 256 a workgroup of the gradient pass takes: with u more, so that u's partial
 // sums (r float32 for each row and workgroup) stay few beside m; as many as the registers hold.
-int grad_subs(int r, bool up) { return up ? (r <= 16 ? 4 : (r <= 32 ? 2 : 1)) : 1; }
+int grad_subs(int r, bool up) { return up && r <= 16 ? 2 : 1; }
 
 // Rows of a gradient tile at most: as many tiles as fill two workgroups on every CU (a tile costs a
 // float32 write and read of its [r, C] sums).
@@ -965,7 +1026,7 @@ void shrink_rb(const ShrinkArgs& a, dim3 grid, hipStream_t s) {
 
 hipError_t shrink(const LoraGroups& q, const uint16_t* m, const uint16_t* w, const float* scale, int64_t C, float* z,
                   int pieces, hipStream_t s) {
-  const int bm = row_tile_log2(q.S, q.G, q.r);
+  const int bm = shrink_tile_log2(q);
   ShrinkArgs a{m, w, scale, q.offsets, q.ids, z, C, int(q.S), int(q.G), int(q.n), q.r, bm, uint32_t(pieces), 0};
   // the unit of the variant that shrink_rb picks
   const int rt = q.r <= 16 ? 1 : (q.r <= 32 ? 2 : (q.r <= 64 ? 4 : 8));
@@ -1004,7 +1065,7 @@ hipError_t expand(const LoraGroups& q, const float* z, int pieces, const uint16_
                   const void* base, void* out, int odt, float* z_out, hipStream_t s) {
   const int bm = row_tile_log2(q.S, q.G, q.r);
   const int64_t tiles = tiles_bound(q.S, q.G, bm);
-  const int chunks = expand_chunks(tiles, C, odt, kWaves, 1024);
+  const int chunks = expand_chunks(tiles, C, odt, kWaves, q.r > 32 ? 512 : 1024);
   ExpandArgs a{z, w, scale, q.offsets, q.ids, base, out, z_out, C, int(q.S), int(q.G), int(q.n), q.r, bm, pieces,
                uint32_t(chunks), int(div_up(div_up(C, odt == 0 ? 64 : 32), chunks))};
   const dim3 grid(unsigned(tiles * chunks));
@@ -1023,8 +1084,8 @@ hipError_t transpose(const uint16_t* src, int64_t n, int64_t R, int64_t C, uint1
 
 template <bool UP, bool BYCOL>
 void grad_rt(const GradArgs& a, unsigned grid, hipStream_t s) {
-  if (a.r <= 16) hipLaunchKernelGGL((grad_kernel<1, UP ? 4 : 1, UP, BYCOL>), dim3(grid), dim3(kThreads), 0, s, a);
-  else if (a.r <= 32) hipLaunchKernelGGL((grad_kernel<2, UP ? 2 : 1, UP, BYCOL>), dim3(grid), dim3(kThreads), 0, s, a);
+  if (a.r <= 16) hipLaunchKernelGGL((grad_kernel<1, UP ? 2 : 1, UP, BYCOL>), dim3(grid), dim3(kThreads), 0, s, a);
+  else if (a.r <= 32) hipLaunchKernelGGL((grad_kernel<2, 1, UP, BYCOL>), dim3(grid), dim3(kThreads), 0, s, a);
   else if (a.r <= 64) hipLaunchKernelGGL((grad_kernel<4, 1, UP, BYCOL>), dim3(grid), dim3(kThreads), 0, s, a);
   else hipLaunchKernelGGL((grad_kernel<8, 1, UP, BYCOL>), dim3(grid), dim3(kThreads), 0, s, a);
 }
@@ -1112,8 +1173,7 @@ bool lora_fused(const LoraGroups& q) {
 size_t lora_ws_bytes(const LoraLaunch& L) {
   const LoraGroups& q = L.q;
   if (lora_fused(q)) return 0;
-  const int64_t tiles = tiles_bound(q.S, q.G, row_tile_log2(q.S, q.G, q.r));
-  return align256(size_t(shrink_pieces(tiles, q.K)) * q.S * q.r * 4);
+  return align256(size_t(shrink_pieces(q, q.K)) * q.S * q.r * 4);
 }
 
 size_t lora_backward_ws_bytes(const LoraBackwardLaunch& L) { return backward_layout(L).total; }
@@ -1122,7 +1182,7 @@ size_t lora_backward_ws_bytes(const LoraBackwardLaunch& L) { return backward_lay
 int64_t lora_blocks(const LoraGroups& q) {
   const int64_t C = q.K > q.N ? q.K : q.N;
   const int64_t tiles = tiles_bound(q.S, q.G, row_tile_log2(q.S, q.G, q.r));
-  int64_t most = tiles * 16;
+  int64_t most = tiles_bound(q.S, q.G, shrink_tile_log2(q)) * 16;
   int64_t grad = 0;
   for (int64_t cols : {q.K, q.N})
     for (bool up : {false, true}) {
@@ -1156,8 +1216,7 @@ hipError_t launch_lora(const LoraLaunch& L, hipStream_t stream) {
     else fused_dt<1>(a, grid, stream);
     return hipGetLastError();
   }
-  const int64_t tiles = tiles_bound(q.S, q.G, row_tile_log2(q.S, q.G, q.r));
-  const int pieces = shrink_pieces(tiles, q.K);
+  const int pieces = shrink_pieces(q, q.K);
   float* z = pieces == 1 && L.z ? L.z : reinterpret_cast<float*>(L.ws);
   if (hipError_t e = shrink(q, L.x, L.a, nullptr, q.K, z, pieces, stream); e != hipSuccess) return e;
   return expand(q, z, pieces, L.b, L.scale, q.N, L.y, L.out, L.out_dtype, pieces > 1 ? L.z : nullptr, stream);
