@@ -166,8 +166,8 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:
-        stream = torch.cuda.current_stream()
+    if stream is None:  # the raw handle of torch.cuda.current_stream(), without building the object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
 
 
@@ -205,6 +205,9 @@ class _on_stream:
 
 
 def _need(t, name, dtypes, shape=None, device=None):
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes and t.is_contiguous()
+            and (shape is None or t.shape == shape) and (device is None or t.device == device)):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a tensor, not {type(t).__name__}")
     if t.device.type != "cuda":

@@ -101,82 +101,60 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t wave_rsrc(const void* base, ui
 }
 constexpr uint32_t kNowhere = 0x80000000u;  // past the end of every buffer (of 2^31 bytes at most)
 
-// Sums of one wave over its units of the columns: acc[b][k] gets rows 16b .. of the tile by ranks
-// 16k .. .  A unit is U matrix steps, 64 U contiguous bytes of each row; a wave takes the units
-// first + wave, first + wave + waves, ... below `end`, the next one's loads in flight while it
-// multiplies.  The adapter is the matrix instruction's first operand, so a lane ends with 4 ranks
-// of one row.
-template <int RB, int RT, int U>
-__device__ __forceinline__ void shrink_sums(const uint16_t* __restrict__ m, const uint16_t* __restrict__ w, uint32_t C,
-                                            int r, int rows, int first, int end, int waves, f32x4 (&acc)[RB][RT]) {
+// Sums of one wave over its units of 64 columns (128 bytes of each row): acc[b][k] gets rows 16b ..
+// of the tile by ranks 16k .. .  The wave takes the units first + wave, first + wave + waves, ...
+// below `end`.  A unit comes in whole lines (8 lanes a row; a matrix operand read straight from
+// memory has neighbouring lanes in different rows, and costs the load path three times as long)
+// through registers into the wave's own LDS, the next AHEAD units' loads in flight.  The 16-byte
+// pieces of a row are exchanged by the row so that reads of 16 rows spread over all banks.  The
+// adapter is the matrix instruction's first operand, so a lane ends with 4 ranks of one row.
+constexpr int kUnitBytes = 2048;  // 16 rows of a unit
+template <int RB, int RT, int AHEAD>
+__device__ __forceinline__ void shrink_sums(uint8_t* lds, const uint16_t* __restrict__ m, const uint16_t* __restrict__ w,
+                                            uint32_t C, int r, int rows, int first, int end, int waves,
+                                            f32x4 (&acc)[RB][RT]) {
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int c = lane & 15, q = lane >> 4;
+  const uint32_t c = lane & 15, q = lane >> 4, lrow = lane >> 3, lpiece = lane & 7;
   const __amdgpu_buffer_rsrc_t mres = wave_rsrc(m, uint32_t(rows) * C * 2u);
   const __amdgpu_buffer_rsrc_t wres = wave_rsrc(w, uint32_t(r) * C * 2u);
-  const uint32_t lane_off = uint32_t(c) * C * 2u + 16u * q, block = 32u * C;  // bytes of 16 rows
-  struct Unit {
-    bf16x8 m[U][RB], w[U][RT];
+  const uint32_t lane_off = lrow * C * 2u + 16u * lpiece, step = 16u * C;  // bytes of 8 rows
+  constexpr int kM = 2 * RB, kLoads = 2 * (RB + RT);
+  uint8_t* own = lds + wave * (RB + RT) * kUnitBytes;
+  auto load = [&](int s, u32x4 (&v)[kLoads]) {  // past the columns: zeros; past the rows of m and w too
+    const uint32_t off = 64u * s + 8u * lpiece < C ? lane_off : kNowhere;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j)
+      v[j] = j < kM ? buf_load(mres, off, 128u * s + j * step) : buf_load(wres, off, 128u * s + (j - kM) * step);
   };
-  auto load = [&](int s, Unit& v) {
+  auto multiply = [&](const u32x4 (&v)[kLoads], auto&& next) {
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t at = uint32_t(s) * (64u * U) + 64u * u;
+    for (int j = 0; j < kLoads; ++j)
+      *reinterpret_cast<u32x4*>(own + 1024 * j + 128 * lrow + 16 * (lpiece ^ ((lrow >> 1) | (4 * (j & 1))))) = v[j];
+    next();
+    bf16x8 f[2][RB + RT];
 #pragma unroll
-      for (int b = 0; b < RB; ++b) v.m[u][b] = buf_load8(mres, lane_off, at + b * block);
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
-      for (int k = 0; k < RT; ++k) v.w[u][k] = buf_load8(wres, lane_off, at + k * block);
-    }
-  };
-  auto mma = [&](const Unit& v) {
+      for (int b = 0; b < RB + RT; ++b)
+        f[u][b] = *reinterpret_cast<const bf16x8*>(own + kUnitBytes * b + 128 * c + 16 * ((4 * u + q) ^ (c >> 1)));
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+    for (int u = 0; u < 2; ++u)
 #pragma unroll
       for (int b = 0; b < RB; ++b)
 #pragma unroll
         for (int k = 0; k < RT; ++k)
-          acc[b][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(v.w[u][k], v.m[u][b], acc[b][k], 0, 0, 0);
+          acc[b][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[u][RB + k], f[u][b], acc[b][k], 0, 0, 0);
   };
-  const int full = int(C / (32u * U)), fend = end < full ? end : full;
-  int s = first + wave;
-  if (s < fend) {
-    Unit a, b;
-    load(s, a);
-    for (; s + waves < fend; s += 2 * waves) {
-      load(s + waves, b);
-      __builtin_amdgcn_sched_barrier(0);
-      mma(a);
-      __builtin_amdgcn_sched_barrier(0);
-      load(s + 2 * waves, a);  // past the piece: read for nothing, inside the buffers or zeros
-      __builtin_amdgcn_sched_barrier(0);
-      mma(b);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    if (s < fend) {
-      mma(a);
-      s += waves;
-    }
-  }
-  if (s < end) {  // the unit that holds the last columns: zeros past them
+  u32x4 v[AHEAD][kLoads];
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t at = uint32_t(s) * (64u * U) + 64u * u;
-      const uint32_t off = at + 16u * q < 2u * C ? lane_off + at : kNowhere;
-      bf16x8 wv[RT];
+  for (int i = 0; i < AHEAD; ++i) load(first + wave + i * waves, v[i]);
+  for (int s = first + wave; s < end; s += AHEAD * waves) {
 #pragma unroll
-      for (int k = 0; k < RT; ++k) wv[k] = buf_load8(wres, off == kNowhere ? kNowhere : off + k * block, 0);
-#pragma unroll
-      for (int b = 0; b < RB; ++b) {
-        const bf16x8 mv = buf_load8(mres, off == kNowhere ? kNowhere : off + b * block, 0);
-#pragma unroll
-        for (int k = 0; k < RT; ++k)
-          acc[b][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[k], mv, acc[b][k], 0, 0, 0);
-      }
-    }
+    for (int i = 0; i < AHEAD; ++i)
+      if (i == 0 || s + i * waves < end)  // loads past the piece are not used
+        multiply(v[i], [&] { load(s + (i + AHEAD) * waves, v[i]); });
   }
 }
-
-// Matrix steps of a unit: two units of RB row and RT rank fragments fit the registers beside the sums.
-constexpr int shrink_steps(int rb, int rt) { return rb + rt <= 3 ? 4 : 2; }
 
 template <int RB, int RT>
 __device__ __forceinline__ void zero_sums(f32x4 (&acc)[RB][RT]) {
@@ -203,7 +181,10 @@ struct ShrinkArgs {
 // sums meet in LDS.
 template <int RB, int RT>
 __global__ void __launch_bounds__(kThreads) shrink_kernel(ShrinkArgs p) {
-  __shared__ f32x4 part[kWaves][RB * RT][kWave];
+  // the waves' units, and after them the waves' sums
+  constexpr int kUnits = kWaves * (RB + RT) * kUnitBytes, kSums = kWaves * RB * RT * kWave * 16;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kUnits > kSums ? kUnits : kSums];
+  f32x4 (*part)[RB * RT][kWave] = reinterpret_cast<f32x4 (*)[RB * RT][kWave]>(lds);
   const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
   const int c = lane & 15, q = lane >> 4;
   const uint32_t tile = blockIdx.x / p.ksplit;
@@ -214,12 +195,12 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(ShrinkArgs p) {
   f32x4 acc[RB][RT];
   zero_sums(acc);
   if (a >= 0) {
-    constexpr int U = shrink_steps(RB, RT);
-    const int units = int((p.C + 32 * U - 1) / (32 * U));
+    const int units = int((p.C + 63) >> 6);
     const int end = (ks + 1) * p.per < units ? (ks + 1) * p.per : units;
-    shrink_sums<RB, RT, U>(p.m + t.row0 * p.C, p.w + int64_t(a) * p.r * p.C, uint32_t(p.C), p.r, t.rows, ks * p.per, end, kWaves,
-                        acc);
+    shrink_sums<RB, RT, 1>(lds, p.m + t.row0 * p.C, p.w + int64_t(a) * p.r * p.C, uint32_t(p.C), p.r, t.rows,
+                           ks * p.per, end, kWaves, acc);
   }
+  __syncthreads();
 #pragma unroll
   for (int b = 0; b < RB; ++b)
 #pragma unroll
@@ -483,16 +464,19 @@ struct FusedArgs {
   int per;
 };
 
-constexpr int kFusedWaves = 16;
+// Waves of the one-launch form: 16, 8 where their units would not fit LDS.
+constexpr int fused_waves(int rp) { return rp <= 32 ? 16 : 8; }
 
 // Both products in one launch for tiles of at most 16 rows (decoded tokens): every workgroup of a
 // tile computes the tile's z for itself, from the adapter's A in the L2 cache, instead of waiting
 // for another launch to do it.
 template <int RP, int ODT>
-__global__ void __launch_bounds__(kFusedWaves * kWave) fused_kernel(FusedArgs p) {
+__global__ void __launch_bounds__(fused_waves(RP) * kWave) fused_kernel(FusedArgs p) {
   typedef Expand<RP, ODT> X;
-  constexpr int RT = (RP + 15) / 16;
-  __shared__ f32x4 part[kFusedWaves][RT][kWave];
+  constexpr int RT = (RP + 15) / 16, kFusedWaves = fused_waves(RP);
+  constexpr int kUnits = kFusedWaves * (1 + RT) * kUnitBytes, kSums = kFusedWaves * RT * kWave * 16;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kUnits > kSums ? kUnits : kSums];
+  f32x4 (*part)[RT][kWave] = reinterpret_cast<f32x4 (*)[RT][kWave]>(lds);
   __shared__ __attribute__((aligned(16))) uint16_t zs[16 * X::kStride];
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t tile = blockIdx.x / p.chunks;
@@ -517,10 +501,10 @@ __global__ void __launch_bounds__(kFusedWaves * kWave) fused_kernel(FusedArgs p)
   f32x4 acc[1][RT];
   zero_sums(acc);
   if (a >= 0) {
-    constexpr int U = RT == 1 ? 4 : (RT == 2 ? 2 : 1);
-    shrink_sums<1, RT, U>(p.x + t.row0 * p.K, p.a + int64_t(a) * p.r * p.K, uint32_t(p.K), p.r, t.rows, 0,
-                          int((p.K + 32 * U - 1) / (32 * U)), kFusedWaves, acc);
+    shrink_sums<1, RT, RT <= 2 ? 2 : 1>(lds, p.x + t.row0 * p.K, p.a + int64_t(a) * p.r * p.K, uint32_t(p.K), p.r,
+                                        t.rows, 0, int((p.K + 63) >> 6), kFusedWaves, acc);
   }
+  __syncthreads();
 #pragma unroll
   for (int k = 0; k < RT; ++k) part[wave][k][lane] = acc[0][k];
   __syncthreads();
@@ -985,7 +969,7 @@ int shrink_tile_log2(const LoraGroups& q) {
 // or four on every CU), no piece under 512 columns (a unit of 128 for each wave).
 int shrink_pieces(const LoraGroups& q, int64_t C) {
   const int64_t tiles = tiles_bound(q.S, q.G, shrink_tile_log2(q));
-  const int64_t want = div_up(q.r > 32 ? 768 : 1024, tiles > 0 ? tiles : 1), most = C / 512;
+  const int64_t want = (q.r > 32 ? 768 : 1024) / (tiles > 0 ? tiles : 1), most = C / 512;
   const int64_t k = want < most ? want : most;
   return int(k < 1 ? 1 : (k > 16 ? 16 : k));
 }
@@ -1028,10 +1012,7 @@ hipError_t shrink(const LoraGroups& q, const uint16_t* m, const uint16_t* w, con
                   int pieces, hipStream_t s) {
   const int bm = shrink_tile_log2(q);
   ShrinkArgs a{m, w, scale, q.offsets, q.ids, z, C, int(q.S), int(q.G), int(q.n), q.r, bm, uint32_t(pieces), 0};
-  // the unit of the variant that shrink_rb picks
-  const int rt = q.r <= 16 ? 1 : (q.r <= 32 ? 2 : (q.r <= 64 ? 4 : 8));
-  const int unit = 32 * shrink_steps(1 << (bm - 4), rt);
-  a.per = int(div_up(div_up(C, unit), pieces));
+  a.per = int(div_up(div_up(C, 64), pieces));
   const dim3 grid(unsigned(tiles_bound(q.S, q.G, bm) * pieces));
   if (grid.x == 0) return hipSuccess;
   if (a.bm_log2 == 4) shrink_rb<1>(a, grid, s);
@@ -1056,16 +1037,18 @@ void expand_dt(const ExpandArgs& a, dim3 grid, hipStream_t s) {
   else expand_rb<4, ODT>(a, grid, s);
 }
 
-int expand_chunks(int64_t tiles, int64_t C, int odt, int waves, int groups_wanted) {
-  const int64_t most = div_up(div_up(C, odt == 0 ? 64 : 32), waves), want = div_up(groups_wanted, tiles > 0 ? tiles : 1);
-  return int(want < most ? want : most);
+// Pieces the columns of an expand are cut into: as many workgroups as are resident together (a
+// second round of few would take as long as the first), a step of 128 bytes for each wave at least.
+int expand_chunks(int64_t tiles, int64_t C, int odt, int waves, int resident) {
+  const int64_t most = div_up(div_up(C, odt == 0 ? 64 : 32), waves), want = resident / (tiles > 0 ? tiles : 1);
+  return int(want < 1 ? 1 : (want < most ? want : most));
 }
 
 hipError_t expand(const LoraGroups& q, const float* z, int pieces, const uint16_t* w, const float* scale, int64_t C,
                   const void* base, void* out, int odt, float* z_out, hipStream_t s) {
   const int bm = row_tile_log2(q.S, q.G, q.r);
   const int64_t tiles = tiles_bound(q.S, q.G, bm);
-  const int chunks = expand_chunks(tiles, C, odt, kWaves, q.r > 32 ? 512 : 1024);
+  const int chunks = expand_chunks(tiles, C, odt, kWaves, q.r > 32 ? 512 : 1280);
   ExpandArgs a{z, w, scale, q.offsets, q.ids, base, out, z_out, C, int(q.S), int(q.G), int(q.n), q.r, bm, pieces,
                uint32_t(chunks), int(div_up(div_up(C, odt == 0 ? 64 : 32), chunks))};
   const dim3 grid(unsigned(tiles * chunks));
@@ -1197,18 +1180,17 @@ int64_t lora_blocks(const LoraGroups& q) {
 
 template <int ODT>
 void fused_dt(const FusedArgs& a, dim3 grid, hipStream_t s) {
-  const dim3 threads(kFusedWaves * kWave);
-  if (a.r <= 8) hipLaunchKernelGGL((fused_kernel<8, ODT>), grid, threads, 0, s, a);
-  else if (a.r <= 16) hipLaunchKernelGGL((fused_kernel<16, ODT>), grid, threads, 0, s, a);
-  else if (a.r <= 32) hipLaunchKernelGGL((fused_kernel<32, ODT>), grid, threads, 0, s, a);
-  else hipLaunchKernelGGL((fused_kernel<64, ODT>), grid, threads, 0, s, a);
+  if (a.r <= 8) hipLaunchKernelGGL((fused_kernel<8, ODT>), grid, dim3(fused_waves(8) * kWave), 0, s, a);
+  else if (a.r <= 16) hipLaunchKernelGGL((fused_kernel<16, ODT>), grid, dim3(fused_waves(16) * kWave), 0, s, a);
+  else if (a.r <= 32) hipLaunchKernelGGL((fused_kernel<32, ODT>), grid, dim3(fused_waves(32) * kWave), 0, s, a);
+  else hipLaunchKernelGGL((fused_kernel<64, ODT>), grid, dim3(fused_waves(64) * kWave), 0, s, a);
 }
 
 hipError_t launch_lora(const LoraLaunch& L, hipStream_t stream) {
   const LoraGroups& q = L.q;
   if (lora_fused(q)) {
     const int64_t tiles = tiles_bound(q.S, q.G, 4);
-    const int chunks = expand_chunks(tiles, q.N, L.out_dtype, kFusedWaves, 256);
+    const int chunks = expand_chunks(tiles, q.N, L.out_dtype, fused_waves(q.r), 256);
     FusedArgs a{L.x, L.a, L.b, L.scale, q.offsets, q.ids, L.y, L.out, L.z, q.K, q.N, int(q.S), int(q.G), int(q.n),
                 q.r, uint32_t(chunks), int(div_up(div_up(q.N, L.out_dtype == 0 ? 64 : 32), chunks))};
     const dim3 grid(unsigned(tiles * chunks));
