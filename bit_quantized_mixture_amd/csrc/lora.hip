@@ -102,8 +102,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t wave_rsrc(const void* base, ui
 constexpr uint32_t kNowhere = 0x80000000u;  // past the end of every buffer (of 2^31 bytes at most)
 
 // Sums of one wave over its units of 64 columns (128 bytes of each row): acc[b][k] gets rows 16b ..
-// of the tile by ranks 16k .. .  The wave takes the units first + wave, first + wave + waves, ...
-// below `end`.  A unit comes in whole lines (8 lanes a row; a matrix operand read straight from
+// of the tile by ranks 16k .. .  The wave takes its share of the units first .. end - 1 one after the
+// other (the waves' units in turn read 10 % slower).  A unit comes in whole lines (8 lanes a row; a matrix operand read straight from
 // memory has neighbouring lanes in different rows, and costs the load path three times as long)
 // through registers into the wave's own LDS, the next AHEAD units' loads in flight.  The 16-byte
 // pieces of a row are exchanged by the row so that reads of 16 rows spread over all banks.  The
@@ -145,14 +145,16 @@ __device__ __forceinline__ void shrink_sums(uint8_t* lds, const uint16_t* __rest
         for (int k = 0; k < RT; ++k)
           acc[b][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[u][RB + k], f[u][b], acc[b][k], 0, 0, 0);
   };
+  const int share = (end - first + waves - 1) / waves, from = first + wave * share;
+  const int to = from + share < end ? from + share : end;
   u32x4 v[AHEAD][kLoads];
 #pragma unroll
-  for (int i = 0; i < AHEAD; ++i) load(first + wave + i * waves, v[i]);
-  for (int s = first + wave; s < end; s += AHEAD * waves) {
+  for (int i = 0; i < AHEAD; ++i) load(from + i, v[i]);
+  for (int s = from; s < to; s += AHEAD) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
-      if (i == 0 || s + i * waves < end)  // loads past the piece are not used
-        multiply(v[i], [&] { load(s + (i + AHEAD) * waves, v[i]); });
+      if (i == 0 || s + i < to)  // loads past the share are not used
+        multiply(v[i], [&] { load(s + i + AHEAD, v[i]); });
   }
 }
 
@@ -586,7 +588,7 @@ struct GradArgs {
   const int32_t* ids;
   float* grad;            // nullable [n, r, C], or [n, C, r] (BYCOL)
   float* parts;           // [parts_cap][r, C] (or [C, r])
-  float* upart;           // nullable [chunks, S, r]: m B, summed over a chunk's columns
+  float* upart;           // nullable [chunks, S, r]: scale * m B, summed over a chunk's columns
   int64_t parts_cap;      // parts there is room for (offsets that are not ascending ask for more)
   uint32_t C;
   int S, G, n, r, most;
@@ -644,17 +646,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
   if (a < 0) return;
   const uint32_t col0 = uint32_t(chunk) * kWCols;
   const bool grad = p.grad != nullptr;
-
-  if (UP) {  // B^T of the chunk: 8 ranks of a column a thread and turn
-    const int per = p.r >> 3;
-    for (int i = tid; i < kWCols * per; i += kThreads) {
-      const int n = i / per, k = 8 * (i - n * per);
-      u32x4 b = u32x4{0u, 0u, 0u, 0u};
-      if (col0 + n < p.C) b = *reinterpret_cast<const u32x4*>(p.w + (int64_t(a) * p.C + col0 + n) * p.r + k);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) wt[(k + j) * kWStride + n] = uint16_t(j & 1 ? b[j >> 1] >> 16 : b[j >> 1] & 0xFFFFu);
-    }
-  }
+  const float sc = p.scale ? p.scale[a] : 1.f;
 
   f32x4 acc[NSUB][4][RT];
 #pragma unroll
@@ -716,6 +708,17 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
   float vv[kVTurns][2];
   load_v(0, vv);
   load_block(0, 0, mv);
+  if (UP) {  // B^T of the chunk: 8 ranks of a column a thread and turn
+    const int per = p.r >> 3;
+    for (int i = tid; i < kWCols * per; i += kThreads) {
+      const int n = i / per, k = 8 * (i - n * per);
+      u32x4 b = u32x4{0u, 0u, 0u, 0u};
+      if (col0 + n < p.C) b = *reinterpret_cast<const u32x4*>(p.w + (int64_t(a) * p.C + col0 + n) * p.r + k);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) wt[(k + j) * kWStride + n] = uint16_t(j & 1 ? b[j >> 1] >> 16 : b[j >> 1] & 0xFFFFu);
+    }
+  }
+
   f32x4 us[RT];
 #pragma unroll
   for (int k = 0; k < RT; ++k) us[k] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -810,7 +813,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
           for (int k = 0; k < RT; ++k) {
             const int rank = 16 * k + 4 * q;
             if (at < t.rows && rank < p.r)
-              *reinterpret_cast<f32x4*>(p.upart + (int64_t(chunk) * p.S + t.row0 + at) * p.r + rank) = us[k];
+              *reinterpret_cast<f32x4*>(p.upart + (int64_t(chunk) * p.S + t.row0 + at) * p.r + rank) = us[k] * sc;
             us[k] = f32x4{0.f, 0.f, 0.f, 0.f};
           }
         }
@@ -818,7 +821,6 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
     }
   }
   if (!grad || t.kept >= p.parts_cap) return;
-  const float sc = p.scale ? p.scale[a] : 1.f;
   float* dst = t.kept < 0 ? p.grad + int64_t(a) * p.r * p.C : p.parts + int64_t(t.kept) * p.r * p.C;
 #pragma unroll
   for (int sub = 0; sub < NSUB; ++sub)
@@ -839,24 +841,36 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
       }
 }
 
-struct ReduceArgs {
+// One gradient's parts.
+struct ReducePart {
   const float* parts;     // [parts_cap, len]
-  const int32_t* offsets;
-  const int32_t* ids;
   float* grad;            // [n, len]
   int64_t len, parts_cap;
-  int S, G, n, most;
-  uint32_t chunks;
+  int most;
+  uint32_t chunks;        // workgroups an adapter has
 };
+struct ReduceArgs {
+  ReducePart of[2];
+  uint32_t first;         // workgroups of of[0]
+  const int32_t* offsets;
+  const int32_t* ids;
+  int S, G, n;
+};
+constexpr int kReduceTurns = 8, kReduceLen = 4 * kThreads * kReduceTurns;
 
 // grad[a] = the sum of the parts of a's groups in order (0 without rows); a group of one tile
 // under ids == NULL has written its adapter's gradient itself.
 __global__ void __launch_bounds__(kThreads) grad_reduce_kernel(ReduceArgs p) {
   const int lane = threadIdx.x & (kWave - 1);
-  const int a = int(blockIdx.x / p.chunks);
-  const int64_t e = (int64_t(blockIdx.x - a * p.chunks) * kThreads + threadIdx.x) * 4;
+  const bool second = blockIdx.x >= p.first;
+  const ReducePart& t = p.of[second ? 1 : 0];
+  const uint32_t block = second ? blockIdx.x - p.first : blockIdx.x;
+  const int a = int(block / t.chunks);
+  const int64_t e0 = int64_t(block - a * t.chunks) * kReduceLen + 4 * threadIdx.x;
   const bool single = p.ids == nullptr;
-  f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
+  f32x4 sum[kReduceTurns];
+#pragma unroll
+  for (int j = 0; j < kReduceTurns; ++j) sum[j] = f32x4{0.f, 0.f, 0.f, 0.f};
   int kbase = 0;
   for (int g0 = 0; g0 < p.G; g0 += kWave) {
     int lo = 0, hi = 0, id = -1;
@@ -864,7 +878,7 @@ __global__ void __launch_bounds__(kThreads) grad_reduce_kernel(ReduceArgs p) {
       group_rows(p.offsets, g0 + lane, p.S, &lo, &hi);
       id = adapter_of(p.ids, g0 + lane, p.n);
     }
-    const int n = grad_tiles(hi - lo, p.most);
+    const int n = grad_tiles(hi - lo, t.most);
     const int k = single && n == 1 ? 0 : n;
     const int ki = wave_scan(k);
     if (single && a >= g0 && a < g0 + kWave && __builtin_amdgcn_readlane(n, a - g0) == 1) return;
@@ -874,69 +888,81 @@ __global__ void __launch_bounds__(kThreads) grad_reduce_kernel(ReduceArgs p) {
       mine &= mine - 1;
       const int64_t first = kbase + __builtin_amdgcn_readlane(ki - k, l);
       int64_t cnt = __builtin_amdgcn_readlane(k, l);
-      if (cnt > p.parts_cap - first) cnt = p.parts_cap - first;
-      if (e < p.len)
-        for (int64_t i = 0; i < cnt; ++i) sum += *reinterpret_cast<const f32x4*>(p.parts + (first + i) * p.len + e);
+      if (cnt > t.parts_cap - first) cnt = t.parts_cap - first;
+      for (int64_t i = 0; i < cnt; ++i) {
+        const float* src = t.parts + (first + i) * t.len;
+        f32x4 v[kReduceTurns];
+#pragma unroll
+        for (int j = 0; j < kReduceTurns; ++j) {
+          const int64_t e = e0 + 4 * kThreads * j;
+          v[j] = *reinterpret_cast<const f32x4*>(src + (e < t.len ? e : 0));
+        }
+#pragma unroll
+        for (int j = 0; j < kReduceTurns; ++j) sum[j] += v[j];
+      }
     }
     kbase += __builtin_amdgcn_readlane(ki, kWave - 1);
   }
-  if (e < p.len) *reinterpret_cast<f32x4*>(p.grad + int64_t(a) * p.len + e) = sum;
+#pragma unroll
+  for (int j = 0; j < kReduceTurns; ++j) {
+    const int64_t e = e0 + 4 * kThreads * j;
+    if (e < t.len) *reinterpret_cast<f32x4*>(t.grad + int64_t(a) * t.len + e) = sum[j];
+  }
 }
 
-// u[p] = scale of p's adapter * the sum of its chunks in order.  A thread has 4 ranks of a row; the
-// row's group is found by bisection.
-struct SumUArgs {
+// Between the gradient pass and what uses u: u[p] = the sum of its chunks in a fixed order (16 lanes
+// have 4 ranks each, the wave's four groups of 16 a quarter of the chunks each; rows of no adapter
+// hold garbage here and there, and nothing reads them), and A^T [n, K, r] for the expand (a thread
+// has 8 ranks of 8 columns).
+struct BetweenArgs {
   const float* upart;     // [chunks, S, r]
-  const float* scale;     // nullable: 1
-  const int32_t* offsets;
-  const int32_t* ids;
   float* u;               // [S, r]
-  int S, G, n, r, chunks;
+  const uint16_t* a;      // [n, r, K]
+  uint16_t* at;           // nullable [n, K, r]
+  int64_t len;            // S * r
+  uint32_t u_blocks;
+  int n, r, chunks, K;
 };
-__global__ void __launch_bounds__(kThreads) sum_u_kernel(SumUArgs p) {
-  const int64_t i = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-  const int per = p.r >> 2;
-  const int64_t row = i / per;
-  if (row >= p.S) return;
-  int lo = 0, hi = p.G;  // the last group that starts at or before the row: the one that holds it, if any does
-  while (lo + 1 < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (p.offsets[mid] <= row) lo = mid;
-    else hi = mid;
-  }
-  // a row outside every group, or of a group without an adapter, has no parts
-  if (p.offsets[lo] > row || p.offsets[lo + 1] <= row) return;
-  const int a = adapter_of(p.ids, lo, p.n);
-  if (a < 0) return;
-  const int64_t piece = int64_t(p.S) * p.r;
-  const float* src = p.upart + row * p.r + 4 * (i - row * per);
+__device__ __forceinline__ void sum_u(const BetweenArgs& p, int64_t wave) {
+  const int lane = threadIdx.x & (kWave - 1);
+  const int64_t e = 4 * (16 * wave + (lane & 15)), at = e < p.len ? e : 0;
   f32x4 sum = f32x4{0.f, 0.f, 0.f, 0.f};
-  int k = 0;
-  for (; k + 4 <= p.chunks; k += 4) {
-    f32x4 o[4];
+  for (int k0 = lane >> 4; k0 < p.chunks; k0 += 32) {  // eight loads in flight (past the last: the last again)
+    f32x4 o[8];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = *reinterpret_cast<const f32x4*>(src + (k + j) * piece);
+    for (int j = 0; j < 8; ++j)
+      o[j] = *reinterpret_cast<const f32x4*>(p.upart + (k0 + 4 * j < p.chunks ? k0 + 4 * j : p.chunks - 1) * p.len + at);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sum += o[j];
+    for (int j = 0; j < 8; ++j)
+      if (k0 + 4 * j < p.chunks) sum += o[j];
   }
-  for (; k < p.chunks; ++k) sum += *reinterpret_cast<const f32x4*>(src + k * piece);
-  *reinterpret_cast<f32x4*>(p.u + row * p.r + 4 * (i - row * per)) = sum * (p.scale ? p.scale[a] : 1.f);
+#pragma unroll
+  for (int m = 16; m < kWave; m <<= 1)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sum[j] += __shfl_xor(sum[j], m, kWave);
+  if (lane < 16 && e < p.len) *reinterpret_cast<f32x4*>(p.u + e) = sum;
 }
-
-// [n, R, C] -> [n, C, R] bf16, 64 x 64 tiles through LDS.
-__global__ void __launch_bounds__(kThreads) transpose_kernel(const uint16_t* __restrict__ src, int R, int C,
-                                                             int tiles_r, int tiles_c, uint16_t* __restrict__ dst) {
-  __shared__ uint16_t t[64][66];
-  const int tc = int(blockIdx.x) % tiles_c, tr = int(blockIdx.x) / tiles_c % tiles_r;
-  const int64_t at = int64_t(int(blockIdx.x) / tiles_c / tiles_r) * R * C;
-  for (int i = threadIdx.x; i < 64 * 64; i += kThreads) {
-    const int r = 64 * tr + i / 64, c = 64 * tc + i % 64;
-    if (r < R && c < C) t[i / 64][i % 64] = src[at + int64_t(r) * C + c];
+__global__ void __launch_bounds__(kThreads) between_kernel(BetweenArgs p) {
+  if (blockIdx.x < p.u_blocks) {
+    sum_u(p, int64_t(blockIdx.x) * kWaves + (threadIdx.x >> 6));
+    return;
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < 64 * 64; i += kThreads) {
-    const int c = 64 * tc + i / 64, r = 64 * tr + i % 64;
-    if (r < R && c < C) dst[at + int64_t(c) * R + r] = t[i % 64][i / 64];
+  const int64_t i = int64_t(blockIdx.x - p.u_blocks) * kThreads + threadIdx.x;
+  const int cols = p.K >> 3, ranks = p.r >> 3;
+  if (i >= int64_t(p.n) * ranks * cols) return;
+  const int64_t col = i % cols, j = i / cols, rank = j % ranks, a = j / ranks;
+  const uint16_t* src = p.a + ((a * p.r + 8 * rank) * p.K + 8 * col);
+  u32x4 v[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) v[k] = *reinterpret_cast<const u32x4*>(src + int64_t(k) * p.K);
+  uint16_t* dst = p.at + ((a * p.K + 8 * col) * p.r + 8 * rank);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    u32x4 o;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      o[k] = perm(v[2 * k + 1][c >> 1], v[2 * k][c >> 1], c & 1 ? 0x07060302u : 0x05040100u);
+    *reinterpret_cast<u32x4*>(dst + int64_t(c) * p.r) = o;
   }
 }
 
@@ -965,11 +991,11 @@ int shrink_tile_log2(const LoraGroups& q) {
   return q.r > 32 && l > 5 ? 5 : l;
 }
 
-// Pieces the columns of a shrink are cut into: as many workgroups as are resident together (three
-// or four on every CU), no piece under 512 columns (a unit of 128 for each wave).
+// Pieces the columns of a shrink are cut into: as many workgroups as are resident together (three on
+// every CU), no piece under 512 columns (two units for each wave).
 int shrink_pieces(const LoraGroups& q, int64_t C) {
   const int64_t tiles = tiles_bound(q.S, q.G, shrink_tile_log2(q));
-  const int64_t want = (q.r > 32 ? 768 : 1024) / (tiles > 0 ? tiles : 1), most = C / 512;
+  const int64_t want = 768 / (tiles > 0 ? tiles : 1), most = C / 512;
   const int64_t k = want < most ? want : most;
   return int(k < 1 ? 1 : (k > 16 ? 16 : k));
 }
@@ -1037,8 +1063,9 @@ void expand_dt(const ExpandArgs& a, dim3 grid, hipStream_t s) {
   else expand_rb<4, ODT>(a, grid, s);
 }
 
-// Pieces the columns of an expand are cut into: as many workgroups as are resident together (a
-// second round of few would take as long as the first), a step of 128 bytes for each wave at least.
+// Pieces the columns of an expand are cut into: as many workgroups as are resident together (by the
+// registers the parts take; a second round of few would take as long as the first: rank 64, 24
+// prompts, 23 us against 32 with twice as many), a step of 128 bytes for each wave at least.
 int expand_chunks(int64_t tiles, int64_t C, int odt, int waves, int resident) {
   const int64_t most = div_up(div_up(C, odt == 0 ? 64 : 32), waves), want = resident / (tiles > 0 ? tiles : 1);
   return int(want < 1 ? 1 : (want < most ? want : most));
@@ -1048,20 +1075,13 @@ hipError_t expand(const LoraGroups& q, const float* z, int pieces, const uint16_
                   const void* base, void* out, int odt, float* z_out, hipStream_t s) {
   const int bm = row_tile_log2(q.S, q.G, q.r);
   const int64_t tiles = tiles_bound(q.S, q.G, bm);
-  const int chunks = expand_chunks(tiles, C, odt, kWaves, q.r > 32 ? 512 : 1280);
+  const int chunks = expand_chunks(tiles, C, odt, kWaves, q.r > 32 ? 512 : (q.r > 16 ? 1280 : 1792));
   ExpandArgs a{z, w, scale, q.offsets, q.ids, base, out, z_out, C, int(q.S), int(q.G), int(q.n), q.r, bm, pieces,
                uint32_t(chunks), int(div_up(div_up(C, odt == 0 ? 64 : 32), chunks))};
   const dim3 grid(unsigned(tiles * chunks));
   if (grid.x == 0) return hipSuccess;
   if (odt == 0) expand_dt<0>(a, grid, s);
   else expand_dt<1>(a, grid, s);
-  return hipGetLastError();
-}
-
-hipError_t transpose(const uint16_t* src, int64_t n, int64_t R, int64_t C, uint16_t* dst, hipStream_t s) {
-  const int64_t tr = div_up(R, 64), tc = div_up(C, 64);
-  hipLaunchKernelGGL(transpose_kernel, dim3(unsigned(n * tr * tc)), dim3(kThreads), 0, s, src, int(R), int(C),
-                     int(tr), int(tc), dst);
   return hipGetLastError();
 }
 
@@ -1073,7 +1093,7 @@ void grad_rt(const GradArgs& a, unsigned grid, hipStream_t s) {
   else hipLaunchKernelGGL((grad_kernel<8, 1, UP, BYCOL>), dim3(grid), dim3(kThreads), 0, s, a);
 }
 
-// The gradient pass over m: grad (nullable) from v, and with w also u.
+// The gradient pass over m: grad (nullable) from v, and with upart also u.
 hipError_t grad_pass(const LoraGroups& q, const float* v, const uint16_t* m, const uint16_t* w, const float* scale,
                      int64_t C, bool by_column, float* grad, float* parts, float* upart, hipStream_t s) {
   const bool up = upart != nullptr;
@@ -1102,28 +1122,24 @@ hipError_t grad_pass(const LoraGroups& q, const float* v, const uint16_t* m, con
     else grad_rt<false, false>(a, grid, s);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
-  if (!grad) return hipSuccess;
-  ReduceArgs d{};
-  d.parts = parts;
-  d.offsets = q.offsets;
-  d.ids = q.ids;
-  d.grad = grad;
-  d.S = a.S;
-  d.len = q.r * C;
-  d.parts_cap = a.parts_cap;
-  d.G = a.G;
-  d.n = a.n;
-  d.most = a.most;
-  d.chunks = uint32_t(div_up(d.len, 4 * kThreads));
-  hipLaunchKernelGGL(grad_reduce_kernel, dim3(unsigned(q.n * d.chunks)), dim3(kThreads), 0, s, d);
-  return hipGetLastError();
+  return hipSuccess;
+}
+
+// Adds the sums over grad's parts to a reduce launch.
+void reduce_of(const LoraGroups& q, int64_t C, bool up, float* grad, const float* parts, ReducePart* t) {
+  t->parts = parts;
+  t->grad = grad;
+  t->len = q.r * C;
+  t->most = grad_rows(q, C, up);
+  t->parts_cap = parts_bound(q, t->most);
+  t->chunks = uint32_t(div_up(t->len, kReduceLen));
 }
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Workspace of a backward call.
 struct BackwardLayout {
-  size_t u, upart, at, parts, total;
+  size_t u, upart, at, parts_a, parts_b, total;
 };
 BackwardLayout backward_layout(const LoraBackwardLaunch& L) {
   const LoraGroups& q = L.q;
@@ -1136,11 +1152,10 @@ BackwardLayout backward_layout(const LoraBackwardLaunch& L) {
   if (need_u) off += align256(size_t(div_up(q.N, kGradCols * grad_subs(q.r, true))) * q.S * q.r * 4);
   w.at = off;
   if (L.gx) off += align256(size_t(q.n) * q.r * q.K * 2);
-  w.parts = off;
-  size_t pa = 0, pb = 0;  // one after the other in the same place
-  if (L.ga) pa = size_t(parts_bound(q, grad_rows(q, q.K, false))) * q.r * q.K * 4;
-  if (L.gb) pb = size_t(parts_bound(q, grad_rows(q, q.N, need_u))) * q.r * q.N * 4;
-  off += align256(pa > pb ? pa : pb);
+  w.parts_a = off;
+  if (L.ga) off += align256(size_t(parts_bound(q, grad_rows(q, q.K, false))) * q.r * q.K * 4);
+  w.parts_b = off;
+  if (L.gb) off += align256(size_t(parts_bound(q, grad_rows(q, q.N, need_u))) * q.r * q.N * 4);
   w.total = off;
   return w;
 }
@@ -1172,8 +1187,8 @@ int64_t lora_blocks(const LoraGroups& q) {
       const int64_t v = grad_tiles_bound(q, grad_rows(q, cols, up)) * div_up(cols, kGradCols);
       grad = v > grad ? v : grad;
     }
-  const int64_t of[] = {tiles * div_up(C, 128), grad, q.n * div_up(int64_t(q.r) * C, 4 * kThreads),
-                        q.n * div_up(q.r, 64) * div_up(C, 64), div_up(q.S * (q.r / 4), kThreads)};
+  const int64_t of[] = {tiles * div_up(C, 128), grad, 2 * q.n * div_up(int64_t(q.r) * C, kReduceLen),
+                        div_up(q.S * (q.r / 4), 16 * kWaves) + div_up(q.n * (q.r / 8) * (q.K / 8), kThreads)};
   for (int64_t v : of) most = v > most ? v : most;
   return most;
 }
@@ -1209,27 +1224,50 @@ hipError_t launch_lora_backward(const LoraBackwardLaunch& L, hipStream_t stream)
   const BackwardLayout w = backward_layout(L);
   char* ws = reinterpret_cast<char*>(L.ws);
   float* u = reinterpret_cast<float*>(ws + w.u);
-  float* parts = reinterpret_cast<float*>(ws + w.parts);
-  const bool need_u = (L.gx || L.ga) && q.S > 0;
+  float* parts_a = reinterpret_cast<float*>(ws + w.parts_a);
+  float* parts_b = reinterpret_cast<float*>(ws + w.parts_b);
+  const bool need_u = L.gx || L.ga;  // as the layout has it
   hipError_t e = hipSuccess;
-  if (need_u || L.gb) {
+  if (q.S > 0) {
     float* upart = need_u ? reinterpret_cast<float*>(ws + w.upart) : nullptr;
-    if ((e = grad_pass(q, L.z, L.g, L.b, L.scale, q.N, true, L.gb, parts, upart, stream)) != hipSuccess) return e;
+    if ((e = grad_pass(q, L.z, L.g, L.b, L.scale, q.N, true, L.gb, parts_b, upart, stream)) != hipSuccess) return e;
+    if (need_u) {
+      uint16_t* at = L.gx ? reinterpret_cast<uint16_t*>(ws + w.at) : nullptr;
+      const int64_t u_blocks = div_up(q.S * (q.r / 4), 16 * kWaves);
+      const int64_t t_blocks = at ? div_up(q.n * (q.r / 8) * (q.K / 8), kThreads) : 0;
+      BetweenArgs a{upart, u, L.a, at, q.S * q.r, uint32_t(u_blocks), int(q.n), q.r,
+                    int(div_up(q.N, kGradCols * grad_subs(q.r, true))), int(q.K)};
+      hipLaunchKernelGGL(between_kernel, dim3(unsigned(u_blocks + t_blocks)), dim3(kThreads), 0, stream, a);
+      if ((e = hipGetLastError()) != hipSuccess) return e;
+      if (L.gx) {
+        e = expand(q, u, 1, at, nullptr, q.K, L.gx_base, L.gx, L.gx_dtype, nullptr, stream);
+        if (e != hipSuccess) return e;
+      }
+      if (L.ga) {
+        e = grad_pass(q, u, L.x, nullptr, nullptr, q.K, false, L.ga, parts_a, nullptr, stream);
+        if (e != hipSuccess) return e;
+      }
+    }
   }
-  if (need_u) {
-    SumUArgs a{reinterpret_cast<const float*>(ws + w.upart), L.scale, q.offsets, q.ids, u, int(q.S), int(q.G),
-               int(q.n), q.r, int(div_up(q.N, kGradCols * grad_subs(q.r, true)))};
-    hipLaunchKernelGGL(sum_u_kernel, dim3(unsigned(div_up(q.S * (q.r / 4), kThreads))), dim3(kThreads), 0, stream, a);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+  if (!L.ga && !L.gb) return e;
+  ReduceArgs d{};
+  d.offsets = q.offsets;
+  d.ids = q.ids;
+  d.S = int(q.S);
+  d.G = int(q.G);
+  d.n = int(q.n);
+  int64_t blocks = 0;
+  if (L.gb) {
+    reduce_of(q, q.N, need_u, L.gb, parts_b, &d.of[0]);
+    blocks = q.n * d.of[0].chunks;
   }
-  if (L.gx && q.S > 0) {
-    uint16_t* at = reinterpret_cast<uint16_t*>(ws + w.at);
-    if ((e = transpose(L.a, q.n, q.r, q.K, at, stream)) != hipSuccess) return e;
-    e = expand(q, u, 1, at, nullptr, q.K, L.gx_base, L.gx, L.gx_dtype, nullptr, stream);
-    if (e != hipSuccess) return e;
+  d.first = uint32_t(blocks);
+  if (L.ga) {
+    reduce_of(q, q.K, false, L.ga, parts_a, &d.of[1]);
+    blocks += q.n * d.of[1].chunks;
   }
-  if (L.ga) e = grad_pass(q, u, L.x, nullptr, nullptr, q.K, false, L.ga, parts, nullptr, stream);
-  return e;
+  hipLaunchKernelGGL(grad_reduce_kernel, dim3(unsigned(blocks)), dim3(kThreads), 0, stream, d);
+  return hipGetLastError();
 }
 
 }  // namespace e4b
