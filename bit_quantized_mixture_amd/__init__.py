@@ -17,7 +17,7 @@ __all__ = [
     "E4B_ROUTE_RENORMALIZE", "E4B_ACT_CLAMPED_GLU", "E4B_GU_INTERLEAVED", "E4B_MXFP4_SCALED", "E4B_MXFP4_FP16", "E4B_COMBINE_ATOMIC", "lib_path", "e4b_version", "e4b_status_string", "e4b_pack_nf4",
     "e4b_pack_mxfp4", "e4b_route_workspace_bytes", "e4b_route_permute", "e4b_moe_workspace_bytes",
     "e4b_moe_forward", "e4b_moe_forward_noalloc", "e4b_noalloc_scratch_bytes", "e4b_stream_probe", "e4b_decode_workspace_bytes", "e4b_moe_decode_step", "MoeArgs", "e4b_dgrad_workspace_bytes", "e4b_grouped_dgrad", "DgradArgs",
-    "e4b_permute_tokens", "e4b_combine_workspace_bytes", "e4b_combine_tokens", "e4b_combine_tokens_backward",
+    "e4b_permute_workspace_bytes", "e4b_permute_tokens", "e4b_combine_workspace_bytes", "e4b_combine_tokens", "e4b_combine_tokens_backward",
     "LoraArgs", "LoraBackwardArgs", "e4b_lora_workspace_bytes", "e4b_grouped_lora",
     "e4b_lora_backward_workspace_bytes", "e4b_grouped_lora_backward",
 ]
@@ -131,7 +131,8 @@ _c_pack_int4 = _decl("e4b_pack_int4_b32", [_vp, _i64, _i64, _i64, _vp, _vp, _vp]
 _c_quant_act = _decl("e4b_quantize_act_int8", [_vp, _i64, _i64, _vp, _vp, _vp])
 _c_int4_ws = _decl("e4b_int4_gemv_workspace_bytes", [ctypes.POINTER(Int4GemvArgs), ctypes.POINTER(_sz)])
 _c_int4_gemv = _decl("e4b_gemv_int4_b32", [ctypes.POINTER(Int4GemvArgs), _vp])
-_c_permute = _decl("e4b_permute_tokens", [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp])
+_c_permute_ws = _decl("e4b_permute_workspace_bytes", [_i32, _i64, _i64, _i32, ctypes.POINTER(_sz)])
+_c_permute = _decl("e4b_permute_tokens", [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp, _sz, _vp])
 _c_combine_ws = _decl("e4b_combine_workspace_bytes", [_i64, _i32, ctypes.POINTER(_sz)])
 _c_combine = _decl("e4b_combine_tokens", [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp, _i32, _vp, _sz, _vp])
 _c_combine_bwd = _decl("e4b_combine_tokens_backward", [_vp, _i32, _vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp,
@@ -706,7 +707,23 @@ def e4b_moe_decode_step(fmt, logits, x, w_gu, s_gu, w_dn, s_dn, k: int, renormal
     return out, out_f32, route_out
 
 
-def e4b_permute_tokens(x, sorted_slots, k: int, out=None, stream=None):
+def e4b_permute_workspace_bytes(T: int, H: int, k: int, dtype=torch.bfloat16) -> int:
+    n = _sz(0)
+    _check("e4b_permute_workspace_bytes", _c_permute_ws(_rows_dtype(dtype, "dtype"), T, H, k, ctypes.byref(n)))
+    return n.value
+
+
+def _small_ws(st, ws, need, dev):
+    """(workspace tensor or None, its address, its bytes): allocated where ws is None and one is needed."""
+    if ws is None:
+        if not need:
+            return None, None, 0
+        ws = st.alloc((need,), dtype=torch.uint8, device=dev)
+    _need(ws, "ws", (torch.uint8,), device=dev)
+    return ws, ws.data_ptr(), ws.numel()
+
+
+def e4b_permute_tokens(x, sorted_slots, k: int, out=None, ws=None, stream=None):
     """The routed copies of the token rows in expert order: out[p] = x[sorted_slots[p] // k].
 
     x [T, H] bf16 or float32; sorted_slots [T*k] int32 from e4b_route_permute.  Returns out
@@ -721,8 +738,10 @@ def e4b_permute_tokens(x, sorted_slots, k: int, out=None, stream=None):
             out = st.alloc((T * k, H), dtype=x.dtype, device=dev)
         else:
             _need(out, "out", (x.dtype,), (T * k, H), dev)
+        need = e4b_permute_workspace_bytes(T, H, k, x.dtype) if ws is None else 0
+        ws, wp, wn = _small_ws(st, ws, need, dev)
         _check("e4b_permute_tokens", _c_permute(x.data_ptr(), dt, T, H, k, sorted_slots.data_ptr(), out.data_ptr(),
-                                                _stream(stream)))
+                                                wp, wn, _stream(stream)))
     return out
 
 
@@ -730,17 +749,6 @@ def e4b_combine_workspace_bytes(T: int, k: int) -> int:
     n = _sz(0)
     _check("e4b_combine_workspace_bytes", _c_combine_ws(T, k, ctypes.byref(n)))
     return n.value
-
-
-def _combine_ws(st, T, k, ws, dev):
-    """(workspace tensor or None, its address, its bytes) of a combine call."""
-    if ws is None:
-        need = e4b_combine_workspace_bytes(T, k)
-        if not need:
-            return None, None, 0
-        ws = st.alloc((need,), dtype=torch.uint8, device=dev)
-    _need(ws, "ws", (torch.uint8,), device=dev)
-    return ws, ws.data_ptr(), ws.numel()
 
 
 def _tokens_of(rows, k):
@@ -766,7 +774,7 @@ def e4b_combine_tokens(rows, sorted_slots, k: int, topk_w=None, out=None, dtype=
     with _on_device(dev, stream) as st:
         if out is None:
             out = st.alloc((T, H), dtype=dtype, device=dev)
-        ws, wp, wn = _combine_ws(st, T, k, ws, dev)
+        ws, wp, wn = _small_ws(st, ws, e4b_combine_workspace_bytes(T, k) if ws is None else 0, dev)
         _check("e4b_combine_tokens", _c_combine(
             rows.data_ptr(), rdt, T, H, k, sorted_slots.data_ptr(), None if topk_w is None else topk_w.data_ptr(),
             out.data_ptr(), odt, wp, wn, _stream(stream)))
@@ -797,7 +805,7 @@ def e4b_combine_tokens_backward(g_out, rows, sorted_slots, k: int, topk_w, g_row
             g_rows = st.alloc((T * k, H), dtype=dtype, device=dev)
         if g_w is None and rows is not None:
             g_w = st.alloc((T, k), dtype=torch.float32, device=dev)
-        ws, wp, wn = _combine_ws(st, T, k, ws, dev)
+        ws, wp, wn = _small_ws(st, ws, e4b_combine_workspace_bytes(T, k) if ws is None else 0, dev)
         _check("e4b_combine_tokens_backward", _c_combine_bwd(
             g_out.data_ptr(), gdt, None if rows is None else rows.data_ptr(), rdt, T, H, k,
             sorted_slots.data_ptr(), topk_w.data_ptr(), g_rows.data_ptr(), ddt,

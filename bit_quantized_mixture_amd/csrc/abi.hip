@@ -237,11 +237,14 @@ int check_tokens(int64_t T, int64_t H, int32_t k) {
   if (T >= lim || T * k >= lim || H >= lim) return E4B_ERR_OVERFLOW;
   // byte offsets are 64-bit; the row blocks have to fit a grid
   if (T * k > (int64_t(1) << 50) / H || e4b::combine_blocks(T, H, k) >= lim ||
-      e4b::permute_blocks(T * k, 2 * H) >= lim)
+      e4b::permute_blocks(T, 2 * H, k) >= lim || e4b::permute_blocks(T, H, k) >= lim)
     return E4B_ERR_OVERFLOW;
   return E4B_OK;
 }
 
+size_t permute_ws_bytes(int32_t dtype, int64_t T, int64_t H, int32_t k) {
+  return align_up(size_t(e4b::permute_inv_slots(T, H, k, dtype == E4B_DT_F32 ? 2 : 1)) * 4);
+}
 size_t combine_ws_bytes(int64_t T, int32_t k) { return align_up(size_t(e4b::combine_inv_slots(T * k)) * 4); }
 
 // Sizes common to the adapter calls.
@@ -360,17 +363,27 @@ int e4b_grouped_lora_backward(const e4b_lora_backward_args* a, void* stream) {
   return launched(e4b::launch_lora_backward(L, (hipStream_t)stream));
 }
 
+int e4b_permute_workspace_bytes(int32_t dtype, int64_t T, int64_t H, int32_t k, size_t* bytes) {
+  if (!bytes || !dtype_ok(dtype)) return E4B_ERR_ARG;
+  const int st = check_tokens(T, H, k);
+  if (st != E4B_OK) return st;
+  *bytes = permute_ws_bytes(dtype, T, H, k);
+  return E4B_OK;
+}
+
 int e4b_permute_tokens(const void* x, int32_t dtype, int64_t T, int64_t H, int32_t k,
-                       const int32_t* sorted_slots, void* rows, void* stream) {
+                       const int32_t* sorted_slots, void* rows, void* ws, size_t ws_bytes, void* stream) {
   if (!dtype_ok(dtype)) return E4B_ERR_ARG;
   int st = check_tokens(T, H, k);
   if (st != E4B_OK) return st;
   if (T == 0) return check_device();
   if (!x || !sorted_slots || !rows) return E4B_ERR_ARG;
-  if (!aligned16(x) || !aligned16(sorted_slots) || !aligned16(rows)) return E4B_ERR_ALIGN;
+  if (!aligned16(x) || !aligned16(sorted_slots) || !aligned16(rows) || !aligned16(ws)) return E4B_ERR_ALIGN;
+  const size_t need = permute_ws_bytes(dtype, T, H, k);
+  if (need && (!ws || ws_bytes < need)) return E4B_ERR_WORKSPACE;
   if ((st = check_device()) != E4B_OK) return st;
-  return launched(e4b::launch_permute(x, dtype == E4B_DT_F32 ? 2 : 1, T * k, H, k, sorted_slots, rows,
-                                      (hipStream_t)stream));
+  return launched(e4b::launch_permute(x, dtype == E4B_DT_F32 ? 2 : 1, T, H, k, sorted_slots, rows,
+                                      static_cast<int32_t*>(ws), (hipStream_t)stream));
 }
 
 int e4b_combine_workspace_bytes(int64_t T, int32_t k, size_t* bytes) {

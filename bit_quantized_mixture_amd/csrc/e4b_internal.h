@@ -162,8 +162,9 @@ size_t decode_ctl_bytes(int64_t H);
 hipError_t launch_decode_step(const DecodeLaunch& L, hipStream_t stream);
 
 // Token rows to expert order and back (tokens.hip).  Element types are e4b_dtype values.
-hipError_t launch_permute(const void* x, int elem_halves, int64_t S, int64_t H, int k, const int32_t* slots,
-                          void* rows, hipStream_t stream);
+hipError_t launch_permute(const void* x, int elem_halves, int64_t T, int64_t H, int k, const int32_t* slots,
+                          void* rows, int32_t* inv, hipStream_t stream);
+int64_t permute_inv_slots(int64_t T, int64_t H, int k, int elem_halves);  // ints of inv (0: not used)
 struct CombineLaunch {
   int64_t T, H;
   int k, rows_dtype, out_dtype;
@@ -187,7 +188,7 @@ struct CombineBackwardLaunch {
 };
 hipError_t launch_combine_backward(const CombineBackwardLaunch& L, hipStream_t stream);
 int64_t combine_inv_slots(int64_t S);  // 0: the kernels find the rows themselves
-int64_t permute_blocks(int64_t S, int64_t halves);
+int64_t permute_blocks(int64_t T, int64_t halves, int k);
 int64_t combine_blocks(int64_t T, int64_t H, int k);
 
 // Low-rank adapters on grouped rows (lora.hip).

@@ -185,17 +185,21 @@ int e4b_route_permute(const float* logits, int64_t T, int64_t E, int32_t k, int3
                       int32_t* topk_ids, float* topk_w, int32_t* expert_offsets,
                       int32_t* sorted_slots, void* ws, size_t ws_bytes, void* stream);
 
+/* Workspace bytes e4b_permute_tokens needs (0 below 128 MB of rows: ws may then be NULL). */
+int e4b_permute_workspace_bytes(int32_t dtype, int64_t T, int64_t H, int32_t k, size_t* bytes);
+
 /*
  * e4b_permute_tokens — the routed copies of the token rows in expert order, the input of the
  * grouped products: rows[p] = x[sorted_slots[p] / k].
  *   x             [T, H] of `dtype` (an e4b_dtype).  Any H >= 1.  1 <= k <= 64, T*k < 2^31.
  *   sorted_slots  [T*k] int32 from e4b_route_permute: a permutation of 0 .. T*k - 1.
  *   rows          [T*k, H] of `dtype` out: bit copies.
+ *   ws            device workspace of at least e4b_permute_workspace_bytes().
  * A slot outside [0, T*k) leaves a row of zeros.  The gradient of x is e4b_combine_tokens of the
  * rows' gradients with topk_w = NULL.
  */
 int e4b_permute_tokens(const void* x, int32_t dtype, int64_t T, int64_t H, int32_t k,
-                       const int32_t* sorted_slots, void* rows, void* stream);
+                       const int32_t* sorted_slots, void* rows, void* ws, size_t ws_bytes, void* stream);
 
 /* Workspace bytes of e4b_combine_tokens and e4b_combine_tokens_backward (0 for small batches:
  * ws may then be NULL). */

@@ -135,6 +135,20 @@ def test_slots_without_a_row_and_named_twice(e4b, T):
     assert (g_w.reshape(-1)[missing] == 0).all() and int(missing.sum()) == 4
 
 
+@pytest.mark.parametrize("T,H,k", [(4100, 2051, 8), (70000, 520, 2), (600000, 31, 4)])
+def test_permute_in_token_order(e4b, T, H, k):
+    """From 128 MB of rows the rows are written token by token; dropped rows and a slot named twice as above."""
+    x, slots = _rows(T, H, BF16, 50), _slots(T, k, 16, 51)
+    assert e4b.e4b_permute_workspace_bytes(T, H, k) > 0
+    out = torch.full((T * k, H), 7.0, dtype=BF16, device=DEV)
+    assert torch.equal(e4b.e4b_permute_tokens(x, slots, k, out=out), x[slots.long() // k])
+    slots[3], slots[T], slots[T * k - 1], slots[70] = -1, T * k, 2 ** 31 - 1, slots[9000]
+    s = slots.long()
+    named = (s >= 0) & (s < T * k)
+    got = e4b.e4b_permute_tokens(x, slots, k, out=out.fill_(7.0))
+    assert torch.equal(got, torch.where(named[:, None], x[torch.where(named, s, 0) // k], torch.zeros_like(got)))
+
+
 def test_infinities_stay_in_their_rows(e4b):
     T, H, k, E = 20, 16, 2, 4
     slots, w = _slots(T, k, E, 21), _weights(T, k, 22)

@@ -9,14 +9,18 @@ FAKE = 0x100000  # aligned, never dereferenced: every call below fails validatio
 
 
 def test_permute_refuses(e4b):
-    def f(x=FAKE, dtype=0, T=16, H=64, k=2, slots=FAKE, rows=FAKE):
-        return e4b._c_permute(x, dtype, T, H, k, slots, rows, None)
+    def f(x=FAKE, dtype=0, T=16, H=64, k=2, slots=FAKE, rows=FAKE, ws=None, n=0):
+        return e4b._c_permute(x, dtype, T, H, k, slots, rows, ws, n, None)
     assert f(dtype=2) == ERR_ARG and f(dtype=-1) == ERR_ARG
     assert f(T=-1) == ERR_ARG and f(H=0) == ERR_ARG and f(k=0) == ERR_ARG
     assert f(x=None) == ERR_ARG and f(slots=None) == ERR_ARG and f(rows=None) == ERR_ARG
     assert f(k=65) == ERR_SHAPE
     assert f(x=FAKE + 2) == ERR_ALIGN and f(rows=FAKE + 8) == ERR_ALIGN
     assert f(T=1 << 30, k=2) == ERR_OVERFLOW and f(H=1 << 31) == ERR_OVERFLOW
+    need = e4b.e4b_permute_workspace_bytes(16384, 4096, 8)
+    assert need >= 4 * 8 * 16384 and e4b.e4b_permute_workspace_bytes(16, 64, 2, torch.float32) == 0
+    assert f(T=16384, H=4096, k=8) == ERR_WORKSPACE and f(T=16384, H=4096, k=8, ws=FAKE, n=need - 1) == ERR_WORKSPACE
+    assert f(T=16384, H=4096, k=8, ws=FAKE + 4, n=need) == ERR_ALIGN
     assert f(T=1 << 62, k=64) == ERR_OVERFLOW and f(T=1 << 30, k=1, H=(1 << 31) - 1) == ERR_OVERFLOW
 
 
