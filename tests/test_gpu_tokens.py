@@ -49,9 +49,9 @@ def _assert_within(got, ref, bound, what):
     assert (over <= 0).all(), f"{what}: over the bound by {float(over.max()):.3e}"
 
 
-# the largest two have more than 4096 slots (the rows are found through the workspace)
+# the last three have more than 4096 slots, the last one more than 65536 (other ways to find the rows)
 SHAPES = [(1, 1, 1, 1), (1, 2048, 8, 128), (3, 7, 2, 4), (5, 64, 5, 5), (17, 1003, 3, 9), (300, 24, 4, 8),
-          (512, 40, 8, 16), (513, 40, 8, 16), (1500, 520, 3, 7)]
+          (512, 40, 8, 16), (513, 40, 8, 16), (1500, 520, 3, 7), (9001, 24, 8, 11)]
 
 
 @pytest.mark.parametrize("T,H,k,E", SHAPES)
@@ -107,7 +107,7 @@ def test_combine_gradients_against_differences(e4b):
         assert abs(left - right) <= T * H * 5 * 30 * 8 * 2.0 ** -24
 
 
-@pytest.mark.parametrize("T", [40, 2000])
+@pytest.mark.parametrize("T", [40, 2000, 20000])
 def test_slots_without_a_row_and_named_twice(e4b, T):
     """A dropped row (slot -1 or past the end) contributes nothing and is left alone; of two rows
     that name one slot the higher counts."""
