@@ -243,16 +243,18 @@ __device__ __forceinline__ Parts split3(float v) {
 __device__ __forceinline__ uint32_t hi2(uint32_t first, uint32_t second) { return perm(second, first, 0x07060302u); }
 
 // Geometry of the second product at RP ranks (r rounded up to a power of two) and out type ODT: the
-// row's z stands as hi | mid | lo parts of RP ranks behind one another in the contraction; a wave
-// takes 128 bytes of every row at a time, kH matrix tiles whose rows are dealt out so that a lane
-// holds 32 consecutive bytes of one row.
+// row's z stands as hi | mid | lo parts of RP ranks behind one another in the contraction, the
+// matrix instruction's first operand.  A wave takes 64 columns at a time, four matrix tiles with the
+// columns dealt out in turn (tile h has columns 4c + h), so that a lane holds 4 consecutive columns
+// and 16 neighbouring lanes a row's 64: the rows are read and written in whole lines.  (With a lane
+// in a row of its own, as the instruction's other orientation has it, each access cost the load path
+// about 45 cycles instead of 16: gx of the 32-expert layer 55 us.)
 template <int RP, int ODT>
 struct Expand {
   static constexpr int kSteps = (3 * RP + 31) / 32;      // 32-deep matrix steps over the three parts
   static constexpr int kFrags = RP >= 32 ? RP / 32 : 1;  // distinct adapter fragments among them
   static constexpr int kStride = 32 * kSteps + 8;        // LDS row in bf16 (16 rows hit distinct banks)
-  static constexpr int kH = ODT == 0 ? 4 : 2;
-  static constexpr int kLaneCols = 4 * kH, kCols = 16 * kH;
+  static constexpr int kH = 4, kCols = 64;
   typedef row_elem<ODT> out_t;
 
   // Ranks rank .. rank + 3 of one row into the LDS row zr.
@@ -266,10 +268,11 @@ struct Expand {
     if (3 * RP + rank < 32 * kSteps) *reinterpret_cast<u32x2*>(zr + 3 * RP + rank) = u32x2{0u, 0u};
   }
 
-  // What a step of 128 bytes a row reads: the rows' bytes and the adapter's fragments.
+  // What a step reads: 4 columns of 4 rows of each row block, and the adapter's fragments.
+  typedef uint32_t vec __attribute__((ext_vector_type(ODT == 0 ? 2 : 4)));
   template <int RB>
   struct Step {
-    u32x4 y[RB][2];
+    vec y[RB][4];
     bf16x8 w[kH][kFrags];
   };
   static constexpr uint32_t kSize = sizeof(out_t);
@@ -279,54 +282,49 @@ struct Expand {
   struct Rows {
     __amdgpu_buffer_rsrc_t base, out, w;
     uint32_t C, r, row_off, w_off[kFrags];
+    int rows;
     bool adapter;
 
-    __device__ __forceinline__ Rows(const out_t* base_, out_t* out_, const uint16_t* w_, uint32_t C_, int r_, int rows,
+    __device__ __forceinline__ Rows(const out_t* base_, out_t* out_, const uint16_t* w_, uint32_t C_, int r_, int rows_,
                                     bool adapter_)
-        : base(wave_rsrc(base_, base_ ? uint32_t(rows) * C_ * kSize : 0u)),  // no base: all of it reads as zero
-          out(wave_rsrc(out_, uint32_t(rows) * C_ * kSize)),
-          w(wave_rsrc(w_, C_ * uint32_t(r_) * 2u)), C(C_), r(uint32_t(r_)), adapter(adapter_) {
+        : base(wave_rsrc(base_, base_ ? uint32_t(rows_) * C_ * kSize : 0u)),  // no base: all of it reads as zero
+          out(wave_rsrc(out_, uint32_t(rows_) * C_ * kSize)),
+          w(wave_rsrc(w_, C_ * uint32_t(r_) * 2u)), C(C_), r(uint32_t(r_)), rows(rows_), adapter(adapter_) {
       const uint32_t lane = threadIdx.x & (kWave - 1), c = lane & 15, q = lane >> 4;
-      row_off = (c * C + kLaneCols * q) * kSize;
+      row_off = (4 * q * C + 4 * c) * kSize;
 #pragma unroll
       for (int f = 0; f < kFrags; ++f) {
         const uint32_t rank = (32u * f + 8u * q) % RP;  // ranks past r meet zeros of z
-        w_off[f] = ((kLaneCols * (c >> 2) + (c & 3)) * r + (rank < r ? rank : 0u)) * 2u;
+        w_off[f] = (4 * c * r + (rank < r ? rank : 0u)) * 2u;
       }
     }
 
-    // The lane's offset of its 16-byte piece e of a row in step s, apart from the row block's.
-    __device__ __forceinline__ uint32_t piece(uint32_t s, int e) const {
-      const uint32_t q = (threadIdx.x & (kWave - 1)) >> 4;
-      const uint32_t col = kCols * s + kLaneCols * q + (16 / kSize) * e;
-      return col < C ? row_off + kCols * kSize * s + 16u * e : kNowhere;
+    // The lane's offset in step s: past every row where its columns are past the last.
+    __device__ __forceinline__ uint32_t lane_off(uint32_t s) const {
+      return kCols * s + 4 * (threadIdx.x & 15) < C ? row_off : kNowhere;
     }
 
     __device__ __forceinline__ void load(uint32_t s, Step<RB>& t) const {
-      const bool whole = kCols * (s + 1) <= C;
+      const uint32_t off = lane_off(s);
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        if (whole) {
+      for (int b = 0; b < RB; ++b)
 #pragma unroll
-          for (int b = 0; b < RB; ++b)
-            t.y[b][e] = buf_load(base, row_off, kCols * kSize * s + 16u * e + b * 16u * C * kSize);
-        } else {
-          const uint32_t at = piece(s, e);
-#pragma unroll
-          for (int b = 0; b < RB; ++b)
-            t.y[b][e] = buf_load(base, at == kNowhere ? kNowhere : at + b * 16u * C * kSize, 0);
+        for (int e = 0; e < 4; ++e) {
+          if (RB == 1 && e >= rows) continue;  // no lane has such a row (decoded tokens)
+          const uint32_t at = (kCols * s + (16 * b + e) * C) * kSize;
+          if constexpr (ODT == 0) t.y[b][e] = __builtin_bit_cast(vec, __builtin_amdgcn_raw_buffer_load_b64(base, off, at, 0));
+          else t.y[b][e] = buf_load(base, off, at);
         }
-      }
       if (adapter) {
 #pragma unroll
         for (int h = 0; h < kH; ++h)
 #pragma unroll
-          for (int f = 0; f < kFrags; ++f) t.w[h][f] = buf_load8(w, w_off[f], (kCols * s + 4u * h) * r * 2u);
+          for (int f = 0; f < kFrags; ++f) t.w[h][f] = buf_load8(w, w_off[f], (kCols * s + h) * r * 2u);
       }
     }
 
     __device__ __forceinline__ void finish(uint32_t s, const Step<RB>& t, const bf16x8 (&zf)[RB][kSteps]) const {
-      const bool whole = kCols * (s + 1) <= C;
+      const uint32_t off = lane_off(s);
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
         f32x4 d[kH];
@@ -337,27 +335,25 @@ struct Expand {
           for (int k = 0; k < kSteps; ++k)
 #pragma unroll
             for (int h = 0; h < kH; ++h)
-              d[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(t.w[h][k % kFrags], zf[b][k], d[h], 0, 0, 0);
+              d[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(zf[b][k], t.w[h][k % kFrags], d[h], 0, 0, 0);
         }
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          u32x4 o;
+        for (int e = 0; e < 4; ++e) {
+          if (RB == 1 && e >= rows) continue;
+          const uint32_t at = (kCols * s + (16 * b + e) * C) * kSize;
+          const vec y = t.y[b][e];
+          if constexpr (ODT == 1) {
+            u32x4 o;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if constexpr (ODT == 1) {
-              o[j] = __float_as_uint(__uint_as_float(t.y[b][e][j]) + d[e][j]);
-            } else {
-              const int i = 8 * e + 2 * j;
-              o[j] = bf16_rne2(__uint_as_float(t.y[b][e][j] << 16) + d[i >> 2][i & 3],
-                               __uint_as_float(t.y[b][e][j] & 0xFFFF0000u) + d[i >> 2][(i & 3) + 1]);
-            }
-          }
-          const uint32_t blk = b * 16u * C * kSize;
-          if (whole) {
-            __builtin_amdgcn_raw_buffer_store_b128(o, out, row_off, kCols * kSize * s + 16u * e + blk, 0);
+            for (int h = 0; h < 4; ++h) o[h] = __float_as_uint(__uint_as_float(y[h]) + d[h][e]);
+            __builtin_amdgcn_raw_buffer_store_b128(o, out, off, at, 0);
           } else {
-            const uint32_t at = piece(s, e);
-            __builtin_amdgcn_raw_buffer_store_b128(o, out, at == kNowhere ? kNowhere : at + blk, 0, 0);
+            u32x2 o;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              o[h] = bf16_rne2(__uint_as_float(y[h] << 16) + d[2 * h][e],
+                               __uint_as_float(y[h] & 0xFFFF0000u) + d[2 * h + 1][e]);
+            __builtin_amdgcn_raw_buffer_store_b64(o, out, off, at, 0);
           }
         }
       }
@@ -375,7 +371,7 @@ struct Expand {
   }
 
   // Steps whose loads a wave has in flight together.
-  static constexpr int ahead(int rb) { return rb == 1 ? (RP <= 32 ? 4 : 2) : (rb == 2 && RP <= 32 ? 2 : 1); }
+  static constexpr int ahead(int rb) { return rb == 1 && RP <= 32 ? 2 : 1; }
 };
 
 struct ExpandArgs {
@@ -495,7 +491,7 @@ __global__ void __launch_bounds__(fused_waves(RP) * kWave) fused_kernel(FusedArg
   const typename X::template Rows<1> rows(y ? y + t.row0 * p.N : nullptr,
                                           static_cast<typename X::out_t*>(p.out) + t.row0 * p.N,
                                           p.b + int64_t(a < 0 ? 0 : a) * p.N * p.r, uint32_t(p.N), p.r, t.rows, a >= 0);
-  constexpr int kAhead = ODT == 1 && RP <= 16 ? 2 : 1;  // 128 registers a lane
+  constexpr int kAhead = 1;  // 128 registers a lane
   int s = chunk * p.per + wave;
   typename X::template Step<1> st[kAhead];  // the first steps' loads go out before z is computed
 #pragma unroll
@@ -1065,9 +1061,9 @@ void expand_dt(const ExpandArgs& a, dim3 grid, hipStream_t s) {
 
 // Pieces the columns of an expand are cut into: as many workgroups as are resident together (by the
 // registers the parts take; a second round of few would take as long as the first: rank 64, 24
-// prompts, 23 us against 32 with twice as many), a step of 128 bytes for each wave at least.
-int expand_chunks(int64_t tiles, int64_t C, int odt, int waves, int resident) {
-  const int64_t most = div_up(div_up(C, odt == 0 ? 64 : 32), waves), want = resident / (tiles > 0 ? tiles : 1);
+// prompts, 23 us against 32 with twice as many), a step for each wave at least.
+int expand_chunks(int64_t tiles, int64_t C, int waves, int resident) {
+  const int64_t most = div_up(div_up(C, 64), waves), want = resident / (tiles > 0 ? tiles : 1);
   return int(want < 1 ? 1 : (want < most ? want : most));
 }
 
@@ -1075,9 +1071,9 @@ hipError_t expand(const LoraGroups& q, const float* z, int pieces, const uint16_
                   const void* base, void* out, int odt, float* z_out, hipStream_t s) {
   const int bm = row_tile_log2(q.S, q.G, q.r);
   const int64_t tiles = tiles_bound(q.S, q.G, bm);
-  const int chunks = expand_chunks(tiles, C, odt, kWaves, q.r > 32 ? 512 : (q.r > 16 ? 1280 : 1792));
+  const int chunks = expand_chunks(tiles, C, kWaves, q.r > 32 ? 512 : (q.r > 16 ? 1280 : 1792));
   ExpandArgs a{z, w, scale, q.offsets, q.ids, base, out, z_out, C, int(q.S), int(q.G), int(q.n), q.r, bm, pieces,
-               uint32_t(chunks), int(div_up(div_up(C, odt == 0 ? 64 : 32), chunks))};
+               uint32_t(chunks), int(div_up(div_up(C, 64), chunks))};
   const dim3 grid(unsigned(tiles * chunks));
   if (grid.x == 0) return hipSuccess;
   if (odt == 0) expand_dt<0>(a, grid, s);
@@ -1205,9 +1201,9 @@ hipError_t launch_lora(const LoraLaunch& L, hipStream_t stream) {
   const LoraGroups& q = L.q;
   if (lora_fused(q)) {
     const int64_t tiles = tiles_bound(q.S, q.G, 4);
-    const int chunks = expand_chunks(tiles, q.N, L.out_dtype, fused_waves(q.r), 256);
+    const int chunks = expand_chunks(tiles, q.N, fused_waves(q.r), 256);
     FusedArgs a{L.x, L.a, L.b, L.scale, q.offsets, q.ids, L.y, L.out, L.z, q.K, q.N, int(q.S), int(q.G), int(q.n),
-                q.r, uint32_t(chunks), int(div_up(div_up(q.N, L.out_dtype == 0 ? 64 : 32), chunks))};
+                q.r, uint32_t(chunks), int(div_up(div_up(q.N, 64), chunks))};
     const dim3 grid(unsigned(tiles * chunks));
     if (L.out_dtype == 0) fused_dt<0>(a, grid, stream);
     else fused_dt<1>(a, grid, stream);
