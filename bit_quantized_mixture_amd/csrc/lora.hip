@@ -1059,11 +1059,13 @@ void expand_dt(const ExpandArgs& a, dim3 grid, hipStream_t s) {
   else expand_rb<4, ODT>(a, grid, s);
 }
 
-// Pieces the columns of an expand are cut into: as many workgroups as are resident together (by the
-// registers the parts take; a second round of few would take as long as the first: rank 64, 24
-// prompts, 23 us against 32 with twice as many), a step for each wave at least.
-int expand_chunks(int64_t tiles, int64_t C, int waves, int resident) {
-  const int64_t most = div_up(div_up(C, 64), waves), want = resident / (tiles > 0 ? tiles : 1);
+// Pieces the columns of an expand are cut into, by the workgroups wanted, a step for each wave at
+// least.  From rank 33 on the parts of a tile's z are worth keeping for as many columns as one
+// resident round leaves (rank 64, 24 prompts: 21 us, 26 with twice the workgroups or more); below,
+// ten workgroups a CU, most of a step or two a wave, keep the memory busy to the end (gx of the
+// 32-expert layer: 39 us, 42 with four, 52 with less than two).
+int expand_chunks(int64_t tiles, int64_t C, int waves, int wanted) {
+  const int64_t most = div_up(div_up(C, 64), waves), want = wanted / (tiles > 0 ? tiles : 1);
   return int(want < 1 ? 1 : (want < most ? want : most));
 }
 
@@ -1071,7 +1073,7 @@ hipError_t expand(const LoraGroups& q, const float* z, int pieces, const uint16_
                   const void* base, void* out, int odt, float* z_out, hipStream_t s) {
   const int bm = row_tile_log2(q.S, q.G, q.r);
   const int64_t tiles = tiles_bound(q.S, q.G, bm);
-  const int chunks = expand_chunks(tiles, C, kWaves, q.r > 32 ? 512 : (q.r > 16 ? 1280 : 1792));
+  const int chunks = expand_chunks(tiles, C, kWaves, q.r > 32 ? 512 : 2560);
   ExpandArgs a{z, w, scale, q.offsets, q.ids, base, out, z_out, C, int(q.S), int(q.G), int(q.n), q.r, bm, pieces,
                uint32_t(chunks), int(div_up(div_up(C, 64), chunks))};
   const dim3 grid(unsigned(tiles * chunks));
