@@ -31,7 +31,8 @@ __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = bf16_rne(v); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 
-// V consecutive elements as float32 (V = 4 or 8).
+// V consecutive elements as float32 (V = 4 or 8).  Rows are written past the caches: what follows is
+// another kernel over more than they hold (the odd batch's token gradients 36 us kept, 27 past).
 template <int V>
 __device__ __forceinline__ void load_vec(const uint16_t* p, float (&v)[V]) {
   uint32_t d[V / 2];
@@ -65,19 +66,19 @@ __device__ __forceinline__ void store_vec(uint16_t* p, const float (&v)[V]) {
     u32x4 q;
 #pragma unroll
     for (int i = 0; i < 4; ++i) q[i] = bf16_rne2(v[2 * i], v[2 * i + 1]);
-    *reinterpret_cast<u32x4_any*>(p) = q;
+    __builtin_nontemporal_store(q, reinterpret_cast<u32x4_any*>(p));
   } else {
     u32x2 q;
     q[0] = bf16_rne2(v[0], v[1]);
     q[1] = bf16_rne2(v[2], v[3]);
-    *reinterpret_cast<u32x2_any*>(p) = q;
+    __builtin_nontemporal_store(q, reinterpret_cast<u32x2_any*>(p));
   }
 }
 template <int V>
 __device__ __forceinline__ void store_vec(float* p, const float (&v)[V]) {
 #pragma unroll
   for (int i = 0; i < V / 4; ++i)
-    *reinterpret_cast<f32x4_any*>(p + 4 * i) = f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+    __builtin_nontemporal_store(f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]}, reinterpret_cast<f32x4_any*>(p + 4 * i));
 }
 
 }  // namespace e4b

@@ -99,6 +99,9 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t wave_rsrc(const void* base, ui
   return buffer_rsrc(reinterpret_cast<const void*>(uint64_t(lo) | (uint64_t(hi) << 32)),
                      __builtin_amdgcn_readfirstlane(bytes));
 }
+// Stores of rows go past the caches (the instruction's non-temporal bit): more is written than they
+// hold, and kept there it slowed the kernels that followed (8-expert down projection 113 us, 99 so).
+constexpr int kPastCaches = 2;
 constexpr uint32_t kNowhere = 0x80000000u;  // past the end of every buffer (of 2^31 bytes at most)
 
 // Sums of one wave over its units of 64 columns (128 bytes of each row): acc[b][k] gets rows 16b ..
@@ -346,14 +349,14 @@ struct Expand {
             u32x4 o;
 #pragma unroll
             for (int h = 0; h < 4; ++h) o[h] = __float_as_uint(__uint_as_float(y[h]) + d[h][e]);
-            __builtin_amdgcn_raw_buffer_store_b128(o, out, off, at, 0);
+            __builtin_amdgcn_raw_buffer_store_b128(o, out, off, at, kPastCaches);
           } else {
             u32x2 o;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
               o[h] = bf16_rne2(__uint_as_float(y[h] << 16) + d[2 * h][e],
                                __uint_as_float(y[h] & 0xFFFF0000u) + d[2 * h + 1][e]);
-            __builtin_amdgcn_raw_buffer_store_b64(o, out, off, at, 0);
+            __builtin_amdgcn_raw_buffer_store_b64(o, out, off, at, kPastCaches);
           }
         }
       }
