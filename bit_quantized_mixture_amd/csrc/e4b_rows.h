@@ -60,6 +60,26 @@ __device__ __forceinline__ void load_vec(const float* p, float (&v)[V]) {
     for (int j = 0; j < 4; ++j) v[4 * i + j] = q[j];
   }
 }
+// The same past the caches, for what is read once.
+template <int V>
+__device__ __forceinline__ void load_once(const uint16_t* p, float (&v)[V]) {
+  static_assert(V == 8, "");
+  const u32x4 q = __builtin_nontemporal_load(reinterpret_cast<const u32x4_any*>(p));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(q[i] << 16);
+    v[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
+  }
+}
+template <int V>
+__device__ __forceinline__ void load_once(const float* p, float (&v)[V]) {
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) {
+    const f32x4 q = __builtin_nontemporal_load(reinterpret_cast<const f32x4_any*>(p + 4 * i));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[4 * i + j] = q[j];
+  }
+}
 template <int V>
 __device__ __forceinline__ void store_vec(uint16_t* p, const float (&v)[V]) {
   if constexpr (V == 8) {

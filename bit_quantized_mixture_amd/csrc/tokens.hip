@@ -174,7 +174,7 @@ __global__ void __launch_bounds__(kThreads) permute_scatter_kernel(const uint16_
 
 // One team item: V columns a lane of one token.  The loads of eight rows go out before the first
 // is used.
-template <int RDT, int ODT, int V, bool SCAN>
+template <int RDT, int ODT, int V, bool SCAN, bool ONCE>
 __global__ void __launch_bounds__(kThreads) combine_rows_kernel(const row_elem<RDT>* __restrict__ rows,
                                                                 const float* __restrict__ w,
                                                                 const int32_t* __restrict__ inv_or_slots,
@@ -219,7 +219,8 @@ __global__ void __launch_bounds__(kThreads) combine_rows_kernel(const row_elem<R
         wj[u] = w ? w[t * k + j] : 1.f;
         const row_elem<RDT>* r = rows + p * H + c;
         if (full) {
-          load_vec<V>(r, v[u]);
+          if constexpr (ONCE) load_once<V>(r, v[u]);
+            else load_vec<V>(r, v[u]);
         } else {
 #pragma unroll
           for (int i = 0; i < V; ++i)
@@ -244,7 +245,7 @@ __global__ void __launch_bounds__(kThreads) combine_rows_kernel(const row_elem<R
 
 // A team for each slot s = t*k + j: reads g_out[t] (the k teams of a token share it in the
 // caches), writes its row's gradient, and sums the weight's gradient over the row.
-template <int GDT, int RDT, int DDT, bool SCAN, bool GW>
+template <int GDT, int RDT, int DDT, bool SCAN, bool GW, bool ONCE>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(
     const row_elem<GDT>* __restrict__ g_out, const row_elem<RDT>* __restrict__ rows,
     const float* __restrict__ w, const int32_t* __restrict__ inv_or_slots, int64_t S, int64_t H, int k,
@@ -269,7 +270,8 @@ __global__ void __launch_bounds__(kThreads) combine_backward_kernel(
       float gv[8], rv[8];
       load_vec<8>(g + 8 * c, gv);
       if (GW) {
-        load_vec<8>(r + 8 * c, rv);
+        if constexpr (ONCE) load_once<8>(r + 8 * c, rv);
+        else load_vec<8>(r + 8 * c, rv);
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum = fmaf(gv[i], rv[i], sum);
       }
@@ -313,6 +315,11 @@ hipError_t launch_inv(const int32_t* slots, int64_t S, int32_t* inv, hipStream_t
   return hipGetLastError();
 }
 
+// Whether rows of so many bytes are read past the caches: what the memory-side cache (256 MB) cannot
+// have kept (2.1 GB: 405 us through it, 372 past it), and not what it may still have from the call
+// that wrote it (combine and its gradient over 71 and 94 MB: 27 and 32 us through it, 35 and 35 past).
+bool past_cache(int64_t bytes) { return bytes > (int64_t(256) << 20); }
+
 template <int RDT, int ODT, int V>
 void combine_types(const CombineLaunch& L, bool scan, hipStream_t stream) {
   const int64_t n = (L.H + V - 1) / V;
@@ -322,10 +329,13 @@ void combine_types(const CombineLaunch& L, bool scan, hipStream_t stream) {
   const auto* rows = static_cast<const row_elem<RDT>*>(L.rows);
   auto* out = static_cast<row_elem<ODT>*>(L.out);
   if (scan)
-    hipLaunchKernelGGL((combine_rows_kernel<RDT, ODT, V, true>), dim3(grid), dim3(kThreads), 0, stream, rows,
+    hipLaunchKernelGGL((combine_rows_kernel<RDT, ODT, V, true, false>), dim3(grid), dim3(kThreads), 0, stream, rows,
                        L.w, L.slots, L.T, L.H, L.k, tl, chunks, out);
+  else if (past_cache(L.T * L.k * L.H * int64_t(sizeof(row_elem<RDT>))))
+    hipLaunchKernelGGL((combine_rows_kernel<RDT, ODT, V, false, true>), dim3(grid), dim3(kThreads), 0, stream, rows,
+                       L.w, L.inv, L.T, L.H, L.k, tl, chunks, out);
   else
-    hipLaunchKernelGGL((combine_rows_kernel<RDT, ODT, V, false>), dim3(grid), dim3(kThreads), 0, stream, rows,
+    hipLaunchKernelGGL((combine_rows_kernel<RDT, ODT, V, false, false>), dim3(grid), dim3(kThreads), 0, stream, rows,
                        L.w, L.inv, L.T, L.H, L.k, tl, chunks, out);
 }
 
@@ -338,11 +348,14 @@ void backward_types(const CombineBackwardLaunch& L, bool scan, hipStream_t strea
   const auto* rows = static_cast<const row_elem<RDT>*>(L.rows);
   auto* d = static_cast<row_elem<DDT>*>(L.g_rows);
   if (scan)
-    hipLaunchKernelGGL((combine_backward_kernel<GDT, RDT, DDT, true, GW>), dim3(grid), dim3(kThreads), 0, stream,
+    hipLaunchKernelGGL((combine_backward_kernel<GDT, RDT, DDT, true, GW, false>), dim3(grid), dim3(kThreads), 0, stream,
                        g, rows, L.w, L.slots, S, L.H, L.k, tl, d, L.g_w);
-  else
-    hipLaunchKernelGGL((combine_backward_kernel<GDT, RDT, DDT, false, GW>), dim3(grid), dim3(kThreads), 0, stream,
+  else if (GW && past_cache(S * L.H * int64_t(sizeof(row_elem<RDT>))))
+    hipLaunchKernelGGL((combine_backward_kernel<GDT, RDT, DDT, false, GW, GW>), dim3(grid), dim3(kThreads), 0, stream,
                        g, rows, L.w, L.inv, S, L.H, L.k, tl, d, L.g_w);
+  else
+    hipLaunchKernelGGL((combine_backward_kernel<GDT, RDT, DDT, false, GW, false>), dim3(grid), dim3(kThreads), 0,
+                       stream, g, rows, L.w, L.inv, S, L.H, L.k, tl, d, L.g_w);
 }
 
 template <int GDT, int DDT>

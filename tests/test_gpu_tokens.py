@@ -149,6 +149,23 @@ def test_permute_in_token_order(e4b, T, H, k):
     assert torch.equal(got, torch.where(named[:, None], x[torch.where(named, s, 0) // k], torch.zeros_like(got)))
 
 
+def test_more_rows_than_the_cache_keeps(e4b):
+    """Rows of 275 MB (read past the caches): combine and its gradients."""
+    T, H, k, E = 16500, 521, 8, 16
+    rows, slots, w, g = _rows(T * k, H, F32, 60), _slots(T, k, E, 61), _weights(T, k, 62), _rows(T, H, BF16, 63)
+    out = e4b.e4b_combine_tokens(rows, slots, k, w, dtype=F32)
+    ref, mag = _combine64(rows, slots, k, w)
+    _assert_within(out, ref, (k + 2) * 2.0 ** -24 * mag, "combine")
+    del ref, mag, out
+    g_rows, g_w = e4b.e4b_combine_tokens_backward(g, rows, slots, k, w)
+    s = slots.long()
+    gs = g.double()[s // k]
+    ref = gs * w.double().reshape(-1)[s, None]
+    _assert_within(g_rows, ref, (2.0 ** -24 + HALF_STEP[BF16] * 1.001) * ref.abs(), "g_rows")
+    prod = gs * rows.double()
+    assert ((g_w.double().reshape(-1)[s] - prod.sum(1)).abs() <= (H + 1) * 2.0 ** -24 * prod.abs().sum(1)).all()
+
+
 def test_infinities_stay_in_their_rows(e4b):
     T, H, k, E = 20, 16, 2, 4
     slots, w = _slots(T, k, E, 21), _weights(T, k, 22)
