@@ -31,24 +31,17 @@ __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ void store1(uint16_t* p, float v) { *p = bf16_rne(v); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 
-// V consecutive elements as float32 (V = 4 or 8).  Rows are written past the caches: what follows is
-// another kernel over more than they hold (the odd batch's token gradients 36 us kept, 27 past).
+// V consecutive elements as float32 (4 or 8 float32, 8 bf16; 4 or 8 of either written).  Rows are
+// written past the caches: kept there they slowed the kernels that followed (7862 slots of 3000
+// float32 back to tokens and again: 36 us a call kept, 27 past).
 template <int V>
 __device__ __forceinline__ void load_vec(const uint16_t* p, float (&v)[V]) {
-  uint32_t d[V / 2];
-  if constexpr (V == 8) {
-    const u32x4 q = *reinterpret_cast<const u32x4_any*>(p);
+  static_assert(V == 8, "");
+  const u32x4 q = *reinterpret_cast<const u32x4_any*>(p);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) d[i] = q[i];
-  } else {
-    const u32x2 q = *reinterpret_cast<const u32x2_any*>(p);
-    d[0] = q[0];
-    d[1] = q[1];
-  }
-#pragma unroll
-  for (int i = 0; i < V / 2; ++i) {
-    v[2 * i] = __uint_as_float(d[i] << 16);
-    v[2 * i + 1] = __uint_as_float(d[i] & 0xFFFF0000u);
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(q[i] << 16);
+    v[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
   }
 }
 template <int V>

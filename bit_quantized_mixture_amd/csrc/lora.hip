@@ -65,6 +65,7 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offsets
     if (int(tile) - base < total) {
       const int l = __ffsll((unsigned long long)__ballot(int(tile) - base < ni)) - 1;
       const int at = int(tile) - base - (__builtin_amdgcn_readlane(ni, l) - __builtin_amdgcn_readlane(n, l));
+      if (at < 0 || at >= __builtin_amdgcn_readlane(n, l)) break;  // sums of offsets that descend can wrap
       const int row0 = __builtin_amdgcn_readlane(lo, l) + (at << bm_log2);
       const int left = __builtin_amdgcn_readlane(hi, l) - row0;
       return RowTile{g0 + l, row0, left < (1 << bm_log2) ? left : (1 << bm_log2)};
@@ -79,12 +80,10 @@ __device__ __forceinline__ int adapter_of(const int32_t* __restrict__ ids, int g
   return a >= 0 && a < n ? a : -1;
 }
 
-__device__ __forceinline__ bf16x8 load8(const uint16_t* p) { return *reinterpret_cast<const bf16x8*>(p); }
-
 // Loads and stores go through buffers that end with the tile's rows or the adapter's matrix: a
 // lane's offset is fixed for the tile, the step's offset is scalar, and what lies past the end
-// reads as zero and is not written, with no test (the issue of address arithmetic, four cycles an
-// instruction and wave, was what bounded the small tiles: 27 us against 12 for 64 decoded tokens).
+// reads as zero and is not written, with no test (64-bit addresses and tests by lane cost the small
+// tiles a tenth: 17.4 us against 15.6 for 64 decoded tokens).
 __device__ __forceinline__ u32x4 buf_load(__amdgpu_buffer_rsrc_t r, uint32_t lane_off, uint32_t off) {
   return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, lane_off, off, 0));
 }
@@ -106,11 +105,12 @@ constexpr uint32_t kNowhere = 0x80000000u;  // past the end of every buffer (of 
 
 // Sums of one wave over its units of 64 columns (128 bytes of each row): acc[b][k] gets rows 16b ..
 // of the tile by ranks 16k .. .  The wave takes its share of the units first .. end - 1 one after the
-// other (the waves' units in turn read 10 % slower).  A unit comes in whole lines (8 lanes a row; a matrix operand read straight from
-// memory has neighbouring lanes in different rows, and costs the load path three times as long)
-// through registers into the wave's own LDS, the next AHEAD units' loads in flight.  The 16-byte
-// pieces of a row are exchanged by the row so that reads of 16 rows spread over all banks.  The
-// adapter is the matrix instruction's first operand, so a lane ends with 4 ranks of one row.
+// other (the waves' units in turn read 10 % slower).  A unit comes in whole lines (8 lanes a row; a
+// matrix operand read straight from memory has neighbouring lanes in different rows, and costs the
+// load path three times as long) through registers into the wave's own LDS, the next AHEAD units'
+// loads in flight.  The 16-byte pieces of a row are exchanged by the row so that reads of 16 rows
+// spread over all banks.  The adapter is the matrix instruction's first operand, so a lane ends with
+// 4 ranks of one row.
 constexpr int kUnitBytes = 2048;  // 16 rows of a unit
 template <int RB, int RT, int AHEAD>
 __device__ __forceinline__ void shrink_sums(uint8_t* lds, const uint16_t* __restrict__ m, const uint16_t* __restrict__ w,
@@ -562,6 +562,7 @@ __device__ __forceinline__ GradTile find_grad_tile(const int32_t* __restrict__ o
       const int nl = __builtin_amdgcn_readlane(n, l), lol = __builtin_amdgcn_readlane(lo, l);
       const int rows = __builtin_amdgcn_readlane(hi, l) - lol;
       const int at = int(tile) - base - (__builtin_amdgcn_readlane(ni, l) - nl);
+      if (at < 0 || at >= nl) break;  // as above
       const int per = (grad_tiles(rows, nl) + 63) & ~63;
       const int64_t first = int64_t(at) * per;
       GradTile t;
@@ -888,7 +889,7 @@ __global__ void __launch_bounds__(kThreads) grad_reduce_kernel(ReduceArgs p) {
       const int l = __ffsll((unsigned long long)mine) - 1;
       mine &= mine - 1;
       const int64_t first = kbase + __builtin_amdgcn_readlane(ki - k, l);
-      int64_t cnt = __builtin_amdgcn_readlane(k, l);
+      int64_t cnt = first < 0 ? 0 : __builtin_amdgcn_readlane(k, l);
       if (cnt > t.parts_cap - first) cnt = t.parts_cap - first;
       for (int64_t i = 0; i < cnt; ++i) {
         const float* src = t.parts + (first + i) * t.len;
@@ -1027,12 +1028,17 @@ int64_t parts_bound(const LoraGroups& q, int most) {
   return q.ids || all < kept ? all : kept;
 }
 
+// 32-row tiles are for ranks over 32, 64-row tiles for the others.
 template <int RB>
 void shrink_rb(const ShrinkArgs& a, dim3 grid, hipStream_t s) {
-  if (a.r <= 16) hipLaunchKernelGGL((shrink_kernel<RB, 1>), grid, dim3(kThreads), 0, s, a);
-  else if (a.r <= 32) hipLaunchKernelGGL((shrink_kernel<RB, 2>), grid, dim3(kThreads), 0, s, a);
-  else if (a.r <= 64) hipLaunchKernelGGL((shrink_kernel<RB, 4>), grid, dim3(kThreads), 0, s, a);
-  else if constexpr (RB <= 2) hipLaunchKernelGGL((shrink_kernel<RB, 8>), grid, dim3(kThreads), 0, s, a);
+  if constexpr (RB != 2) {
+    if (a.r <= 16) hipLaunchKernelGGL((shrink_kernel<RB, 1>), grid, dim3(kThreads), 0, s, a);
+    else if (a.r <= 32) hipLaunchKernelGGL((shrink_kernel<RB, 2>), grid, dim3(kThreads), 0, s, a);
+  }
+  if constexpr (RB != 4) {
+    if (a.r > 64) hipLaunchKernelGGL((shrink_kernel<RB, 8>), grid, dim3(kThreads), 0, s, a);
+    else if (a.r > 32) hipLaunchKernelGGL((shrink_kernel<RB, 4>), grid, dim3(kThreads), 0, s, a);
+  }
 }
 
 hipError_t shrink(const LoraGroups& q, const uint16_t* m, const uint16_t* w, const float* scale, int64_t C, float* z,
@@ -1048,13 +1054,17 @@ hipError_t shrink(const LoraGroups& q, const uint16_t* m, const uint16_t* w, con
   return hipGetLastError();
 }
 
+// 32-row tiles are for ranks over 64, 64-row tiles for the others.
 template <int RB, int ODT>
 void expand_rb(const ExpandArgs& a, dim3 grid, hipStream_t s) {
-  if (a.r <= 8) hipLaunchKernelGGL((expand_kernel<RB, 8, ODT>), grid, dim3(kThreads), 0, s, a);
-  else if (a.r <= 16) hipLaunchKernelGGL((expand_kernel<RB, 16, ODT>), grid, dim3(kThreads), 0, s, a);
-  else if (a.r <= 32) hipLaunchKernelGGL((expand_kernel<RB, 32, ODT>), grid, dim3(kThreads), 0, s, a);
-  else if (a.r <= 64) hipLaunchKernelGGL((expand_kernel<RB, 64, ODT>), grid, dim3(kThreads), 0, s, a);
-  else if constexpr (RB <= 2) hipLaunchKernelGGL((expand_kernel<RB, 128, ODT>), grid, dim3(kThreads), 0, s, a);
+  if constexpr (RB != 2) {
+    if (a.r <= 8) hipLaunchKernelGGL((expand_kernel<RB, 8, ODT>), grid, dim3(kThreads), 0, s, a);
+    else if (a.r <= 16) hipLaunchKernelGGL((expand_kernel<RB, 16, ODT>), grid, dim3(kThreads), 0, s, a);
+    else if (a.r <= 32) hipLaunchKernelGGL((expand_kernel<RB, 32, ODT>), grid, dim3(kThreads), 0, s, a);
+    else if (a.r <= 64) hipLaunchKernelGGL((expand_kernel<RB, 64, ODT>), grid, dim3(kThreads), 0, s, a);
+  }
+  if constexpr (RB != 4)
+    if (a.r > 64) hipLaunchKernelGGL((expand_kernel<RB, 128, ODT>), grid, dim3(kThreads), 0, s, a);
 }
 
 template <int ODT>

@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(kThreads) combine_rows_kernel(const row_elem<R
         const row_elem<RDT>* r = rows + p * H + c;
         if (full) {
           if constexpr (ONCE) load_once<V>(r, v[u]);
-            else load_vec<V>(r, v[u]);
+          else load_vec<V>(r, v[u]);
         } else {
 #pragma unroll
           for (int i = 0; i < V; ++i)

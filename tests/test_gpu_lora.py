@@ -218,6 +218,66 @@ def test_nan_and_infinity_stay_in_their_row(e4b, where):
         assert torch.equal(torch.isfinite(gb[1]).all(1), torch.arange(p.N, device=DEV) != 5)
 
 
+@pytest.mark.parametrize("r", [16, 64, 104])
+def test_what_is_outside_does_not_reach_the_results(e4b, r):
+    """NaN in rows of no group, in rows of groups without an adapter and in the workspace."""
+    p = Problem(K=160, N=144, r=r, lengths=[21, 50, 3, 70, 130], ids=[1, -1, 0, 1, 5], n=3, before=5, after=40)
+    y, g, z = _normal(9, p.S, p.N, dtype=F32), _normal(10, p.S, p.N), _normal(11, p.S, p.r, dtype=F32)
+    inside = torch.zeros(p.S, dtype=torch.bool, device=DEV)
+    for rows, _ in p.groups():
+        inside[rows] = True
+
+    def step(x, g, z, byte):
+        sizes = (p.S, p.K, p.N, p.r, 5, 3)
+        ws = [torch.full((n,), byte, dtype=torch.uint8, device=DEV)
+              for n in (max(16, e4b.e4b_lora_workspace_bytes(*sizes)), e4b.e4b_lora_backward_workspace_bytes(*sizes, True))]
+        out = e4b.e4b_grouped_lora(x, p.a, p.b, p.scale, p.offsets, p.ids, y=y, ws=ws[0])[0]
+        gx, ga, gb = e4b.e4b_grouped_lora_backward(g, x, z, p.a, p.b, p.scale, p.offsets, p.ids, ws=ws[1])
+        return out[inside], gx[inside], ga, gb
+
+    clean = step(p.x, g, z, 0)
+    soiled = []
+    for t in (p.x, g, z):
+        t = t.clone()
+        t[~inside] = float("nan")
+        soiled.append(t)
+    assert all(torch.isfinite(t).all() for t in clean)
+    assert all(torch.equal(u, v) for u, v in zip(clean, step(*soiled, 0xFF)))
+
+
+def test_binding_refuses(e4b):
+    p = Problem(K=64, N=48, r=8, lengths=[20, 30])
+    y, g, z = _normal(9, p.S, p.N), _normal(10, p.S, p.N), _normal(11, p.S, p.r, dtype=F32)
+    head, tail = (p.x, p.a, p.b), (p.scale, p.offsets)
+    wide = torch.empty(p.S, 2 * p.K, dtype=BF16, device=DEV)
+    for kind, args, kw in (
+            (ValueError, (wide[:, :64], p.a, p.b, *tail), {}),                      # strided
+            (ValueError, (p.x.float(), p.a, p.b, *tail), {}),
+            (ValueError, (p.x, p.a[:, :, :56].contiguous(), p.b, *tail), {}),
+            (ValueError, (p.x, p.a, p.b[:1].contiguous(), *tail), {}),
+            (ValueError, (*head, p.scale[:1].contiguous(), p.offsets), {}),
+            (ValueError, (*head, p.scale, p.offsets.long()), {}),
+            (ValueError, (*head, p.scale, p.offsets[:1]), {}),
+            (ValueError, (*head, *tail), {"y": y, "dtype": F32, "out": y.float()}),
+            (ValueError, (*head, *tail), {"dtype": torch.float16}),
+            (ValueError, (*head, *tail), {"z": torch.empty(p.S, 16, device=DEV)}),
+            (e4b.E4BError, (*head, *tail), {"out": torch.empty(p.S * p.N + 1, device=DEV)[1:].view(p.S, p.N)}),
+            (e4b.E4BError, (p.x, torch.cat([p.a, p.a[:, :4]], 1), torch.cat([p.b, p.b[:, :, :4]], 2), *tail), {})):
+        with pytest.raises(kind):
+            e4b.e4b_grouped_lora(*args, **kw)
+    for kind, args, kw in (
+            (ValueError, (g.t(), p.x, z, p.a, p.b, *tail), {}),
+            (TypeError, (g, None, z, p.a, p.b, *tail), {}),
+            (TypeError, (g, p.x, None, p.a, p.b, *tail), {}),
+            (ValueError, (g, p.x, z, p.a, p.b, *tail), {"gx": False, "gx_base": p.x}),
+            (ValueError, (g, p.x, z, p.a, p.b, *tail), {"gx": p.x.float(), "gx_base": p.x}),
+            (ValueError, (g, p.x, z, p.a, p.b, *tail), {"ga": p.a}),
+            (e4b.E4BError, (g, p.x, z, p.a, p.b, *tail), {"gx": False, "ga": False, "gb": False}),
+            (e4b.E4BError, (g, p.x, z, p.a, p.b, *tail), {"ws": torch.empty(16, dtype=torch.uint8, device=DEV)})):
+        with pytest.raises(kind):
+            e4b.e4b_grouped_lora_backward(*args, **kw)
+
+
 def test_empty_batch_and_empty_groups(e4b):
     p = Problem(K=64, N=48, r=8, lengths=[0, 0, 0])
     assert p.S == 0

@@ -215,6 +215,31 @@ def test_empty_batch(e4b):
     assert g_rows.shape == (0, 8) and g_w.shape == (0, 2)
 
 
+def test_binding_refuses(e4b):
+    T, H, k = 6, 16, 2
+    x, slots, w = _rows(T, H, BF16, 1), _slots(T, k, 4, 2), _weights(T, k, 3)
+    rows = _rows(T * k, H, F32, 4)
+    for f in (lambda: e4b.e4b_permute_tokens(_rows(H, T, BF16, 1).t(), slots, k),  # strided
+              lambda: e4b.e4b_permute_tokens(x.half(), slots, k),
+              lambda: e4b.e4b_permute_tokens(x, slots.long(), k),
+              lambda: e4b.e4b_permute_tokens(x, slots, 3),
+              lambda: e4b.e4b_permute_tokens(x, slots, k, out=rows),
+              lambda: e4b.e4b_combine_tokens(rows, slots, 5, w),
+              lambda: e4b.e4b_combine_tokens(rows, slots, k, w.to(BF16)),
+              lambda: e4b.e4b_combine_tokens(rows, slots, k, w[:3]),
+              lambda: e4b.e4b_combine_tokens(rows, slots, k, w, dtype=torch.float16),
+              lambda: e4b.e4b_combine_tokens_backward(x, rows[:4], slots, k, w),
+              lambda: e4b.e4b_combine_tokens_backward(x, None, slots, k, w, g_w=w)):
+        with pytest.raises(ValueError):
+            f()
+    with pytest.raises(TypeError):
+        e4b.e4b_combine_tokens_backward(x, rows, slots, k, None)
+    for f in (lambda: e4b.e4b_permute_tokens(_rows(1, H, BF16, 1), torch.zeros(65, dtype=torch.int32, device=DEV), 65),
+              lambda: e4b.e4b_combine_tokens(torch.empty(T * k * H + 1, device=DEV)[1:].view(T * k, H), slots, k, w)):
+        with pytest.raises(e4b.E4BError):
+            f()
+
+
 def test_routed_layer_order(e4b):
     """permute and combine with the slots of e4b_route_permute: identity experts give each token
     back, weighted by weights that sum to one."""
