@@ -231,23 +231,33 @@ class _on_device:
     """Context of the calls below: the tensors' device made the current one (a launch goes to the
     current device) and, inside it, the stream of the call: the given one or the device's
     current one.  A torch stream of another device is refused."""
+    __slots__ = ("guard", "on")
+    alloc = staticmethod(torch.empty)  # on the device's current stream, where none is given
 
     def __init__(self, dev, stream):
-        if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
-        self.guard = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-        self.on = _on_stream(stream)
+        self.on = None
+        if stream is not None:
+            if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
+            self.on = _on_stream(stream)
+        self.guard = None if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
     def __enter__(self):
         if self.guard is not None:
             self.guard.__enter__()
-        return self.on.__enter__()
+        return self if self.on is None else self.on.__enter__()
 
     def __exit__(self, *exc):
-        self.on.__exit__(*exc)
+        if self.on is not None:
+            self.on.__exit__(*exc)
         if self.guard is not None:
             self.guard.__exit__(*exc)
         return False
+
+
+def _stream_on(dev, stream):
+    """_stream for tensors on `dev`."""
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else _stream(stream)
 
 
 def _rows_dtype(dtype, name):
@@ -741,7 +751,7 @@ def e4b_permute_tokens(x, sorted_slots, k: int, out=None, ws=None, stream=None):
         need = e4b_permute_workspace_bytes(T, H, k, x.dtype) if ws is None else 0
         ws, wp, wn = _small_ws(st, ws, need, dev)
         _check("e4b_permute_tokens", _c_permute(x.data_ptr(), dt, T, H, k, sorted_slots.data_ptr(), out.data_ptr(),
-                                                wp, wn, _stream(stream)))
+                                                wp, wn, _stream_on(dev, stream)))
     return out
 
 
@@ -777,7 +787,7 @@ def e4b_combine_tokens(rows, sorted_slots, k: int, topk_w=None, out=None, dtype=
         ws, wp, wn = _small_ws(st, ws, e4b_combine_workspace_bytes(T, k) if ws is None else 0, dev)
         _check("e4b_combine_tokens", _c_combine(
             rows.data_ptr(), rdt, T, H, k, sorted_slots.data_ptr(), None if topk_w is None else topk_w.data_ptr(),
-            out.data_ptr(), odt, wp, wn, _stream(stream)))
+            out.data_ptr(), odt, wp, wn, _stream_on(dev, stream)))
     return out
 
 
@@ -809,7 +819,7 @@ def e4b_combine_tokens_backward(g_out, rows, sorted_slots, k: int, topk_w, g_row
         _check("e4b_combine_tokens_backward", _c_combine_bwd(
             g_out.data_ptr(), gdt, None if rows is None else rows.data_ptr(), rdt, T, H, k,
             sorted_slots.data_ptr(), topk_w.data_ptr(), g_rows.data_ptr(), ddt,
-            None if g_w is None else g_w.data_ptr(), wp, wn, _stream(stream)))
+            None if g_w is None else g_w.data_ptr(), wp, wn, _stream_on(dev, stream)))
     return g_rows, g_w
 
 
@@ -902,7 +912,7 @@ def e4b_grouped_lora(x, a, b, scale, group_offsets, group_adapter=None, y=None, 
         args.x, args.out = x.data_ptr(), out.data_ptr()
         need = _ws_of(_c_lora_ws, "e4b_lora_workspace_bytes", args) if ws is None else 0
         ws = _give_ws(st, ws, need, args, dev)
-        _check("e4b_grouped_lora", _c_lora(ctypes.byref(args), _stream(stream)))
+        _check("e4b_grouped_lora", _c_lora(ctypes.byref(args), _stream_on(dev, stream)))
     return out, z
 
 
@@ -970,5 +980,5 @@ def e4b_grouped_lora_backward(g, x, z, a, b, scale, group_offsets, group_adapter
         args.g = g.data_ptr()
         need = _ws_of(_c_lora_bwd_ws, "e4b_lora_backward_workspace_bytes", args) if ws is None else 0
         ws = _give_ws(st, ws, need, args, dev)
-        _check("e4b_grouped_lora_backward", _c_lora_bwd(ctypes.byref(args), _stream(stream)))
+        _check("e4b_grouped_lora_backward", _c_lora_bwd(ctypes.byref(args), _stream_on(dev, stream)))
     return tuple(outs)
