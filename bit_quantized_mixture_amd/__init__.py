@@ -797,7 +797,7 @@ def e4b_combine_tokens_backward(g_out, rows, sorted_slots, k: int, topk_w, g_row
 
     g_out [T, H] bf16 or float32; rows, sorted_slots, topk_w as given to the forward call.  g_rows
     is of `dtype` (or the dtype of `g_rows` where that is given).  rows=None: the router is frozen,
-    g_w is not computed and None is returned for it.
+    g_w is not computed and None is returned for it.  A row that names no slot is not written.
     """
     gdt = _need_rows(g_out, "g_out")
     T, H = g_out.shape

@@ -183,7 +183,9 @@ struct ShrinkArgs {
 };
 
 // A workgroup: up to 16 * RB rows of a group and one piece of the columns; its waves'
-// sums meet in LDS.
+// sums meet in LDS.  Bound: HBM, by x: 8192 rows of 14336 at rank 16 (239 MB) take 49 us, 4.9 TB/s.
+// 5003 rows of 2880 at rank 64 (29 MB) take 13 us, most of it the round of latencies of a workgroup
+// that has three units a wave.
 template <int RB, int RT>
 __global__ void __launch_bounds__(kThreads) shrink_kernel(ShrinkArgs p) {
   // the waves' units, and after them the waves' sums
@@ -392,7 +394,10 @@ struct ExpandArgs {
   int per;                // column steps of a chunk
 };
 
-// A workgroup: up to 16 * RB rows of a group and one piece of the columns.
+// A workgroup: up to 16 * RB rows of a group and one piece of the columns.  Bound: HBM, by the rows
+// read and written: 8192 rows of 4096 float32 at rank 16 (270 MB) take 50 us, 5.3 TB/s; 5003 bf16 rows
+// of 2880 at rank 64 (60 MB) 21 us, where the z of a tile and its three parts (made by each workgroup
+// before its first product) are a third.
 template <int RB, int RP, int ODT>
 __global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs p) {
   typedef Expand<RP, ODT> X;
@@ -470,7 +475,9 @@ constexpr int fused_waves(int rp) { return rp <= 32 ? 16 : 8; }
 
 // Both products in one launch for tiles of at most 16 rows (decoded tokens): every workgroup of a
 // tile computes the tile's z for itself, from the adapter's A in the L2 cache, instead of waiting
-// for another launch to do it.
+// for another launch to do it.  Bound: the chain of latencies (offsets, x and A, the waves' sums, B
+// and y): one token at [14336, 4096] and rank 16 takes 8 us, 64 of 48 adapters (36 MB) 15 us, 512 rows
+// of 128 adapters at [1536, 2048] (23 MB) 10.5 us.
 template <int RP, int ODT>
 __global__ void __launch_bounds__(fused_waves(RP) * kWave) fused_kernel(FusedArgs p) {
   typedef Expand<RP, ODT> X;
@@ -625,8 +632,11 @@ __device__ __forceinline__ s16x4 lds_read_tr(const uint8_t* at) {
 // loads in flight) into LDS.  grad: a wave has 64 of the block's columns; the contraction runs over
 // the rows, so m is read transposed, and v stands in LDS transposed in its three parts.  u: a wave
 // has 16 of the block's rows and all its columns; B stands in LDS transposed.
-// Bound: HBM.  One pass instead of two (u on its own, grad on its own) reads m once: the gradients
-// of the 8-expert gate_up adapters took 387 us in separate passes over float32 matrix instructions.
+// Bound: HBM in long groups: g of 8192 rows of 28672 at rank 16 (470 MB) takes 116 us, 4.1 TB/s (4.3
+// with u's partial sums).  32 groups of 128 .. 384 rows of 2880 at rank 32 (47 MB) take 26 us: one
+// round of workgroups that ends with the longest group, four or five blocks one after the other.
+// One pass instead of two reads m once: 8192 rows of 28672 took 387 us for all gradients with a pass
+// each for u and grad (and float32 matrix instructions), 191 so.
 template <int RT, int NSUB, bool UP, bool BYCOL>
 __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
   constexpr int kVStride = kGradRows + 8;               // v^T row in bf16
@@ -861,7 +871,8 @@ struct ReduceArgs {
 constexpr int kReduceTurns = 8, kReduceLen = 4 * kThreads * kReduceTurns;
 
 // grad[a] = the sum of the parts of a's groups in order (0 without rows); a group of one tile
-// under ids == NULL has written its adapter's gradient itself.
+// under ids == NULL has written its adapter's gradient itself.  Bound: the launch behind the passes'
+// writes; both gradients in one launch take 5.5 us at 8 adapters of rank 16, [28672, 4096].
 __global__ void __launch_bounds__(kThreads) grad_reduce_kernel(ReduceArgs p) {
   const int lane = threadIdx.x & (kWave - 1);
   const bool second = blockIdx.x >= p.first;
@@ -915,7 +926,8 @@ __global__ void __launch_bounds__(kThreads) grad_reduce_kernel(ReduceArgs p) {
 // Between the gradient pass and what uses u: u[p] = the sum of its chunks in a fixed order (16 lanes
 // have 4 ranks each, the wave's four groups of 16 a quarter of the chunks each; rows of no adapter
 // hold garbage here and there, and nothing reads them), and A^T [n, K, r] for the expand (a thread
-// has 8 ranks of 8 columns).
+// has 8 ranks of 8 columns).  Bound: the launch and one round of loads behind the pass's writes: 8 us
+// for 56 chunks of 8192 rows at rank 16 (29 MB), 9 for 12 chunks at rank 32 and 6 MB of A.
 struct BetweenArgs {
   const float* upart;     // [chunks, S, r]
   float* u;               // [S, r]
@@ -983,7 +995,9 @@ int log2_up(int64_t v) {
 }
 
 // Rows of a shrink or expand tile: 16 where groups average no more (decoded tokens), else 64, or
-// 32 at ranks over 64, whose parts fill the registers.
+// 32 at ranks over 64, whose parts fill the registers.  64 groups at [2048, 2048], rank 64, us with
+// 16-row and with 64-row tiles: 14 rows a group 16.4 and 19.6, 20 rows 22.7 and 21.4; 32 groups at
+// [4096, 4096], rank 16: 14 rows 11.7 and 12.4, 20 rows 13.9 and 13.4, 32 rows 17.6 and 15.1.
 int row_tile_log2(int64_t S, int64_t G, int r) { return S <= 16 * G ? 4 : (r > 64 ? 5 : 6); }
 
 // Rows of a shrink tile: 32 from rank 33 on, where the sums and fragments of 64 rows leave room for
@@ -994,7 +1008,8 @@ int shrink_tile_log2(const LoraGroups& q) {
 }
 
 // Pieces the columns of a shrink are cut into: as many workgroups as are resident together (three on
-// every CU), no piece under 512 columns (two units for each wave).
+// every CU; 24 prompts of rank 64: 31 us a call, 37 with a third more), no piece under 512 columns
+// (two units for each wave).
 int shrink_pieces(const LoraGroups& q, int64_t C) {
   const int64_t tiles = tiles_bound(q.S, q.G, shrink_tile_log2(q));
   const int64_t want = 768 / (tiles > 0 ? tiles : 1), most = C / 512;
@@ -1007,7 +1022,9 @@ int shrink_pieces(const LoraGroups& q, int64_t C) {
 int grad_subs(int r, bool up) { return up && r <= 16 ? 2 : 1; }
 
 // Rows of a gradient tile at most: as many tiles as fill two workgroups on every CU (a tile costs a
-// float32 write and read of its [r, C] sums).
+// float32 write and read of its [r, C] sums).  Gradients of 32 experts at [2880, 2880] and of 8 at
+// [28672, 4096]: 96 and 191 us; with half as many tiles again 111 and 198, with three quarters as many
+// 95 and 193.
 int grad_rows(const LoraGroups& q, int64_t C, bool up) {
   const int64_t chunks = div_up(C, kGradCols * grad_subs(q.r, up));
   const int64_t used = q.G < q.S ? q.G : q.S;
@@ -1176,7 +1193,9 @@ BackwardLayout backward_layout(const LoraBackwardLaunch& L) {
 }  // namespace
 
 // Whether the forward call runs as one launch: tiles of at most 16 rows, and an A that a CU reads
-// from the L2 cache in a few microseconds, about what the second launch would cost.
+// from the L2 cache in a few microseconds, about what the second launch would cost.  us in one launch
+// and in two: 64 tokens of 48 adapters at r K = 65536 15.2 and 24.4, at 131072 21.7 and 26.8, at 262144
+// 23.8 and 16.7 (one token: 8.0 and 7.4, where a second launch costs the host 3; 13.1 and 8.2).
 bool lora_fused(const LoraGroups& q) {
   return row_tile_log2(q.S, q.G, q.r) == 4 && q.r <= 64 && int64_t(q.r) * q.K <= (1 << 17);
 }

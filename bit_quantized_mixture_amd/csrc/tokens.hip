@@ -17,7 +17,8 @@ namespace {
 constexpr int kThreads = 256;
 // Up to this many slots a kernel that needs inv finds its tokens' rows by reading sorted_slots
 // itself (16 KB from the L2 cache for each workgroup, all loads in flight); beyond, one small launch
-// or two write inv to the workspace.
+// or two write inv to the workspace.  Combine of float32 rows of 2048, us itself and behind a launch:
+// 1024 slots 4.4 and 7.5, 4096 slots 9.2 and 10.0, 6400 slots 18.9 and 15.5.
 constexpr int64_t kScanSlots = 4096;
 
 __global__ void __launch_bounds__(kThreads) fill_inv_kernel(int32_t* __restrict__ inv, int64_t S) {
@@ -87,7 +88,7 @@ __device__ __forceinline__ void scan_slots(const int32_t* __restrict__ slots, in
 }
 
 // rows[p] = x[slots[p] / k]; `halves` 2-byte units a row, moved as they are.  A slot outside
-// [0, S) leaves a row of zeros.
+// [0, S) leaves a row of zeros.  67 MB of rows take 21 us.
 __global__ void __launch_bounds__(kThreads) permute_kernel(const uint16_t* __restrict__ x,
                                                            const int32_t* __restrict__ slots, int64_t S,
                                                            int64_t halves, int k, int team_log2,
@@ -120,8 +121,8 @@ __global__ void __launch_bounds__(kThreads) permute_kernel(const uint16_t* __res
 
 // The same in token order: a team item is up to 512 columns of one token, read once and written to
 // the k rows of its slots.  The gather above reads each x row k times (from the memory-side cache,
-// beside the stream of rows): 1.07 GB of rows took 310 us against 232 here, with stores that are not
-// kept in the caches.  Behind the items, workgroups look for rows that inv does not lead to (a slot
+// beside the stream of rows): 1.07 GB of rows took 310 us against 233 a call here, with stores that are
+// not kept in the caches; 225 of them in this kernel, 5.4 TB/s.  Behind the items, workgroups look for rows that inv does not lead to (a slot
 // out of range: zeros; a slot that a higher row names too) and write them by themselves.
 __global__ void __launch_bounds__(kThreads) permute_scatter_kernel(const uint16_t* __restrict__ x,
                                                                    const int32_t* __restrict__ slots,
@@ -173,7 +174,8 @@ __global__ void __launch_bounds__(kThreads) permute_scatter_kernel(const uint16_
 }
 
 // One team item: V columns a lane of one token.  The loads of eight rows go out before the first
-// is used.
+// is used.  131072 float32 rows of 4096 (2.28 GB) take 364 us, 6.3 TB/s; 12297 bf16 rows of 2880 into
+// float32 (118 MB) 24 us, 4.9 TB/s; one token's eight rows of 2048 3.5 us, a chain of latencies.
 template <int RDT, int ODT, int V, bool SCAN, bool ONCE>
 __global__ void __launch_bounds__(kThreads) combine_rows_kernel(const row_elem<RDT>* __restrict__ rows,
                                                                 const float* __restrict__ w,
@@ -244,7 +246,8 @@ __global__ void __launch_bounds__(kThreads) combine_rows_kernel(const row_elem<R
 }
 
 // A team for each slot s = t*k + j: reads g_out[t] (the k teams of a token share it in the
-// caches), writes its row's gradient, and sums the weight's gradient over the row.
+// caches), writes its row's gradient, and sums the weight's gradient over the row.  8192 float32 rows
+// of 2880 with bf16 gradients (153 MB) take 32 us, 4.8 TB/s.
 template <int GDT, int RDT, int DDT, bool SCAN, bool GW, bool ONCE>
 __global__ void __launch_bounds__(kThreads) combine_backward_kernel(
     const row_elem<GDT>* __restrict__ g_out, const row_elem<RDT>* __restrict__ rows,

@@ -19,8 +19,11 @@
  * and scaled per block, products accumulate in fp32, and only the final output is
  * rounded to bf16 (grouped-nf4-gemm 0.25.0 project description, opening section).  No
  * dequantised copy of a weight is ever written.  Beside the forward: the input gradient of
- * the grouped product on the same packed stacks (e4b_grouped_dgrad), and an int4-b32
- * routed decode GEMV with exact integer block sums (e4b_pack_int4_b32, e4b_gemv_int4_b32).
+ * the grouped product on the same packed stacks (e4b_grouped_dgrad), an int4-b32
+ * routed decode GEMV with exact integer block sums (e4b_pack_int4_b32, e4b_gemv_int4_b32),
+ * token rows to expert order and back with their gradients (e4b_permute_tokens,
+ * e4b_combine_tokens, e4b_combine_tokens_backward), and low-rank adapters on grouped rows with
+ * theirs (e4b_grouped_lora, e4b_grouped_lora_backward).
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are DEVICE pointers, owned by the caller, row-major and dense.
@@ -195,7 +198,8 @@ int e4b_permute_workspace_bytes(int32_t dtype, int64_t T, int64_t H, int32_t k, 
  *   sorted_slots  [T*k] int32 from e4b_route_permute: a permutation of 0 .. T*k - 1.
  *   rows          [T*k, H] of `dtype` out: bit copies.
  *   ws            device workspace of at least e4b_permute_workspace_bytes().
- * A slot outside [0, T*k) leaves a row of zeros.  The gradient of x is e4b_combine_tokens of the
+ * A slot outside [0, T*k) leaves a row of zeros.  No output overlaps an input, here and in the
+ * two calls below.  The gradient of x is e4b_combine_tokens of the
  * rows' gradients with topk_w = NULL.
  */
 int e4b_permute_tokens(const void* x, int32_t dtype, int64_t T, int64_t H, int32_t k,
@@ -226,7 +230,7 @@ int e4b_combine_tokens(const void* rows, int32_t rows_dtype, int64_t T, int64_t 
  *   g_rows  [T*k, H] of g_rows_dtype out (bf16 is what e4b_grouped_dgrad takes).
  *   g_w     [T, k] float32 out, or NULL (frozen router; rows may then be NULL).
  * Sums are float32 in a fixed order.  A slot that no row names gets g_w = 0; a row that names no
- * slot is left as it was.
+ * slot, or one that a higher row names too, is left as it was.
  */
 int e4b_combine_tokens_backward(const void* g_out, int32_t g_dtype, const void* rows, int32_t rows_dtype,
                                 int64_t T, int64_t H, int32_t k, const int32_t* sorted_slots,
@@ -456,7 +460,10 @@ int e4b_lora_backward_workspace_bytes(const e4b_lora_backward_args* a, size_t* b
  * the sums over the rows of every group that uses adapter a (0 for an adapter without rows).
  * Rows of a group without an adapter get gx = gx_base; rows outside every group are left as they
  * were.  Float32 sums in a fixed order: deterministic.  ga and gb are overwritten.  At least one
- * of gx, ga, gb is given.  Synchronous errors as e4b_moe_forward.
+ * of gx, ga, gb is given.  A and B are finite; a NaN or infinity in a row of g, x or z may reach
+ * that row of gx and the gradients of its adapter (as NaN where the exact value is infinite), and
+ * nothing else.  Apart from gx_base == gx the outputs and the workspace overlap no other argument.
+ * Synchronous errors as e4b_moe_forward.
  */
 int e4b_grouped_lora_backward(const e4b_lora_backward_args* a, void* stream);
 
