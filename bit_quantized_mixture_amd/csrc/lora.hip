@@ -123,8 +123,10 @@ __device__ __forceinline__ void shrink_sums(uint8_t* lds, const uint16_t* __rest
   const uint32_t lane_off = lrow * C * 2u + 16u * lpiece, step = 16u * C;  // bytes of 8 rows
   constexpr int kM = 2 * RB, kLoads = 2 * (RB + RT);
   uint8_t* own = lds + wave * (RB + RT) * kUnitBytes;
-  auto load = [&](int s, u32x4 (&v)[kLoads]) {  // past the columns: zeros; past the rows of m and w too
-    const uint32_t off = 64u * s + 8u * lpiece < C ? lane_off : kNowhere;
+  const int share = (end - first + waves - 1) / waves, from = first + wave * share;
+  const int to = from + share < end ? from + share : end;
+  auto load = [&](int s, u32x4 (&v)[kLoads]) {  // past the share and the columns: zeros; past the rows of m and w too
+    const uint32_t off = s < to && 64u * s + 8u * lpiece < C ? lane_off : kNowhere;
 #pragma unroll
     for (int j = 0; j < kLoads; ++j)
       v[j] = j < kM ? buf_load(mres, off, 128u * s + j * step) : buf_load(wres, off, 128u * s + (j - kM) * step);
@@ -148,16 +150,16 @@ __device__ __forceinline__ void shrink_sums(uint8_t* lds, const uint16_t* __rest
         for (int k = 0; k < RT; ++k)
           acc[b][k] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(f[u][RB + k], f[u][b], acc[b][k], 0, 0, 0);
   };
-  const int share = (end - first + waves - 1) / waves, from = first + wave * share;
-  const int to = from + share < end ? from + share : end;
   u32x4 v[AHEAD][kLoads];
 #pragma unroll
   for (int i = 0; i < AHEAD; ++i) load(from + i, v[i]);
   for (int s = from; s < to; s += AHEAD) {
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i)
-      if (i == 0 || s + i < to)  // loads past the share are not used
-        multiply(v[i], [&] { load(s + i + AHEAD, v[i]); });
+      if (i == 0 || s + i < to)
+        multiply(v[i], [&] {
+          if (s + i + AHEAD < to) load(s + i + AHEAD, v[i]);
+        });
   }
 }
 
@@ -447,7 +449,8 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs p) {
   for (int s = chunk * p.per + wave; s < end; s += kAhead * kWaves) {
     typename X::template Step<RB> st[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) rows.load(s + i * kWaves, st[i]);
+    for (int i = 0; i < kAhead; ++i)
+      if (i == 0 || s + i * kWaves < end) rows.load(s + i * kWaves, st[i]);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i)
       if (i == 0 || s + i * kWaves < end) rows.finish(s + i * kWaves, st[i], zf);
@@ -501,11 +504,11 @@ __global__ void __launch_bounds__(fused_waves(RP) * kWave) fused_kernel(FusedArg
   const typename X::template Rows<1> rows(y ? y + t.row0 * p.N : nullptr,
                                           static_cast<typename X::out_t*>(p.out) + t.row0 * p.N,
                                           p.b + int64_t(a < 0 ? 0 : a) * p.N * p.r, uint32_t(p.N), p.r, t.rows, a >= 0);
-  constexpr int kAhead = 1;  // 128 registers a lane
   int s = chunk * p.per + wave;
-  typename X::template Step<1> st[kAhead];  // the first steps' loads go out before z is computed
-#pragma unroll
-  for (int i = 0; i < kAhead; ++i) rows.load(s + i * kFusedWaves, st[i]);
+  // The first step's loads go out before z is computed (two steps' made 64 tokens no faster, 15.3 us,
+  // and one token slower, 10.0 us instead of 8.0).
+  typename X::template Step<1> st;
+  if (s < end) rows.load(s, st);
   f32x4 acc[1][RT];
   zero_sums(acc);
   if (a >= 0) {
@@ -530,13 +533,9 @@ __global__ void __launch_bounds__(fused_waves(RP) * kWave) fused_kernel(FusedArg
   bf16x8 zf[1][X::kSteps];
   X::template fragments<1>(zs, zf);
   while (s < end) {
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i)
-      if (s + i * kFusedWaves < end) rows.finish(s + i * kFusedWaves, st[i], zf);
-    s += kAhead * kFusedWaves;
-    if (s >= end) break;
-#pragma unroll
-    for (int i = 0; i < kAhead; ++i) rows.load(s + i * kFusedWaves, st[i]);
+    rows.finish(s, st, zf);
+    s += kFusedWaves;
+    if (s < end) rows.load(s, st);
   }
 }
 
