@@ -26,7 +26,7 @@ constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
 
 struct RowTile {
-  int group;
+  int adapter;     // -1: none
   int64_t row0;
   int rows;        // 1 .. bm; 0: no such tile
 };
@@ -50,15 +50,23 @@ __device__ __forceinline__ void group_rows(const int32_t* __restrict__ offsets, 
   *hi = b < *lo ? *lo : (b > S ? S : b);
 }
 
+__device__ __forceinline__ int adapter_of(const int32_t* __restrict__ ids, int group, int n) {
+  const int a = ids ? ids[group] : group;
+  return a >= 0 && a < n ? a : -1;
+}
+
 // Tile `tile` of the list that cuts every group into pieces of 1 << bm_log2 rows, found by each
-// wave from the offsets, 64 groups a step.
-__device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offsets, int G, int S, int bm_log2,
-                                             uint32_t tile) {
+// wave from the offsets, 64 groups a step (their adapters are read beside them: one latency, not two).
+__device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offsets, const int32_t* __restrict__ ids,
+                                             int n_adapters, int G, int S, int bm_log2, uint32_t tile) {
   const int lane = threadIdx.x & (kWave - 1);
   int base = 0;
   for (int g0 = 0; g0 < G; g0 += kWave) {
-    int lo = 0, hi = 0;
-    if (g0 + lane < G) group_rows(offsets, g0 + lane, S, &lo, &hi);
+    int lo = 0, hi = 0, a = -1;
+    if (g0 + lane < G) {
+      group_rows(offsets, g0 + lane, S, &lo, &hi);
+      a = adapter_of(ids, g0 + lane, n_adapters);
+    }
     const int n = int((int64_t(hi) - lo + (1 << bm_log2) - 1) >> bm_log2);
     const int ni = wave_scan(n);
     const int total = __builtin_amdgcn_readlane(ni, kWave - 1);
@@ -68,16 +76,11 @@ __device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offsets
       if (at < 0 || at >= __builtin_amdgcn_readlane(n, l)) break;  // sums of offsets that descend can wrap
       const int row0 = __builtin_amdgcn_readlane(lo, l) + (at << bm_log2);
       const int left = __builtin_amdgcn_readlane(hi, l) - row0;
-      return RowTile{g0 + l, row0, left < (1 << bm_log2) ? left : (1 << bm_log2)};
+      return RowTile{__builtin_amdgcn_readlane(a, l), row0, left < (1 << bm_log2) ? left : (1 << bm_log2)};
     }
     base += total;
   }
-  return RowTile{0, 0, 0};
-}
-
-__device__ __forceinline__ int adapter_of(const int32_t* __restrict__ ids, int group, int n) {
-  const int a = ids ? ids[group] : group;
-  return a >= 0 && a < n ? a : -1;
+  return RowTile{-1, 0, 0};
 }
 
 // Loads and stores go through buffers that end with the tile's rows or the adapter's matrix: a
@@ -198,9 +201,9 @@ __global__ void __launch_bounds__(kThreads) shrink_kernel(ShrinkArgs p) {
   const int c = lane & 15, q = lane >> 4;
   const uint32_t tile = blockIdx.x / p.ksplit;
   const int ks = int(blockIdx.x - tile * p.ksplit);
-  const RowTile t = find_tile(p.offsets, p.G, p.S, p.bm_log2, tile);
+  const RowTile t = find_tile(p.offsets, p.ids, p.n, p.G, p.S, p.bm_log2, tile);
   if (t.rows == 0) return;
-  const int a = adapter_of(p.ids, t.group, p.n);
+  const int a = t.adapter;
   f32x4 acc[RB][RT];
   zero_sums(acc);
   if (a >= 0) {
@@ -406,9 +409,9 @@ __global__ void __launch_bounds__(kThreads) expand_kernel(ExpandArgs p) {
   __shared__ __attribute__((aligned(16))) uint16_t zs[16 * RB * X::kStride];
   const uint32_t tile = blockIdx.x / p.chunks;
   const int chunk = int(blockIdx.x - tile * p.chunks);
-  const RowTile t = find_tile(p.offsets, p.G, p.S, p.bm_log2, tile);
+  const RowTile t = find_tile(p.offsets, p.ids, p.n, p.G, p.S, p.bm_log2, tile);
   if (t.rows == 0) return;
-  const int a = adapter_of(p.ids, t.group, p.n);
+  const int a = t.adapter;
   const bool z_out = p.z_out && chunk == 0;
   if (a < 0 && p.base == p.out && !z_out) return;  // these rows stay as they are
 
@@ -492,9 +495,9 @@ __global__ void __launch_bounds__(fused_waves(RP) * kWave) fused_kernel(FusedArg
   const int lane = threadIdx.x & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t tile = blockIdx.x / p.chunks;
   const int chunk = int(blockIdx.x - tile * p.chunks);
-  const RowTile t = find_tile(p.offsets, p.G, p.S, 4, tile);
+  const RowTile t = find_tile(p.offsets, p.ids, p.n, p.G, p.S, 4, tile);
   if (t.rows == 0) return;
-  const int a = adapter_of(p.ids, t.group, p.n);
+  const int a = t.adapter;
   const bool z_out = p.z && chunk == 0;
   if (a < 0 && p.y == p.out && !z_out) return;
   const float sc = a >= 0 && p.scale ? p.scale[a] : 1.f;
@@ -542,7 +545,7 @@ __global__ void __launch_bounds__(fused_waves(RP) * kWave) fused_kernel(FusedArg
 // A tile of the gradient pass: group g's rows cut evenly into ceil(rows / most) pieces of a multiple
 // of 64 rows (the last ones may hold fewer, or none).
 struct GradTile {
-  int group, row0, rows;
+  int adapter, row0, rows;
   int kept;        // index among the tiles that write parts; -1: the group's only tile
   bool valid;
 };
@@ -552,13 +555,17 @@ __device__ __forceinline__ int grad_tiles(int rows, int most) {
 }
 
 // As find_tile.  `single`: a group of one tile is not counted among the kept ones.
-__device__ __forceinline__ GradTile find_grad_tile(const int32_t* __restrict__ offsets, int G, int S, int most,
-                                                   uint32_t tile, bool single) {
+__device__ __forceinline__ GradTile find_grad_tile(const int32_t* __restrict__ offsets, const int32_t* __restrict__ ids,
+                                                   int n_adapters, int G, int S, int most, uint32_t tile,
+                                                   bool single) {
   const int lane = threadIdx.x & (kWave - 1);
   int base = 0, kbase = 0;
   for (int g0 = 0; g0 < G; g0 += kWave) {
-    int lo = 0, hi = 0;
-    if (g0 + lane < G) group_rows(offsets, g0 + lane, S, &lo, &hi);
+    int lo = 0, hi = 0, a = -1;
+    if (g0 + lane < G) {
+      group_rows(offsets, g0 + lane, S, &lo, &hi);
+      a = adapter_of(ids, g0 + lane, n_adapters);
+    }
     const int n = grad_tiles(hi - lo, most);
     const int k = single && n == 1 ? 0 : n;
     const int ni = wave_scan(n), ki = wave_scan(k);
@@ -572,7 +579,7 @@ __device__ __forceinline__ GradTile find_grad_tile(const int32_t* __restrict__ o
       const int per = (grad_tiles(rows, nl) + 63) & ~63;
       const int64_t first = int64_t(at) * per;
       GradTile t;
-      t.group = g0 + l;
+      t.adapter = __builtin_amdgcn_readlane(a, l);
       t.rows = int(rows - first < 0 ? 0 : (rows - first < per ? rows - first : per));
       t.row0 = lol + (t.rows > 0 ? int(first) : 0);
       t.kept = single && nl == 1 ? -1 : kbase + __builtin_amdgcn_readlane(ki - k, l) + at;
@@ -582,7 +589,7 @@ __device__ __forceinline__ GradTile find_grad_tile(const int32_t* __restrict__ o
     base += total;
     kbase += __builtin_amdgcn_readlane(ki, kWave - 1);
   }
-  return GradTile{0, 0, 0, 0, false};
+  return GradTile{-1, 0, 0, 0, false};
 }
 
 struct GradArgs {
@@ -649,9 +656,9 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
   const int c = lane & 15, q = lane >> 4;
   const uint32_t tile = blockIdx.x / p.chunks;
   const int chunk = int(blockIdx.x - tile * p.chunks);
-  const GradTile t = find_grad_tile(p.offsets, p.G, p.S, p.most, tile, p.ids == nullptr);
+  const GradTile t = find_grad_tile(p.offsets, p.ids, p.n, p.G, p.S, p.most, tile, p.ids == nullptr);
   if (!t.valid) return;
-  const int a = adapter_of(p.ids, t.group, p.n);
+  const int a = t.adapter;
   if (a < 0) return;
   const uint32_t col0 = uint32_t(chunk) * kWCols;
   const bool grad = p.grad != nullptr;
