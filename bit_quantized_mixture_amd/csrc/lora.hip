@@ -188,8 +188,8 @@ struct ShrinkArgs {
 };
 
 // A workgroup: up to 16 * RB rows of a group and one piece of the columns; its waves'
-// sums meet in LDS.  Bound: HBM, by x: 8192 rows of 14336 at rank 16 (239 MB) take 49 us, 4.9 TB/s.
-// 5003 rows of 2880 at rank 64 (29 MB) take 13 us, most of it the round of latencies of a workgroup
+// sums meet in LDS.  Bound: HBM, by x: 8192 rows of 14336 at rank 16 (239 MB) take 48 us, 5.0 TB/s.
+// 5003 rows of 2880 at rank 64 (29 MB) take 12 us, most of it the round of latencies of a workgroup
 // that has three units a wave.
 template <int RB, int RT>
 __global__ void __launch_bounds__(kThreads) shrink_kernel(ShrinkArgs p) {
@@ -400,7 +400,7 @@ struct ExpandArgs {
 };
 
 // A workgroup: up to 16 * RB rows of a group and one piece of the columns.  Bound: HBM, by the rows
-// read and written: 8192 rows of 4096 float32 at rank 16 (270 MB) take 50 us, 5.3 TB/s; 5003 bf16 rows
+// read and written: 8192 rows of 4096 float32 at rank 16 (270 MB) take 51 us, 5.3 TB/s; 5003 bf16 rows
 // of 2880 at rank 64 (60 MB) 21 us, where the z of a tile and its three parts (made by each workgroup
 // before its first product) are a third.
 template <int RB, int RP, int ODT>
@@ -482,8 +482,8 @@ constexpr int fused_waves(int rp) { return rp <= 32 ? 16 : 8; }
 // Both products in one launch for tiles of at most 16 rows (decoded tokens): every workgroup of a
 // tile computes the tile's z for itself, from the adapter's A in the L2 cache, instead of waiting
 // for another launch to do it.  Bound: the chain of latencies (offsets, x and A, the waves' sums, B
-// and y): one token at [14336, 4096] and rank 16 takes 8 us, 64 of 48 adapters (36 MB) 15 us, 512 rows
-// of 128 adapters at [1536, 2048] (23 MB) 10.5 us.
+// and y): one token at [14336, 4096] and rank 16 takes 7.5 us, 64 of 48 adapters (36 MB) 14.8 us, 512
+// rows of 128 adapters at [1536, 2048] (23 MB) 9.6 us.
 template <int RP, int ODT>
 __global__ void __launch_bounds__(fused_waves(RP) * kWave) fused_kernel(FusedArgs p) {
   typedef Expand<RP, ODT> X;
@@ -508,8 +508,8 @@ __global__ void __launch_bounds__(fused_waves(RP) * kWave) fused_kernel(FusedArg
                                           static_cast<typename X::out_t*>(p.out) + t.row0 * p.N,
                                           p.b + int64_t(a < 0 ? 0 : a) * p.N * p.r, uint32_t(p.N), p.r, t.rows, a >= 0);
   int s = chunk * p.per + wave;
-  // The first step's loads go out before z is computed (two steps' made 64 tokens no faster, 15.3 us,
-  // and one token slower, 10.0 us instead of 8.0).
+  // The first step's loads go out before z is computed (two steps' made 64 tokens no faster, 15.3 us
+  // and 15.4, and one token slower, 10.0 us and 8.0).
   typename X::template Step<1> st;
   if (s < end) rows.load(s, st);
   f32x4 acc[1][RT];
@@ -1200,8 +1200,8 @@ BackwardLayout backward_layout(const LoraBackwardLaunch& L) {
 
 // Whether the forward call runs as one launch: tiles of at most 16 rows, and an A that a CU reads
 // from the L2 cache in a few microseconds, about what the second launch would cost.  us in one launch
-// and in two: 64 tokens of 48 adapters at r K = 65536 15.2 and 24.4, at 131072 21.7 and 26.8, at 262144
-// 23.8 and 16.7 (one token: 8.0 and 7.4, where a second launch costs the host 3; 13.1 and 8.2).
+// and in two: 64 tokens of 48 adapters at r K = 65536 14.8 and 20.7, at 131072 20.7 and 24.1, at 262144
+// 22.6 and 15.9 (one token: 7.5 and 6.9, where a second launch costs the host 3; 12.5 and 8.2).
 bool lora_fused(const LoraGroups& q) {
   return row_tile_log2(q.S, q.G, q.r) == 4 && q.r <= 64 && int64_t(q.r) * q.K <= (1 << 17);
 }
