@@ -235,11 +235,15 @@ int check_tokens(int64_t T, int64_t H, int32_t k) {
   if (k > 64) return E4B_ERR_SHAPE;
   const int64_t lim = int64_t(1) << 31;
   if (T >= lim || T * k >= lim || H >= lim) return E4B_ERR_OVERFLOW;
-  // byte offsets are 64-bit; the row blocks have to fit a grid
-  if (T * k > (int64_t(1) << 50) / H || e4b::combine_blocks(T, H, k) >= lim ||
-      e4b::permute_blocks(T, 2 * H, k) >= lim || e4b::permute_blocks(T, H, k) >= lim)
-    return E4B_ERR_OVERFLOW;
-  return E4B_OK;
+  // byte offsets are 64-bit
+  return T * k > (int64_t(1) << 50) / H ? E4B_ERR_OVERFLOW : E4B_OK;
+}
+// The work items of a call's largest launch have to fit a grid.
+int check_items(int64_t items) { return items >= e4b::kLaunchItems ? E4B_ERR_OVERFLOW : E4B_OK; }
+
+int check_permute(int32_t dtype, int64_t T, int64_t H, int32_t k) {
+  const int st = check_tokens(T, H, k);
+  return st != E4B_OK ? st : check_items(e4b::permute_items(T, H, k, dtype == E4B_DT_F32 ? 2 : 1));
 }
 
 size_t permute_ws_bytes(int32_t dtype, int64_t T, int64_t H, int32_t k) {
@@ -266,7 +270,7 @@ int check_lora(int32_t r, int64_t S, int64_t K, int64_t N, int64_t groups, int64
   q->r = r;
   q->offsets = offsets;
   q->ids = ids;
-  return e4b::lora_blocks(*q) >= lim ? E4B_ERR_OVERFLOW : E4B_OK;
+  return E4B_OK;
 }
 
 int lora_launch_of(const e4b_lora_args* a, e4b::LoraLaunch* L) {
@@ -283,7 +287,7 @@ int lora_launch_of(const e4b_lora_args* a, e4b::LoraLaunch* L) {
   L->out = a->out;
   L->z = a->z;
   L->ws = a->ws;
-  return E4B_OK;
+  return check_items(e4b::lora_items(*L));
 }
 
 int lora_backward_launch_of(const e4b_lora_backward_args* a, e4b::LoraBackwardLaunch* L) {
@@ -303,7 +307,7 @@ int lora_backward_launch_of(const e4b_lora_backward_args* a, e4b::LoraBackwardLa
   L->ga = a->ga;
   L->gb = a->gb;
   L->ws = a->ws;
-  return E4B_OK;
+  return check_items(e4b::lora_backward_items(*L));
 }
 
 }  // namespace
@@ -365,7 +369,7 @@ int e4b_grouped_lora_backward(const e4b_lora_backward_args* a, void* stream) {
 
 int e4b_permute_workspace_bytes(int32_t dtype, int64_t T, int64_t H, int32_t k, size_t* bytes) {
   if (!bytes || !dtype_ok(dtype)) return E4B_ERR_ARG;
-  const int st = check_tokens(T, H, k);
+  const int st = check_permute(dtype, T, H, k);
   if (st != E4B_OK) return st;
   *bytes = permute_ws_bytes(dtype, T, H, k);
   return E4B_OK;
@@ -374,7 +378,7 @@ int e4b_permute_workspace_bytes(int32_t dtype, int64_t T, int64_t H, int32_t k, 
 int e4b_permute_tokens(const void* x, int32_t dtype, int64_t T, int64_t H, int32_t k,
                        const int32_t* sorted_slots, void* rows, void* ws, size_t ws_bytes, void* stream) {
   if (!dtype_ok(dtype)) return E4B_ERR_ARG;
-  int st = check_tokens(T, H, k);
+  int st = check_permute(dtype, T, H, k);
   if (st != E4B_OK) return st;
   if (T == 0) return check_device();
   if (!x || !sorted_slots || !rows) return E4B_ERR_ARG;
@@ -399,6 +403,7 @@ int e4b_combine_tokens(const void* rows, int32_t rows_dtype, int64_t T, int64_t 
                        void* ws, size_t ws_bytes, void* stream) {
   if (!dtype_ok(rows_dtype) || !dtype_ok(out_dtype)) return E4B_ERR_ARG;
   int st = check_tokens(T, H, k);
+  if (st == E4B_OK) st = check_items(e4b::combine_items(T, H, rows_dtype));
   if (st != E4B_OK) return st;
   if (T == 0) return check_device();
   if (!rows || !sorted_slots || !out) return E4B_ERR_ARG;
@@ -428,6 +433,7 @@ int e4b_combine_tokens_backward(const void* g_out, int32_t g_dtype, const void* 
                                 void* ws, size_t ws_bytes, void* stream) {
   if (!dtype_ok(g_dtype) || !dtype_ok(rows_dtype) || !dtype_ok(g_rows_dtype)) return E4B_ERR_ARG;
   int st = check_tokens(T, H, k);
+  if (st == E4B_OK) st = check_items(e4b::combine_backward_items(T, H, k));
   if (st != E4B_OK) return st;
   if (T == 0) return check_device();
   if (!g_out || !sorted_slots || !topk_w || !g_rows) return E4B_ERR_ARG;

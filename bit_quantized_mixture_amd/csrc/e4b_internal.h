@@ -188,8 +188,11 @@ struct CombineBackwardLaunch {
 };
 hipError_t launch_combine_backward(const CombineBackwardLaunch& L, hipStream_t stream);
 int64_t combine_inv_slots(int64_t S);  // 0: the kernels find the rows themselves
-int64_t permute_blocks(int64_t T, int64_t halves, int k);
-int64_t combine_blocks(int64_t T, int64_t H, int k);
+// Work items of a call's largest launch (a launch takes fewer than kLaunchItems).
+constexpr int64_t kLaunchItems = int64_t(1) << 32;
+int64_t permute_items(int64_t T, int64_t H, int k, int elem_halves);
+int64_t combine_items(int64_t T, int64_t H, int rows_dtype);
+int64_t combine_backward_items(int64_t T, int64_t H, int k);
 
 // Low-rank adapters on grouped rows (lora.hip).
 struct LoraGroups {
@@ -228,7 +231,8 @@ struct LoraBackwardLaunch {
 // Workspace sizes go by q's sizes and ids and by which outputs are set.
 size_t lora_ws_bytes(const LoraLaunch& L);
 size_t lora_backward_ws_bytes(const LoraBackwardLaunch& L);
-int64_t lora_blocks(const LoraGroups& q);
+int64_t lora_items(const LoraLaunch& L);
+int64_t lora_backward_items(const LoraBackwardLaunch& L);
 hipError_t launch_lora(const LoraLaunch& L, hipStream_t stream);
 hipError_t launch_lora_backward(const LoraBackwardLaunch& L, hipStream_t stream);
 

@@ -1107,11 +1107,14 @@ int expand_chunks(int64_t tiles, int64_t C, int waves, int wanted) {
   return int(want < 1 ? 1 : (want < most ? want : most));
 }
 
+int expand_wanted(int r) { return r > 32 ? 512 : 2560; }
+constexpr int kFusedWanted = 256;
+
 hipError_t expand(const LoraGroups& q, const float* z, int pieces, const uint16_t* w, const float* scale, int64_t C,
                   const void* base, void* out, int odt, float* z_out, hipStream_t s) {
   const int bm = row_tile_log2(q.S, q.G, q.r);
   const int64_t tiles = tiles_bound(q.S, q.G, bm);
-  const int chunks = expand_chunks(tiles, C, kWaves, q.r > 32 ? 512 : 2560);
+  const int chunks = expand_chunks(tiles, C, kWaves, expand_wanted(q.r));
   ExpandArgs a{z, w, scale, q.offsets, q.ids, base, out, z_out, C, int(q.S), int(q.G), int(q.n), q.r, bm, pieces,
                uint32_t(chunks), int(div_up(div_up(C, 64), chunks))};
   const dim3 grid(unsigned(tiles * chunks));
@@ -1171,6 +1174,10 @@ void reduce_of(const LoraGroups& q, int64_t C, bool up, float* grad, const float
   t->chunks = uint32_t(div_up(t->len, kReduceLen));
 }
 
+// Workgroups of the launch between the passes: those that sum u, and those that transpose A.
+int64_t between_u_blocks(const LoraGroups& q) { return div_up(q.S * (q.r / 4), 16 * kWaves); }
+int64_t between_at_blocks(const LoraGroups& q) { return div_up(q.n * (q.r / 8) * (q.K / 8), kThreads); }
+
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
 
 // Workspace of a backward call.
@@ -1214,21 +1221,34 @@ size_t lora_ws_bytes(const LoraLaunch& L) {
 
 size_t lora_backward_ws_bytes(const LoraBackwardLaunch& L) { return backward_layout(L).total; }
 
-// Workgroups of the largest grid a call with these sizes starts.
-int64_t lora_blocks(const LoraGroups& q) {
-  const int64_t C = q.K > q.N ? q.K : q.N;
+// Work items of the largest grid a call starts.
+int64_t expand_blocks(const LoraGroups& q, int64_t C) {
   const int64_t tiles = tiles_bound(q.S, q.G, row_tile_log2(q.S, q.G, q.r));
-  int64_t most = tiles_bound(q.S, q.G, shrink_tile_log2(q)) * 16;
-  int64_t grad = 0;
-  for (int64_t cols : {q.K, q.N})
-    for (bool up : {false, true}) {
-      const int64_t v = grad_tiles_bound(q, grad_rows(q, cols, up)) * div_up(cols, kGradCols);
-      grad = v > grad ? v : grad;
-    }
-  const int64_t of[] = {tiles * div_up(C, 128), grad, 2 * q.n * div_up(int64_t(q.r) * C, kReduceLen),
-                        div_up(q.S * (q.r / 4), 16 * kWaves) + div_up(q.n * (q.r / 8) * (q.K / 8), kThreads)};
-  for (int64_t v : of) most = v > most ? v : most;
-  return most;
+  return tiles * expand_chunks(tiles, C, kWaves, expand_wanted(q.r));
+}
+int64_t lora_items(const LoraLaunch& L) {
+  const LoraGroups& q = L.q;
+  if (lora_fused(q)) {
+    const int64_t tiles = tiles_bound(q.S, q.G, 4);
+    return tiles * expand_chunks(tiles, q.N, fused_waves(q.r), kFusedWanted) * fused_waves(q.r) * kWave;
+  }
+  const int64_t shrink = tiles_bound(q.S, q.G, shrink_tile_log2(q)) * shrink_pieces(q, q.K);
+  const int64_t expand = expand_blocks(q, q.N);
+  return (shrink > expand ? shrink : expand) * kThreads;
+}
+int64_t lora_backward_items(const LoraBackwardLaunch& L) {
+  const LoraGroups& q = L.q;
+  const bool need_u = L.gx || L.ga;
+  const auto pass = [&](int64_t C, bool up) {
+    return grad_tiles_bound(q, grad_rows(q, C, up)) * div_up(C, kGradCols * grad_subs(q.r, up));
+  };
+  const auto sums = [&](int64_t C) { return q.n * div_up(q.r * C, kReduceLen); };
+  const int64_t blocks[] = {pass(q.N, need_u), L.ga ? pass(q.K, false) : 0, L.gx ? expand_blocks(q, q.K) : 0,
+                            need_u ? between_u_blocks(q) + (L.gx ? between_at_blocks(q) : 0) : 0,
+                            (L.gb ? sums(q.N) : 0) + (L.ga ? sums(q.K) : 0)};
+  int64_t most = 0;
+  for (int64_t v : blocks) most = v > most ? v : most;
+  return most * kThreads;
 }
 
 template <int ODT>
@@ -1243,7 +1263,7 @@ hipError_t launch_lora(const LoraLaunch& L, hipStream_t stream) {
   const LoraGroups& q = L.q;
   if (lora_fused(q)) {
     const int64_t tiles = tiles_bound(q.S, q.G, 4);
-    const int chunks = expand_chunks(tiles, q.N, fused_waves(q.r), 256);
+    const int chunks = expand_chunks(tiles, q.N, fused_waves(q.r), kFusedWanted);
     FusedArgs a{L.x, L.a, L.b, L.scale, q.offsets, q.ids, L.y, L.out, L.z, q.K, q.N, int(q.S), int(q.G), int(q.n),
                 q.r, uint32_t(chunks), int(div_up(div_up(q.N, 64), chunks))};
     const dim3 grid(unsigned(tiles * chunks));
@@ -1271,8 +1291,8 @@ hipError_t launch_lora_backward(const LoraBackwardLaunch& L, hipStream_t stream)
     if ((e = grad_pass(q, L.z, L.g, L.b, L.scale, q.N, true, L.gb, parts_b, upart, stream)) != hipSuccess) return e;
     if (need_u) {
       uint16_t* at = L.gx ? reinterpret_cast<uint16_t*>(ws + w.at) : nullptr;
-      const int64_t u_blocks = div_up(q.S * (q.r / 4), 16 * kWaves);
-      const int64_t t_blocks = at ? div_up(q.n * (q.r / 8) * (q.K / 8), kThreads) : 0;
+      const int64_t u_blocks = between_u_blocks(q);
+      const int64_t t_blocks = at ? between_at_blocks(q) : 0;
       BetweenArgs a{upart, u, L.a, at, q.S * q.r, uint32_t(u_blocks), int(q.n), q.r,
                     int(div_up(q.N, kGradCols * grad_subs(q.r, true))), int(q.K)};
       hipLaunchKernelGGL(between_kernel, dim3(unsigned(u_blocks + t_blocks)), dim3(kThreads), 0, stream, a);

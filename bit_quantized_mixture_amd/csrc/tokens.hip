@@ -376,22 +376,25 @@ void backward_rows(const CombineBackwardLaunch& L, bool scan, hipStream_t stream
 
 int64_t combine_inv_slots(int64_t S) { return S > kScanSlots ? S : 0; }
 
-// Workgroups of the largest grid these launchers start for the sizes (checked against the 2^31
-// limit by the caller).
-int64_t permute_blocks(int64_t T, int64_t halves, int k) {
-  const int64_t n = (halves + 7) / 8, S = T * k;
+// Work items of the largest grid each launcher starts for the sizes (the caller checks them against
+// a launch's limit; the slots' inverse has T * k at most).
+int64_t permute_items(int64_t T, int64_t H, int k, int elem_halves) {
+  const int64_t n = (H * elem_halves + 7) / 8, S = T * k;
   const int tl = team_log2_of(n);
   const int64_t per = kThreads >> tl, chunks = (n + (1 << tl) - 1) >> tl;
-  const int64_t a = (S + per - 1) / per, b = (T * chunks + per - 1) / per + (S + kThreads - 1) / kThreads;
-  return a > b ? a : b;
+  if (permute_inv_slots(T, H, k, elem_halves) == 0) return (S + per - 1) / per * kThreads;
+  return ((T * chunks + per - 1) / per + (S + kThreads - 1) / kThreads) * kThreads;
 }
-int64_t combine_blocks(int64_t T, int64_t H, int k) {
-  const int64_t n = (H + 3) / 4;
+int64_t combine_items(int64_t T, int64_t H, int rows_dtype) {
+  const int V = rows_dtype == 0 ? 8 : 4;
+  const int64_t n = (H + V - 1) / V;
   const int tl = team_log2_of(n);
-  const int64_t items = T * ((n + (1 << tl) - 1) >> tl);
-  const int64_t per = kThreads >> tl, per8 = kThreads >> team_log2_of((H + 7) / 8);
-  const int64_t a = (items + per - 1) / per, b = (T * k + per8 - 1) / per8;
-  return a > b ? a : b;
+  const int64_t per = kThreads >> tl;
+  return (T * ((n + (1 << tl) - 1) >> tl) + per - 1) / per * kThreads;
+}
+int64_t combine_backward_items(int64_t T, int64_t H, int k) {
+  const int64_t per = kThreads >> team_log2_of((H + 7) / 8);
+  return (T * k + per - 1) / per * kThreads;
 }
 
 // Token order from 128 MB of rows on, where what it saves (a fifth to a quarter of the time) is more

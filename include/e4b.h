@@ -75,7 +75,8 @@ typedef enum e4b_status {
   E4B_ERR_ALIGN = -3,       /* a pointer is not 16-byte aligned */
   E4B_ERR_WORKSPACE = -4,   /* workspace missing or smaller than the queried size */
   E4B_ERR_UNSUPPORTED = -5, /* current device is not gfx950 */
-  E4B_ERR_OVERFLOW = -6,    /* a count does not fit the index types (T*k >= 2^31, ...) */
+  E4B_ERR_OVERFLOW = -6,    /* a count does not fit the index types (T*k >= 2^31, ...) or a launch
+                             * (2^32 work items) */
   E4B_ERR_HIP = -7,         /* a HIP runtime call or kernel launch failed */
   E4B_ERR_TOO_LARGE = -8    /* more workspace than e4b_moe_forward_noalloc's fixed scratch */
 } e4b_status;
@@ -194,7 +195,10 @@ int e4b_permute_workspace_bytes(int32_t dtype, int64_t T, int64_t H, int32_t k, 
 /*
  * e4b_permute_tokens — the routed copies of the token rows in expert order, the input of the
  * grouped products: rows[p] = x[sorted_slots[p] / k].
- *   x             [T, H] of `dtype` (an e4b_dtype).  Any H >= 1.  1 <= k <= 64, T*k < 2^31.
+ *   x             [T, H] of `dtype` (an e4b_dtype).  Any H >= 1.  1 <= k <= 64, T*k < 2^31.  Here and in
+ *                 the two calls below a launch takes fewer than 2^32 lanes of 16 bytes or, where a row
+ *                 is gathered or its gradient written, 2^26 rows of more than 512 bytes: 34 GB and more
+ *                 may be E4B_ERR_OVERFLOW.
  *   sorted_slots  [T*k] int32 from e4b_route_permute: a permutation of 0 .. T*k - 1.
  *   rows          [T*k, H] of `dtype` out: bit copies.
  *   ws            device workspace of at least e4b_permute_workspace_bytes().
