@@ -946,6 +946,8 @@ def e4b_grouped_lora_backward(g, x, z, a, b, scale, group_offsets, group_adapter
     args = LoraBackwardArgs()
     _lora_common(args, a, b, scale, group_offsets, group_adapter, S, K, N, dev)
     r, n = args.r, args.adapters
+    if gx is False and ga is False and gb is False:
+        raise E4BError("e4b_grouped_lora_backward", -1)  # also without rows, where the C call has no gx to see
     if gx is False and gx_base is not None:
         raise ValueError("gx_base is only for gx")
     if ga is not False:

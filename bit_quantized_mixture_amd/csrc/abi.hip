@@ -352,7 +352,8 @@ int e4b_grouped_lora_backward(const e4b_lora_backward_args* a, void* stream) {
   e4b::LoraBackwardLaunch L;
   int st = lora_backward_launch_of(a, &L);
   if (st != E4B_OK) return st;
-  if (!a->gx && !a->ga && !a->gb) return E4B_ERR_ARG;
+  // without rows gx is empty (its pointer may be NULL), and alone it asks for nothing
+  if (!a->gx && !a->ga && !a->gb) return a->S == 0 ? check_device() : E4B_ERR_ARG;
   // without rows the inputs may be empty; the adapters' gradients are still written (zeros)
   if (!a->group_offsets || !a->a || !a->b) return E4B_ERR_ARG;
   if (a->S > 0 && (!a->g || (a->ga && !a->x) || (a->gb && !a->z))) return E4B_ERR_ARG;

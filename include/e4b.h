@@ -464,7 +464,7 @@ int e4b_lora_backward_workspace_bytes(const e4b_lora_backward_args* a, size_t* b
  * the sums over the rows of every group that uses adapter a (0 for an adapter without rows).
  * Rows of a group without an adapter get gx = gx_base; rows outside every group are left as they
  * were.  Float32 sums in a fixed order: deterministic.  ga and gb are overwritten.  At least one
- * of gx, ga, gb is given.  A and B are finite; a NaN or infinity in a row of g, x or z may reach
+ * of gx, ga, gb is given (with S = 0 all may be NULL: an empty gx).  A and B are finite; a NaN or infinity in a row of g, x or z may reach
  * that row of gx and the gradients of its adapter (as NaN where the exact value is infinite), and
  * nothing else.  Apart from gx_base == gx the outputs and the workspace overlap no other argument.
  * Synchronous errors as e4b_moe_forward.
