@@ -1030,11 +1030,15 @@ int grad_subs(int r, bool up) { return up && r <= 16 ? 2 : 1; }
 // Rows of a gradient tile at most: as many tiles as fill two workgroups on every CU (a tile costs a
 // float32 write and read of its [r, C] sums).  Gradients of 32 experts at [2880, 2880] and of 8 at
 // [28672, 4096]: 96 and 191 us; with half as many tiles again 111 and 198, with three quarters as many
-// 95 and 193.
+// 95 and 193.  Each group's rest is about half a tile, and is taken off the tiles that are wanted, but
+// no more than half of them: where many groups share the rows, one that has most of them still has to
+// be cut (16384 rows in 128 groups at [2048, 2048], rank 32: 126 us, and with half the rows in one group
+// 138; 499 where the groups' rests took all and that group was a single tile).
 int grad_rows(const LoraGroups& q, int64_t C, bool up) {
   const int64_t chunks = div_up(C, kGradCols * grad_subs(q.r, up));
   const int64_t used = q.G < q.S ? q.G : q.S;
-  int64_t tiles = 512 / chunks - used / 2;  // about half a tile for each group is its rest
+  const int64_t round = 512 / chunks;
+  int64_t tiles = round - (used < round ? used / 2 : round / 2);
   if (tiles < 1) tiles = 1;
   int64_t most = (div_up(q.S, tiles) + 63) / 64 * 64;
   return int(most < 128 ? 128 : (most > (1 << 20) ? 1 << 20 : most));
