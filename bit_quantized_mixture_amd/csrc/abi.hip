@@ -259,7 +259,7 @@ int check_lora(int32_t r, int64_t S, int64_t K, int64_t N, int64_t groups, int64
   const int64_t lim = int64_t(1) << 31, big = int64_t(1) << 48;
   const int64_t wide = K > N ? K : N;
   // a tile's rows and an adapter's matrix are addressed with 32-bit byte offsets
-  if (S >= lim || wide > (int64_t(1) << 23) || groups >= lim || adapters >= lim || S > big / wide ||
+  if (S >= lim || wide > (int64_t(1) << 23) || groups > e4b::kLoraGroups || adapters >= lim || S > big / wide ||
       adapters > big / (wide * r))
     return E4B_ERR_OVERFLOW;
   q->S = S;

@@ -391,7 +391,7 @@ int e4b_dgrad_workspace_bytes(const e4b_dgrad_args* a, size_t* bytes);
 int e4b_grouped_dgrad(const e4b_dgrad_args* a, void* stream);
 
 /* Arguments of e4b_grouped_lora.  Sizes: K % 8 == 0, N % 8 == 0, r % 8 == 0, 8 <= r <= 128;
- * K, N <= 2^23; S, groups and adapters below 2^31.  Smaller or mixed ranks: pad A and B with zeros. */
+ * K, N <= 2^23; groups <= 65536; S and adapters below 2^31.  Smaller or mixed ranks: pad A and B with zeros. */
 typedef struct e4b_lora_args {
   int32_t r;              /* rank */
   int32_t out_dtype;      /* e4b_dtype of y and out */
