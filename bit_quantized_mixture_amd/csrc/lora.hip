@@ -338,14 +338,17 @@ struct Expand {
 #pragma unroll
       for (int b = 0; b < RB; ++b) {
         f32x4 d[kH];
-#pragma unroll
-        for (int h = 0; h < kH; ++h) d[h] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (adapter) {
+#pragma unroll
+          for (int h = 0; h < kH; ++h) d[h] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
           for (int k = 0; k < kSteps; ++k)
 #pragma unroll
             for (int h = 0; h < kH; ++h)
               d[h] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(zf[b][k], t.w[h][k % kFrags], d[h], 0, 0, 0);
+        } else {  // y + -0 is y, whichever zero y is
+#pragma unroll
+          for (int h = 0; h < kH; ++h) d[h] = f32x4{-0.f, -0.f, -0.f, -0.f};
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
