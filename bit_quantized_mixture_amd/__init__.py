@@ -892,8 +892,8 @@ def e4b_grouped_lora(x, a, b, scale, group_offsets, group_adapter=None, y=None, 
     args = LoraArgs()
     _lora_common(args, a, b, scale, group_offsets, group_adapter, S, K, N, dev)
     if y is not None:
-        dtype = y.dtype
         _need_rows(y, "y", (S, N), dev)
+        dtype = y.dtype
         args.y = y.data_ptr()
     if out is not None:
         _need_rows(out, "out", (S, N), dev)
@@ -957,8 +957,8 @@ def e4b_grouped_lora_backward(g, x, z, a, b, scale, group_offsets, group_adapter
         _need(z, "z", (torch.float32,), (S, r), dev)
         args.z = z.data_ptr()
     if gx_base is not None:
-        dtype = gx_base.dtype
         _need_rows(gx_base, "gx_base", (S, K), dev)
+        dtype = gx_base.dtype
         args.gx_base = gx_base.data_ptr()
     if isinstance(gx, torch.Tensor):
         _need_rows(gx, "gx", (S, K), dev)
