@@ -106,6 +106,15 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t wave_rsrc(const void* base, ui
 constexpr int kPastCaches = 2;
 constexpr uint32_t kNowhere = 0x80000000u;  // past the end of every buffer (of 2^31 bytes at most)
 
+// 16 bytes a lane.  A store of more than 64 bits reads its registers some cycles after it is issued,
+// and the compiler keeps their next values away for as long, except where the offset is in a scalar
+// register: there nothing stood between such a store and the next write of its first register, and
+// with other work on the CU some rows came out with that value in them.  So the whole offset is the
+// lane's (past-the-end lanes still are: kNowhere and a tile's offsets stay under 2^32).
+__device__ __forceinline__ void store_wide(u32x4 v, __amdgpu_buffer_rsrc_t r, uint32_t lane_off) {
+  __builtin_amdgcn_raw_buffer_store_b128(v, r, lane_off, 0, kPastCaches);
+}
+
 // Sums of one wave over its units of 64 columns (128 bytes of each row): acc[b][k] gets rows 16b ..
 // of the tile by ranks 16k .. .  The wave takes its share of the units first .. end - 1 one after the
 // other (the waves' units in turn read 10 % slower).  A unit comes in whole lines (8 lanes a row; a
@@ -359,7 +368,7 @@ struct Expand {
             u32x4 o;
 #pragma unroll
             for (int h = 0; h < 4; ++h) o[h] = __float_as_uint(__uint_as_float(y[h]) + d[h][e]);
-            __builtin_amdgcn_raw_buffer_store_b128(o, out, off, at, kPastCaches);
+            store_wide(o, out, off + at);
           } else {
             u32x2 o;
 #pragma unroll
