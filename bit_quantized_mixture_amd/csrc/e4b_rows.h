@@ -33,7 +33,8 @@ __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 
 // V consecutive elements as float32 (4 or 8 float32, 8 bf16; 4 or 8 of either written).  Rows are
 // written past the caches: kept there they slowed the kernels that followed (7862 slots of 3000
-// float32 back to tokens and again: 36 us a call kept, 27 past).
+// float32 back to tokens and again: 36 us a call kept, 27 past; measured without a call that reads
+// them in between).
 template <int V>
 __device__ __forceinline__ void load_vec(const uint16_t* p, float (&v)[V]) {
   static_assert(V == 8, "");

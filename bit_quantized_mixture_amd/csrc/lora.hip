@@ -4,8 +4,9 @@
 //   forward    z = x A_a^T,  out = y + s_a z B_a^T
 //   backward   u = s_a g B_a,  gx = gx0 + u A_a,  gA_a = sum_p u_p^T x_p,  gB_a = s_a sum_p g_p^T z_p
 // with A_a [r, K], B_a [N, r] bf16, r = 8 .. 128.  About 2r / b flop for each byte moved (b the
-// bytes of an element read and written): bound by memory at every rank taken here, so the kernels
-// are three streaming passes with the matrix unit beside them:
+// bytes of an element read and written): by its bytes and operations alone memory bounds every rank
+// taken here, so the kernels are three streaming passes with the matrix unit beside them (the gradients
+// above rank 32 are not that near: z and u there cost as much as g, at one workgroup a CU):
 //   shrink   [rows, C] x [r, C]^T -> [rows, r]     (z from x and A)
 //   expand   [rows, r] x [C, r]^T added to [rows, C]   (out from z and B; gx from u and A^T)
 //   grad     [rows, r]^T x [rows, C] -> [r, C]     (gA from u and x; gB from z and g, with u in the same pass)
@@ -102,7 +103,8 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t wave_rsrc(const void* base, ui
                      __builtin_amdgcn_readfirstlane(bytes));
 }
 // Stores of rows go past the caches (the instruction's non-temporal bit): more is written than they
-// hold, and kept there it slowed the kernels that followed (8-expert down projection 113 us, 99 so).
+// hold, and kept there it slowed the kernels that followed (8-expert down projection 113 us, 99 so: the
+// call again and again, with no reader of the rows in between).
 constexpr int kPastCaches = 2;
 constexpr uint32_t kNowhere = 0x80000000u;  // past the end of every buffer (of 2^31 bytes at most)
 
@@ -197,8 +199,8 @@ struct ShrinkArgs {
 };
 
 // A workgroup: up to 16 * RB rows of a group and one piece of the columns; its waves'
-// sums meet in LDS.  Bound: HBM, by x: 8192 rows of 14336 at rank 16 (239 MB) take 48 us, 5.0 TB/s.
-// 5003 rows of 2880 at rank 64 (29 MB) take 12 us, most of it the round of latencies of a workgroup
+// sums meet in LDS.  Bound: HBM, by x: 8192 rows of 14336 at rank 16 (239 MB) take 47 us, 5.0 TB/s.
+// 5003 rows of 2880 at rank 64 (29 MB) take 11 us, most of it the round of latencies of a workgroup
 // that has three units a wave.
 template <int RB, int RT>
 __global__ void __launch_bounds__(kThreads) shrink_kernel(ShrinkArgs p) {
@@ -412,7 +414,7 @@ struct ExpandArgs {
 };
 
 // A workgroup: up to 16 * RB rows of a group and one piece of the columns.  Bound: HBM, by the rows
-// read and written: 8192 rows of 4096 float32 at rank 16 (270 MB) take 51 us, 5.3 TB/s; 5003 bf16 rows
+// read and written: 8192 rows of 4096 float32 at rank 16 (270 MB) take 50 us, 5.4 TB/s; 5003 bf16 rows
 // of 2880 at rank 64 (60 MB) 21 us, where the z of a tile and its three parts (made by each workgroup
 // before its first product) are a third.
 template <int RB, int RP, int ODT>
@@ -492,10 +494,13 @@ struct FusedArgs {
 constexpr int fused_waves(int rp) { return rp <= 32 ? 16 : 8; }
 
 // Both products in one launch for tiles of at most 16 rows (decoded tokens): every workgroup of a
-// tile computes the tile's z for itself, from the adapter's A in the L2 cache, instead of waiting
-// for another launch to do it.  Bound: the chain of latencies (offsets, x and A, the waves' sums, B
-// and y): one token at [14336, 4096] and rank 16 takes 7.5 us, 64 of 48 adapters (36 MB) 14.8 us, 512
-// rows of 128 adapters at [1536, 2048] (23 MB) 9.6 us.
+// tile computes the tile's z for itself, from all of x and the adapter's A, instead of waiting for
+// another launch to do it.  A tile's workgroups have neighbouring ids and run on different XCDs, so
+// each reads x and A through an L2 cache of its own: 64 tokens of 48 adapters fetch 50 MB from beyond
+// them, where the inputs are at most 32 MB.
+// Bound: that, and the chain of latencies (offsets, x and A, the waves' sums, B and y).  The kernel
+// alone, traced: one token at [14336, 4096] and rank 16 7.9 us, 64 of 48 adapters (36 MB read and
+// written) 14.1 us, 512 rows of 128 adapters at [1536, 2048] (23 MB) 9.8 us.
 template <int RP, int ODT>
 __global__ void __launch_bounds__(fused_waves(RP) * kWave) fused_kernel(FusedArgs p) {
   typedef Expand<RP, ODT> X;
@@ -650,8 +655,8 @@ __device__ __forceinline__ s16x4 lds_read_tr(const uint8_t* at) {
 // loads in flight) into LDS.  grad: a wave has 64 of the block's columns; the contraction runs over
 // the rows, so m is read transposed, and v stands in LDS transposed in its three parts.  u: a wave
 // has 16 of the block's rows and all its columns; B stands in LDS transposed.
-// Bound: HBM in long groups: g of 8192 rows of 28672 at rank 16 (470 MB) takes 116 us, 4.1 TB/s (4.3
-// with u's partial sums).  32 groups of 128 .. 384 rows of 2880 at rank 32 (47 MB) take 26 us: one
+// Bound: HBM in long groups: g of 8192 rows of 28672 at rank 16 (470 MB) takes 117 us, 4.0 TB/s (4.2
+// with u's partial sums).  32 groups of 128 .. 384 rows of 2880 at rank 32 (47 MB) take 25 us: one
 // round of workgroups that ends with the longest group, four or five blocks one after the other.
 // One pass instead of two reads m once: 8192 rows of 28672 took 387 us for all gradients with a pass
 // each for u and grad (and float32 matrix instructions), 191 so.
@@ -1025,9 +1030,11 @@ int shrink_tile_log2(const LoraGroups& q) {
   return q.r > 32 && l > 5 ? 5 : l;
 }
 
-// Pieces the columns of a shrink are cut into: as many workgroups as are resident together (three on
-// every CU; 24 prompts of rank 64: 31 us a call, 37 with a third more), no piece under 512 columns
-// (two units for each wave).
+// Pieces the columns of a shrink are cut into: as many workgroups as are resident together up to rank
+// 64 (three on every CU; 24 prompts of rank 64: 31 us a call, 37 with a third more), no piece under 512
+// columns (two units for each wave).  Above rank 64 two are resident, and three are still wanted: with
+// 768 and with 512, us a call at rank 128, 24 prompts at [2880, 2880] 55 and 59, 2048 rows of 8 experts
+// at [4096, 4096] 39 and 46, but 8192 rows at [4096, 14336] 157 and 148.
 int shrink_pieces(const LoraGroups& q, int64_t C) {
   const int64_t tiles = tiles_bound(q.S, q.G, shrink_tile_log2(q));
   const int64_t want = 768 / (tiles > 0 ? tiles : 1), most = C / 512;
@@ -1039,8 +1046,11 @@ int shrink_pieces(const LoraGroups& q, int64_t C) {
 // sums (r float32 for each row and workgroup) stay few beside m; as many as the registers hold.
 int grad_subs(int r, bool up) { return up && r <= 16 ? 2 : 1; }
 
-// Rows of a gradient tile at most: as many tiles as fill two workgroups on every CU (a tile costs a
-// float32 write and read of its [r, C] sums).  Gradients of 32 experts at [2880, 2880] and of 8 at
+// Rows of a gradient tile at most: as many tiles as give every CU two workgroups (a tile costs a
+// float32 write and read of its [r, C] sums).  Up to rank 32 that is one resident round.  Above, a CU
+// holds one workgroup and it is two; with 512 and with 256 workgroups, us a call at ranks 64 and 128, 32
+// experts at [2880, 2880] 128 / 285 and 131 / 286, 8 experts at [14336, 4096] 235 / 585 and 225 / 567,
+// half of 16384 rows in one of 64 groups at rank 64 257 and 271.  Gradients of 32 experts at [2880, 2880] and of 8 at
 // [28672, 4096]: 96 and 191 us; with half as many tiles again 111 and 198, with three quarters as many
 // 95 and 193.  Each group's rest is about half a tile, and is taken off the tiles that are wanted, but
 // no more than half of them: where many groups share the rows, one that has most of them still has to
@@ -1061,7 +1071,9 @@ int64_t grad_tiles_bound(const LoraGroups& q, int most) {
 }
 
 // Tiles that write parts: all where adapters are shared by groups; without ids only those of
-// groups of several tiles, at most two for each `most` rows.
+// groups of several tiles, at most two for each `most` rows.  With ids that is a float32 [r, C] for every
+// group that has rows, written and read again, whether its adapter has other groups or not: 8192 rows in
+// 1024 groups at rank 64, [14336, 4096], ask for 5 GB.
 int64_t parts_bound(const LoraGroups& q, int most) {
   const int64_t all = grad_tiles_bound(q, most), kept = 2 * q.S / most;
   return q.ids || all < kept ? all : kept;
@@ -1221,8 +1233,8 @@ BackwardLayout backward_layout(const LoraBackwardLaunch& L) {
 
 }  // namespace
 
-// Whether the forward call runs as one launch: tiles of at most 16 rows, and an A that a CU reads
-// from the L2 cache in a few microseconds, about what the second launch would cost.  us in one launch
+// Whether the forward call runs as one launch: tiles of at most 16 rows, and an A that every workgroup
+// of a tile reads in a few microseconds, about what the second launch would cost.  us in one launch
 // and in two: 64 tokens of 48 adapters at r K = 65536 14.8 and 20.7, at 131072 20.7 and 24.1, at 262144
 // 22.6 and 15.9 (one token: 7.5 and 6.9, where a second launch costs the host 3; 12.5 and 8.2).
 bool lora_fused(const LoraGroups& q) {

@@ -123,8 +123,9 @@ __global__ void __launch_bounds__(kThreads) permute_kernel(const uint16_t* __res
 // The same in token order: a team item is up to 512 columns of one token, read once and written to
 // the k rows of its slots.  The gather above reads each x row k times (from the memory-side cache,
 // beside the stream of rows): 1.07 GB of rows took 310 us against 233 a call here, with stores that are
-// not kept in the caches; 225 of them in this kernel, 5.4 TB/s.  Behind the items, workgroups look for rows that inv does not lead to (a slot
-// out of range: zeros; a slot that a higher row names too) and write them by themselves.
+// not kept in the caches; 225 of them in this kernel, 5.4 TB/s.  Behind the items, workgroups look for
+// rows that inv does not lead to (a slot out of range: zeros; a slot that a higher row names too) and
+// write them by themselves.
 __global__ void __launch_bounds__(kThreads) permute_scatter_kernel(const uint16_t* __restrict__ x,
                                                                    const int32_t* __restrict__ slots,
                                                                    const int32_t* __restrict__ inv, int64_t T,

@@ -424,8 +424,8 @@ int e4b_lora_workspace_bytes(const e4b_lora_args* a, size_t* bytes);
  * per-expert adapters of QLoRA training).  For every row p of group g with adapter a:
  *   z[p] = x[p] A_a^T,   out[p] = y[p] + scale[a] * z[p] B_a^T.
  * Rows of a group without an adapter get out = y and z = 0; rows outside every group are left as
- * they were.  z is the float32 sum of exact products, and enters the second product unrounded;
- * out is rounded once.  Deterministic.  A and B are finite.  Apart from y == out the outputs and
+ * they were.  z is the float32 sum of exact products; scale * z, in float32, enters the second
+ * product with all its bits; out is rounded once.  Deterministic.  A and B are finite.  Apart from y == out the outputs and
  * the workspace overlap no other argument.  Synchronous errors as e4b_moe_forward.
  */
 int e4b_grouped_lora(const e4b_lora_args* a, void* stream);
@@ -455,7 +455,9 @@ typedef struct e4b_lora_backward_args {
 } e4b_lora_backward_args;
 
 /* Workspace bytes e4b_grouped_lora_backward needs: by the sizes in `a`, by which of gx, ga and
- * gb are set and by whether group_adapter is (the pointers are not followed). */
+ * gb are set and by whether group_adapter is (the pointers are not followed).  For gx and ga
+ * u's sums take S * r * 4 bytes for each 256 columns of N (512 up to rank 16); with group_adapter
+ * ga and gb take r * (K + N) * 4 for each group that can have rows. */
 int e4b_lora_backward_workspace_bytes(const e4b_lora_backward_args* a, size_t* bytes);
 
 /*
