@@ -9,7 +9,8 @@ from gpu_helpers import DEV
 pytestmark = pytest.mark.gpu
 
 
-@pytest.mark.parametrize("r,dtype", [(8, base.F32), (16, base.F32), (32, base.F32), (64, base.F32), (128, base.F32), (32, base.BF16)])
+@pytest.mark.parametrize("r,dtype", [(8, base.F32), (16, base.F32), (32, base.F32), (64, base.F32), (128, base.F32),
+                                     (8, base.BF16), (16, base.BF16), (32, base.BF16), (64, base.BF16), (128, base.BF16)])
 def test_rows_of_a_layer(e4b, r, dtype):
     """8192 rows of 32 experts at [2880, 2880], an expert without an adapter among them."""
     lengths = [(131 * i) % 200 + 150 for i in range(31)]
