@@ -37,7 +37,7 @@ def listed():
         {"name": "product_decode", "kind": "product", "T": 64, "K": 2048, "N": 1536, "E": 128, "k": 8, "skew": 0.0, "x": "bf16",
          "out": "f32", "bias": False},
         # a prompt of odd length through a down projection, rows in expert order, some experts much asked for
-        {"name": "product_ragged", "kind": "product", "T": 8168, "K": 1536, "N": 4096, "E": 64, "k": 1, "skew": 1.0, "x": "f32",
+        {"name": "product_ragged", "kind": "product", "T": 8168, "K": 1536, "N": 4096, "E": 64, "k": 1, "skew": 0.5, "x": "f32",
          "out": "bf16", "bias": False},
         # the 32-expert layer's gate_up projection over 2048 tokens
         {"name": "product_layer", "kind": "product", "T": 2048, "K": 2880, "N": 5760, "E": 32, "k": 4, "skew": 0.0, "x": "bf16",
@@ -81,9 +81,11 @@ def draw(rng):
             E = _log(rng, 1, 128)
             k = min(E, rng.randint(1, 8))
             case = {"kind": kind, "T": max(1, _log(rng, 1, 16384) // k), "K": 32 * _log(rng, 2, 448),
-                    "N": rng.choice([_log(rng, 64, 28672), 8 * _log(rng, 8, 3584), 8 * _log(rng, 8, 3584)]), "E": E, "k": k, "skew": rng.choice([0.0, 0.5, 1.0]), "x": rng.choice(["bf16", "f32"]),
+                    "N": rng.choice([_log(rng, 64, 28672), 8 * _log(rng, 8, 3584), 8 * _log(rng, 8, 3584)]), "E": E, "k": k, "skew": rng.choice([0.0, 0.25, 0.5]), "x": rng.choice(["bf16", "f32"]),
                     "out": rng.choice(["f32", "bf16"]), "bias": rng.random() < 0.5}
-            if E * case["N"] * case["K"] > 1e9:  # the plain form decodes the stack to float32
+            # the plain form decodes the stack to float32 and pads every expert's rows to the longest
+            longest = 3 * case["T"] * k * ((1 - case["skew"]) / E + case["skew"] / math.sqrt(E)) + 8
+            if E * case["N"] * case["K"] > 1e9 or E * longest * (case["K"] + case["N"]) > 2e9:
                 continue
         elif kind == "lora_grad8":
             experts = rng.random() < 0.5
@@ -91,7 +93,8 @@ def draw(rng):
             case = {"kind": kind, "S": _log(rng, 16, 16384), "K": 32 * _log(rng, 2, 448), "N": 8 * _log(rng, 8, 3584),
                     "r": 8 * _log(rng, 1, 16), "groups": groups, "adapters": groups if experts else rng.randint(1, groups),
                     "experts": experts, "out": rng.choice(["f32", "bf16"])}
-            if case["adapters"] * case["r"] * (case["K"] + case["N"]) > 1e8:
+            padded = (2 * case["S"] + 8 * groups) * (case["K"] + case["N"])
+            if case["adapters"] * case["r"] * (case["K"] + case["N"]) > 1e8 or padded > 2e9:
                 continue
         elif kind == "rows8":
             case = {"kind": kind, "S": _log(rng, 1, 131072), "C": 32 * _log(rng, 2, 448), "rows": rng.choice(["bf16", "f32"])}
@@ -193,6 +196,13 @@ def _offsets(lengths):
     return torch.from_numpy(np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)).to(DEV)
 
 
+def _places(lengths):
+    """Row numbers of every group, padded to the longest with the number of rows: [groups, longest]."""
+    ends, longest = np.cumsum(lengths), max(1, max(lengths))
+    place = (ends - lengths)[:, None] + np.arange(longest)[None, :]
+    return torch.from_numpy(np.where(place < ends[:, None], place, ends[-1]).astype(np.int64)).to(DEV)
+
+
 def prepare(case, seed):
     gen, rng = torch.Generator(device=DEV), np.random.default_rng(seed)
     gen.manual_seed(seed)
@@ -214,7 +224,8 @@ def prepare(case, seed):
         else:      # rows in expert order already
             s["slots"] = None
             s["lengths"] = _lengths(T, E, case["skew"], rng)
-        s["offsets"] = _offsets(s["lengths"])
+        s["offsets"], s["place"] = _offsets(s["lengths"]), _places([n for n in s["lengths"] if n])
+        s["used"] = torch.from_numpy(np.flatnonzero(s["lengths"])).to(DEV)  # experts with rows
         packed = [_pack4(*_to4(normal(N, K, dtype=torch.float32, std=0.02))) for _ in range(E)]
         s["w"], s["ws"] = (torch.stack([p[i] for p in packed]) for i in (0, 1))
         s["bias"] = normal(E, N, dtype=torch.float32, std=0.02) if case["bias"] else None
@@ -224,7 +235,8 @@ def prepare(case, seed):
         S, K, N, r, n, G = (case[v] for v in ("S", "K", "N", "r", "adapters", "groups"))
         s["lengths"] = _lengths(S, G, 0.0, rng)
         ids = np.arange(G) if case["experts"] else np.where(rng.random(G) < 0.1, -1, rng.integers(0, n, G))
-        s["ids"], s["offsets"] = ids.tolist(), _offsets(s["lengths"])
+        s["ids"], s["offsets"], s["place"] = ids.tolist(), _offsets(s["lengths"]), _places(s["lengths"])
+        s["ids_long"] = torch.from_numpy(ids.astype(np.int64)).to(DEV)
         s["adapter"] = None if case["experts"] else torch.from_numpy(ids.astype(np.int32)).to(DEV)
         s["q"], s["qs"] = _to8(normal(S, K))
         s["a"], s["b"] = normal(n, r, K, std=K ** -0.5), normal(n, N, r, std=r ** -0.5)
@@ -284,19 +296,26 @@ def _run_plain(s):
     return _glu_plain(s["rows"].float(), c).to(out), _glu_grad_plain(s["g"].float(), _values8(*kept), c).to(out)
 
 
+def _padded(rows, place):
+    """Rows of every group, padded with zeros: [groups, longest, columns] in float32."""
+    return torch.cat([rows.float(), torch.zeros_like(rows[:1], dtype=torch.float32)])[place]
+
+
+def _rows_of(padded, place, S):
+    """The padded rows at their places: [S, columns]."""
+    out = torch.empty(S + 1, padded.shape[-1], device=padded.device)
+    out[place.reshape(-1)] = padded.reshape(-1, padded.shape[-1])
+    return out[:S]
+
+
 def _product_plain(s, c):
     x = s["x"] if s["slots"] is None else s["x"][s["slots"].long() // c["k"]]
-    x = _values4(*_to4(x))
-    w = [_values4(*_unpack4(s["w"][e], s["ws"][e])) if n else None for e, n in enumerate(s["lengths"])]
-    out = torch.empty(x.shape[0], c["N"], device=x.device)
-    lo = 0
-    for e, n in enumerate(s["lengths"]):
-        if n:
-            out[lo:lo + n] = x[lo:lo + n] @ w[e].T
-            if s["bias"] is not None:
-                out[lo:lo + n] += s["bias"][e]
-        lo += n
-    return out.to(DTYPES[c["out"]])
+    x = _padded(_values4(*_to4(x)), s["place"])
+    w = _values4(*_unpack4(s["w"][s["used"]], s["ws"][s["used"]]))
+    out = torch.bmm(w, x.transpose(1, 2).contiguous()).transpose(1, 2)
+    if s["bias"] is not None:
+        out = out + s["bias"][s["used"]][:, None, :]
+    return _rows_of(out, s["place"], c["T"] * c["k"]).to(DTYPES[c["out"]])
 
 
 def _halves(rows, c):
@@ -326,18 +345,18 @@ def _glu_grad_plain(g, rows, c):
 
 
 def _lora_plain(s, c):
-    x, g = _values8(s["q"], s["qs"]), s["g"].float()
-    a, b = s["a"].float(), s["b"].float()
-    gx, ga, gb = s["gx"].float(), torch.zeros_like(a), torch.zeros_like(b)
-    lo = 0
-    for n, i in zip(s["lengths"], s["ids"]):
-        rows = slice(lo, lo + n)
-        lo += n
-        if n and i >= 0:
-            u = (g[rows] @ b[i]) * s["scale"][i]
-            gx[rows] += u @ a[i]
-            ga[i] += u.T @ x[rows]
-            gb[i] += (g[rows].T @ s["z"][rows]) * s["scale"][i]
+    ids, S, n = s["ids_long"].clamp_min(0), c["S"], s["a"].shape[0]
+    x, g, z = (_padded(v, s["place"]) for v in (_values8(s["q"], s["qs"]), s["g"], s["z"]))
+    a, b = s["a"].float()[ids], s["b"].float()[ids]
+    scale = torch.where(s["ids_long"] >= 0, s["scale"][ids], 0.0)[:, None, None]
+    u = torch.bmm(g, b) * scale
+    gx = s["gx"].float() + _rows_of(torch.bmm(u, a), s["place"], S)
+    ga = torch.bmm(u.transpose(1, 2).contiguous(), x)
+    gb = torch.bmm(g.transpose(1, 2).contiguous(), z) * scale
+    # an adapter's gradient is the sum over the groups that use it
+    uses = (s["ids_long"][None, :] == torch.arange(n, device=ga.device)[:, None]).float()
+    ga = (uses @ ga.reshape(len(ga), -1)).reshape(s["a"].shape)
+    gb = (uses @ gb.reshape(len(gb), -1)).reshape(s["b"].shape)
     return gx.to(DTYPES[c["out"]]), ga, gb
 
 
