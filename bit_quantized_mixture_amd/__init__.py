@@ -20,6 +20,8 @@ __all__ = [
     "e4b_permute_workspace_bytes", "e4b_permute_tokens", "e4b_combine_workspace_bytes", "e4b_combine_tokens", "e4b_combine_tokens_backward",
     "LoraArgs", "LoraBackwardArgs", "e4b_lora_workspace_bytes", "e4b_grouped_lora",
     "e4b_lora_backward_workspace_bytes", "e4b_grouped_lora_backward",
+    "e4b_checkpoint_rows", "e4b_restore_rows", "e4b_glu", "e4b_glu_backward", "e4b_quantize_act_mxfp4",
+    "Mxfp4GemmArgs", "e4b_grouped_gemm_mxfp4",
 ]
 
 E4B_FMT_NF4, E4B_FMT_MXFP4 = 0, 1
@@ -29,7 +31,7 @@ E4B_ROUTE_RENORMALIZE = 1
 E4B_ACT_CLAMPED_GLU, E4B_GU_INTERLEAVED = 0x10, 0x20
 E4B_MXFP4_SCALED, E4B_MXFP4_FP16 = 0x40, 0x80
 E4B_COMBINE_ATOMIC = 0x100
-E4B_DT_BF16, E4B_DT_F32 = 0, 1
+E4B_DT_BF16, E4B_DT_F32, E4B_DT_I8 = 0, 1, 2
 _FMT = {"nf4": E4B_FMT_NF4, "mxfp4": E4B_FMT_MXFP4, E4B_FMT_NF4: E4B_FMT_NF4, E4B_FMT_MXFP4: E4B_FMT_MXFP4}
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -105,6 +107,14 @@ class LoraBackwardArgs(ctypes.Structure):
     ]
 
 
+class Mxfp4GemmArgs(ctypes.Structure):
+    """Mirror of struct e4b_mxfp4_gemm_args."""
+    _fields_ = [
+        ("out_dtype", _i32), ("reserved", _i32), ("E", _i64), ("N", _i64), ("K", _i64), ("S", _i64), ("x", _vp),
+        ("x_scales", _vp), ("w", _vp), ("w_scales", _vp), ("bias", _vp), ("expert_offsets", _vp), ("out", _vp),
+    ]
+
+
 def _decl(name, argtypes, restype=ctypes.c_int):
     fn = getattr(_lib, name)
     fn.argtypes = argtypes
@@ -141,6 +151,14 @@ _c_lora_ws = _decl("e4b_lora_workspace_bytes", [ctypes.POINTER(LoraArgs), ctypes
 _c_lora = _decl("e4b_grouped_lora", [ctypes.POINTER(LoraArgs), _vp])
 _c_lora_bwd_ws = _decl("e4b_lora_backward_workspace_bytes", [ctypes.POINTER(LoraBackwardArgs), ctypes.POINTER(_sz)])
 _c_lora_bwd = _decl("e4b_grouped_lora_backward", [ctypes.POINTER(LoraBackwardArgs), _vp])
+
+_c_lora_bwd_x8 = _decl("e4b_grouped_lora_backward_x8", [ctypes.POINTER(LoraBackwardArgs), _vp, _vp, _vp])
+_c_checkpoint = _decl("e4b_checkpoint_rows", [_vp, _i32, _i64, _i64, _vp, _vp, _vp])
+_c_restore = _decl("e4b_restore_rows", [_vp, _vp, _i64, _i64, _vp, _i32, _vp])
+_c_glu = _decl("e4b_glu", [_vp, _i32, _vp, _i64, _i64, _i32, _vp, _i32, _vp, _vp, _vp])
+_c_glu_bwd = _decl("e4b_glu_backward", [_vp, _i32, _vp, _i32, _vp, _i64, _i64, _i32, _vp, _i32, _vp])
+_c_quant_mxfp4 = _decl("e4b_quantize_act_mxfp4", [_vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp, _vp])
+_c_mxfp4_gemm = _decl("e4b_grouped_gemm_mxfp4", [ctypes.POINTER(Mxfp4GemmArgs), _vp])
 
 
 class E4BError(RuntimeError):
@@ -928,14 +946,15 @@ def e4b_lora_backward_workspace_bytes(S: int, K: int, N: int, r: int, groups: in
 
 
 def e4b_grouped_lora_backward(g, x, z, a, b, scale, group_offsets, group_adapter=None, gx_base=None, gx=None,
-                              ga=None, gb=None, dtype=torch.float32, ws=None, stream=None):
+                              ga=None, gb=None, dtype=torch.float32, ws=None, stream=None, x_scales=None):
     """Gradients of e4b_grouped_lora: (gx [S, K], ga [adapters, r, K], gb [adapters, N, r]).
 
     g [S, N] bf16: the gradient of out; x, a, b, scale, group_offsets, group_adapter as given to the
     forward call and z as it returned.  gx_base [S, K] bf16 or float32 (the base projection's
     gradient, e.g. of e4b_grouped_dgrad) is added to gx, which may be gx_base itself; gx is
     allocated in its dtype, else `dtype`.  gx, ga, gb: a tensor to fill, None to allocate it, False
-    where it is not wanted (x may be None without ga, z without gb).  ga and gb are float32.
+    where it is not wanted (x may be None without ga, z without gb).  ga and gb are float32.  x kept
+    in 8 bits: x the int8 codes and x_scales [S, K/32] uint8, as e4b_checkpoint_rows returns them.
     """
     _need(g, "g", _BF16)
     if g.dim() != 2:
@@ -950,7 +969,10 @@ def e4b_grouped_lora_backward(g, x, z, a, b, scale, group_offsets, group_adapter
         raise E4BError("e4b_grouped_lora_backward", -1)  # also without rows, where the C call has no gx to see
     if gx is False and gx_base is not None:
         raise ValueError("gx_base is only for gx")
-    if ga is not False:
+    if x_scales is not None and ga is not False:
+        _need(x, "x", (torch.int8,), (S, K), dev)
+        _need(x_scales, "x_scales", (torch.uint8,), (S, K // 32), dev)
+    elif ga is not False:
         _need(x, "x", _BF16, (S, K), dev)
         args.x = x.data_ptr()
     if gb is not False:
@@ -982,5 +1004,185 @@ def e4b_grouped_lora_backward(g, x, z, a, b, scale, group_offsets, group_adapter
         args.g = g.data_ptr()
         need = _ws_of(_c_lora_bwd_ws, "e4b_lora_backward_workspace_bytes", args) if ws is None else 0
         ws = _give_ws(st, ws, need, args, dev)
-        _check("e4b_grouped_lora_backward", _c_lora_bwd(ctypes.byref(args), _stream_on(dev, stream)))
+        if x_scales is not None and ga is not False:
+            _check("e4b_grouped_lora_backward_x8", _c_lora_bwd_x8(ctypes.byref(args), x.data_ptr(), x_scales.data_ptr(),
+                                                                  _stream_on(dev, stream)))
+        else:
+            _check("e4b_grouped_lora_backward", _c_lora_bwd(ctypes.byref(args), _stream_on(dev, stream)))
     return tuple(outs)
+
+
+def _rows8(st, codes, scales, S, C, dev):
+    """The codes and scales of an 8-bit checkpoint to fill: allocated where they are None."""
+    if codes is None:
+        codes = st.alloc((S, C), dtype=torch.int8, device=dev)
+    else:
+        _need(codes, "codes", (torch.int8,), (S, C), dev)
+    if scales is None:
+        scales = st.alloc((S, C // 32), dtype=torch.uint8, device=dev)
+    else:
+        _need(scales, "scales", (torch.uint8,), (S, C // 32), dev)
+    return codes, scales
+
+
+def e4b_checkpoint_rows(x, codes=None, scales=None, stream=None):
+    """Rows kept in 8 bits: x [S, C] bf16 or float32 -> (codes int8 [S, C], scales uint8 [S, C/32]).
+
+    Each 32 columns of a row share a power of two; a value is off by at most 1/127 of its block's
+    largest.  C % 32 == 0.  Read back by e4b_restore_rows, e4b_glu, e4b_glu_backward and
+    e4b_grouped_lora_backward (x_scales).
+    """
+    dt = _need_rows(x, "x")
+    S, C = x.shape
+    dev = x.device
+    with _on_device(dev, stream) as st:
+        codes, scales = _rows8(st, codes, scales, S, C, dev)
+        _check("e4b_checkpoint_rows", _c_checkpoint(x.data_ptr(), dt, S, C, codes.data_ptr(), scales.data_ptr(),
+                                                    _stream_on(dev, stream)))
+    return codes, scales
+
+
+def _need_rows8(codes, scales, name, device=None):
+    """(S, C) of an 8-bit checkpoint."""
+    _need(codes, name, (torch.int8,), None, device)
+    if codes.dim() != 2:
+        raise ValueError(f"{name} must be a matrix, got shape {tuple(codes.shape)}")
+    S, C = codes.shape
+    _need(scales, f"the scales of {name}", (torch.uint8,), (S, C // 32), codes.device)
+    return S, C
+
+
+def e4b_restore_rows(codes, scales, out=None, dtype=torch.bfloat16, stream=None):
+    """The rows that e4b_checkpoint_rows has kept, [S, C] of `dtype` (bf16 or float32, exact in both)."""
+    S, C = _need_rows8(codes, scales, "codes")
+    dev = codes.device
+    odt = _rows_dtype(dtype, "dtype") if out is None else _need_rows(out, "out", (S, C), dev)
+    with _on_device(dev, stream) as st:
+        if out is None:
+            out = st.alloc((S, C), dtype=dtype, device=dev)
+        _check("e4b_restore_rows", _c_restore(codes.data_ptr(), scales.data_ptr(), S, C, out.data_ptr(), odt,
+                                              _stream_on(dev, stream)))
+    return out
+
+
+def _glu_rows(rows, row_scales, act, interleaved):
+    """(S, I, e4b_dtype, scales' address, flags) of a glu call's rows."""
+    if act not in ("swiglu", "clamped_glu"):
+        raise ValueError(f"act must be 'swiglu' or 'clamped_glu', not {act!r}")
+    if row_scales is None:
+        dt, sp = _need_rows(rows, "rows"), None
+    else:
+        _need_rows8(rows, row_scales, "rows")
+        dt, sp = E4B_DT_I8, row_scales.data_ptr()
+    S, C = rows.shape
+    if C % 2:
+        raise ValueError(f"rows must be [S, 2I], got shape {tuple(rows.shape)}")
+    flags = (E4B_ACT_CLAMPED_GLU if act == "clamped_glu" else 0) | (E4B_GU_INTERLEAVED if interleaved else 0)
+    return S, C // 2, dt, sp, flags
+
+
+def e4b_glu(rows, row_scales=None, act="swiglu", interleaved=False, out=None, dtype=torch.bfloat16, checkpoint=False,
+            stream=None):
+    """The gated activation on rows: h = silu(gate) * up, or the clamped GLU of e4b_moe_forward.
+
+    rows [S, 2I] bf16 or float32 (I gates, then I ups; interleaved: pairs), or the int8 codes of
+    e4b_checkpoint_rows with their row_scales.  Returns (h [S, I] of `dtype`, checkpoint): with
+    checkpoint=True, or a pair of tensors to fill, the rows in 8 bits (codes, scales) for
+    e4b_glu_backward, else None.  I % 32 == 0 (interleaved: I % 16).
+    """
+    S, I, dt, sp, flags = _glu_rows(rows, row_scales, act, interleaved)
+    dev = rows.device
+    odt = _rows_dtype(dtype, "dtype") if out is None else _need_rows(out, "out", (S, I), dev)
+    keep = checkpoint is not False and checkpoint is not None
+    if keep and row_scales is not None:
+        raise ValueError("rows in 8 bits are their own checkpoint")
+    with _on_device(dev, stream) as st:
+        if out is None:
+            out = st.alloc((S, I), dtype=dtype, device=dev)
+        kept = _rows8(st, *((None, None) if checkpoint is True else checkpoint), S, 2 * I, dev) if keep else None
+        _check("e4b_glu", _c_glu(rows.data_ptr(), dt, sp, S, I, flags, out.data_ptr(), odt,
+                                 kept[0].data_ptr() if keep else None, kept[1].data_ptr() if keep else None,
+                                 _stream_on(dev, stream)))
+    return out, kept
+
+
+def e4b_glu_backward(g, rows, row_scales=None, act="swiglu", interleaved=False, out=None, dtype=torch.bfloat16,
+                     stream=None):
+    """The gradient of e4b_glu's rows: g [S, I] bf16 or float32 -> [S, 2I] of `dtype`, laid out as rows.
+
+    rows, row_scales, act, interleaved as given to e4b_glu, or the checkpoint that it returned.
+    """
+    S, I, dt, sp, flags = _glu_rows(rows, row_scales, act, interleaved)
+    dev = rows.device
+    gdt = _need_rows(g, "g", (S, I), dev)
+    odt = _rows_dtype(dtype, "dtype") if out is None else _need_rows(out, "out", (S, 2 * I), dev)
+    with _on_device(dev, stream) as st:
+        if out is None:
+            out = st.alloc((S, 2 * I), dtype=dtype, device=dev)
+        _check("e4b_glu_backward", _c_glu_bwd(g.data_ptr(), gdt, rows.data_ptr(), dt, sp, S, I, flags, out.data_ptr(),
+                                              odt, _stream_on(dev, stream)))
+    return out
+
+
+def e4b_quantize_act_mxfp4(x, sorted_slots=None, k: int = 1, blocks=None, scales=None, stream=None):
+    """Rows to MXFP4: x [T, K] bf16 or float32 -> (blocks uint8 [T*k, K/32, 16], scales uint8 [T*k, K/32]).
+
+    sorted_slots [T*k] int32 from e4b_route_permute: row p comes from x[sorted_slots[p] // k]; None:
+    the rows as they are (k = 1).  K % 32 == 0.  The left operand of e4b_grouped_gemm_mxfp4.
+    """
+    dt = _need_rows(x, "x")
+    T, K = x.shape
+    dev = x.device
+    if sorted_slots is None:
+        if k != 1:
+            raise ValueError(f"k = {k} rows for each token need sorted_slots")
+    else:
+        _need(sorted_slots, "sorted_slots", (torch.int32,), (T * k,), dev)
+    with _on_device(dev, stream) as st:
+        if blocks is None:
+            blocks = st.alloc((T * k, K // 32, 16), dtype=torch.uint8, device=dev)
+        else:
+            _need(blocks, "blocks", (torch.uint8,), (T * k, K // 32, 16), dev)
+        if scales is None:
+            scales = st.alloc((T * k, K // 32), dtype=torch.uint8, device=dev)
+        else:
+            _need(scales, "scales", (torch.uint8,), (T * k, K // 32), dev)
+        _check("e4b_quantize_act_mxfp4", _c_quant_mxfp4(
+            x.data_ptr(), dt, T, K, k, None if sorted_slots is None else sorted_slots.data_ptr(), blocks.data_ptr(),
+            scales.data_ptr(), _stream_on(dev, stream)))
+    return blocks, scales
+
+
+def e4b_grouped_gemm_mxfp4(x, x_scales, w, w_scales, expert_offsets, bias=None, out=None, dtype=torch.float32,
+                           stream=None):
+    """The rows of one projection of an MXFP4 stack: out[p] = W_e @ x[p] + bias[e] for expert e's rows.
+
+    x [S, K/32, 16] and x_scales [S, K/32] from e4b_quantize_act_mxfp4; w [E, N, K/32, 16] and w_scales
+    [E, N, K/32] from e4b_pack_mxfp4; expert_offsets [E+1] int32; bias [E, N] float32 or None.  Returns
+    out [S, N] of `dtype` (bf16 or float32); rows outside every group are not written.
+    """
+    u8 = (torch.uint8,)
+    _need(w, "w", u8)
+    if w.dim() != 4 or w.shape[3] != 16:
+        raise ValueError(f"w must be [E, N, K/32, 16], got shape {tuple(w.shape)}")
+    E, N, B, dev = w.shape[0], w.shape[1], w.shape[2], w.device
+    _need(w_scales, "w_scales", u8, (E, N, B), dev)
+    _need(x, "x", u8, device=dev)
+    S = x.shape[0] if x.dim() else 0
+    if x.shape != (S, B, 16):
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected [S, {B}, 16]")
+    _need(x_scales, "x_scales", u8, (S, B), dev)
+    _need(expert_offsets, "expert_offsets", (torch.int32,), (E + 1,), dev)
+    a = Mxfp4GemmArgs()
+    if bias is not None:
+        _need(bias, "bias", (torch.float32,), (E, N), dev)
+        a.bias = bias.data_ptr()
+    a.out_dtype = _rows_dtype(dtype, "dtype") if out is None else _need_rows(out, "out", (S, N), dev)
+    with _on_device(dev, stream) as st:
+        if out is None:
+            out = st.alloc((S, N), dtype=dtype, device=dev)
+        a.E, a.N, a.K, a.S = E, N, 32 * B, S
+        a.x, a.x_scales, a.w, a.w_scales = x.data_ptr(), x_scales.data_ptr(), w.data_ptr(), w_scales.data_ptr()
+        a.expert_offsets, a.out = expert_offsets.data_ptr(), out.data_ptr()
+        _check("e4b_grouped_gemm_mxfp4", _c_mxfp4_gemm(ctypes.byref(a), _stream_on(dev, stream)))
+    return out

@@ -11,7 +11,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 LIB = os.path.join(HERE, "libe4b.so")
 SOURCES = ["abi.hip", "pack.hip", "route.hip", "moe.hip", "gemv.hip", "dgrad.hip", "int4.hip", "probe.hip", "scaled.hip", "tokens.hip",
-           "lora.hip"]
+           "lora.hip", "act.hip", "mxrows.hip"]
 
 
 def hipcc() -> str:

@@ -310,6 +310,65 @@ int lora_backward_launch_of(const e4b_lora_backward_args* a, e4b::LoraBackwardLa
   return check_items(e4b::lora_backward_items(*L));
 }
 
+// The adapters' backward call, x in bf16 or (x8) in 8 bits.
+int lora_backward(const e4b_lora_backward_args* a, bool x8, const int8_t* codes, const uint8_t* scales, void* stream) {
+  e4b::LoraBackwardLaunch L;
+  int st = lora_backward_launch_of(a, &L);
+  if (st != E4B_OK) return st;
+  if (x8 && a->x) return E4B_ERR_ARG;
+  if (x8 && a->K % 32) return E4B_ERR_SHAPE;
+  L.x8 = codes;
+  L.x8_scales = scales;
+  const bool no_x = x8 ? !codes || !scales : !a->x;
+  // without rows gx is empty (its pointer may be NULL), and alone it asks for nothing
+  if (!a->gx && !a->ga && !a->gb) return a->S == 0 ? check_device() : E4B_ERR_ARG;
+  // without rows the inputs may be empty; the adapters' gradients are still written (zeros)
+  if (!a->group_offsets || !a->a || !a->b) return E4B_ERR_ARG;
+  if (a->S > 0 && (!a->g || (a->ga && no_x) || (a->gb && !a->z))) return E4B_ERR_ARG;
+  const void* ptrs[] = {a->g, a->x, a->z, a->a, a->b, a->scale, a->group_offsets, a->group_adapter,
+                        a->gx_base, a->gx, a->ga, a->gb, a->ws, codes, scales};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return E4B_ERR_ALIGN;
+  const size_t need = a->S > 0 ? e4b::lora_backward_ws_bytes(L) : 0;
+  if (need && !a->ws) return E4B_ERR_ARG;
+  if (need && a->ws_bytes < need) return E4B_ERR_WORKSPACE;
+  if ((st = check_device()) != E4B_OK) return st;
+  return launched(e4b::launch_lora_backward(L, (hipStream_t)stream));
+}
+
+// Rows in 8 bits.
+int check_rows8(int64_t S, int64_t C, int32_t dtype) {
+  if (S < 0 || C <= 0) return E4B_ERR_ARG;
+  if (C % 32) return E4B_ERR_SHAPE;
+  if (S > (int64_t(1) << 40) / C) return E4B_ERR_OVERFLOW;
+  return check_items(e4b::rows8_items(S, C, dtype));
+}
+
+int glu_launch_of(const void* rows, int32_t rows_dtype, const uint8_t* row_scales, int64_t S, int64_t I, int32_t flags,
+                  void* out, int32_t out_dtype, e4b::GluLaunch* L) {
+  if ((!dtype_ok(rows_dtype) && rows_dtype != E4B_DT_I8) || !dtype_ok(out_dtype)) return E4B_ERR_ARG;
+  if (flags & ~(E4B_ACT_CLAMPED_GLU | E4B_GU_INTERLEAVED)) return E4B_ERR_ARG;
+  if (S < 0 || I <= 0) return E4B_ERR_ARG;
+  L->interleaved = (flags & E4B_GU_INTERLEAVED) != 0;
+  if (I % (L->interleaved ? 16 : 32)) return E4B_ERR_SHAPE;
+  if (S > (int64_t(1) << 40) / I) return E4B_ERR_OVERFLOW;
+  L->clamped = (flags & E4B_ACT_CLAMPED_GLU) != 0;
+  L->S = S;
+  L->I = I;
+  L->rows_dtype = rows_dtype;
+  L->out_dtype = out_dtype;
+  L->rows = rows;
+  L->row_scales = row_scales;
+  L->out = out;
+  return check_items(e4b::glu_items(S, I, rows_dtype, L->interleaved));
+}
+
+// The pointers of a call with rows.
+int check_glu(const e4b::GluLaunch& L) {
+  if (!L.rows || !L.out || (L.rows_dtype == E4B_DT_I8) != (L.row_scales != nullptr)) return E4B_ERR_ARG;
+  return aligned16(L.rows) && aligned16(L.out) && aligned16(L.row_scales) ? E4B_OK : E4B_ERR_ALIGN;
+}
+
 }  // namespace
 
 extern "C" {
@@ -349,23 +408,112 @@ int e4b_lora_backward_workspace_bytes(const e4b_lora_backward_args* a, size_t* b
 }
 
 int e4b_grouped_lora_backward(const e4b_lora_backward_args* a, void* stream) {
-  e4b::LoraBackwardLaunch L;
-  int st = lora_backward_launch_of(a, &L);
+  return lora_backward(a, false, nullptr, nullptr, stream);
+}
+
+int e4b_grouped_lora_backward_x8(const e4b_lora_backward_args* a, const int8_t* x_codes, const uint8_t* x_scales,
+                                 void* stream) {
+  return lora_backward(a, true, x_codes, x_scales, stream);
+}
+
+int e4b_checkpoint_rows(const void* x, int32_t dtype, int64_t S, int64_t C, int8_t* codes, uint8_t* scales,
+                        void* stream) {
+  if (!dtype_ok(dtype)) return E4B_ERR_ARG;
+  int st = check_rows8(S, C, dtype);
   if (st != E4B_OK) return st;
-  // without rows gx is empty (its pointer may be NULL), and alone it asks for nothing
-  if (!a->gx && !a->ga && !a->gb) return a->S == 0 ? check_device() : E4B_ERR_ARG;
-  // without rows the inputs may be empty; the adapters' gradients are still written (zeros)
-  if (!a->group_offsets || !a->a || !a->b) return E4B_ERR_ARG;
-  if (a->S > 0 && (!a->g || (a->ga && !a->x) || (a->gb && !a->z))) return E4B_ERR_ARG;
-  const void* ptrs[] = {a->g, a->x, a->z, a->a, a->b, a->scale, a->group_offsets, a->group_adapter,
-                        a->gx_base, a->gx, a->ga, a->gb, a->ws};
+  if (S == 0) return check_device();
+  if (!x || !codes || !scales) return E4B_ERR_ARG;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return E4B_ERR_ALIGN;
+  if ((st = check_device()) != E4B_OK) return st;
+  return launched(e4b::launch_checkpoint(x, dtype, S * C, codes, scales, (hipStream_t)stream));
+}
+
+int e4b_restore_rows(const int8_t* codes, const uint8_t* scales, int64_t S, int64_t C, void* out, int32_t out_dtype,
+                     void* stream) {
+  if (!dtype_ok(out_dtype)) return E4B_ERR_ARG;
+  int st = check_rows8(S, C, E4B_DT_I8);
+  if (st != E4B_OK) return st;
+  if (S == 0) return check_device();
+  if (!codes || !scales || !out) return E4B_ERR_ARG;
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(out)) return E4B_ERR_ALIGN;
+  if ((st = check_device()) != E4B_OK) return st;
+  return launched(e4b::launch_restore(codes, scales, S * C, out, out_dtype, (hipStream_t)stream));
+}
+
+int e4b_glu(const void* rows, int32_t rows_dtype, const uint8_t* row_scales, int64_t S, int64_t I, int32_t flags,
+            void* h, int32_t h_dtype, int8_t* codes, uint8_t* scales, void* stream) {
+  e4b::GluLaunch L{};
+  int st = glu_launch_of(rows, rows_dtype, row_scales, S, I, flags, h, h_dtype, &L);
+  if (st != E4B_OK) return st;
+  if ((codes == nullptr) != (scales == nullptr) || (codes && rows_dtype == E4B_DT_I8)) return E4B_ERR_ARG;
+  if (S == 0) return check_device();
+  if ((st = check_glu(L)) != E4B_OK) return st;
+  if (!aligned16(codes) || !aligned16(scales)) return E4B_ERR_ALIGN;
+  L.codes = codes;
+  L.scales = scales;
+  if ((st = check_device()) != E4B_OK) return st;
+  return launched(e4b::launch_glu(L, (hipStream_t)stream));
+}
+
+int e4b_glu_backward(const void* g, int32_t g_dtype, const void* rows, int32_t rows_dtype, const uint8_t* row_scales,
+                     int64_t S, int64_t I, int32_t flags, void* g_rows, int32_t g_rows_dtype, void* stream) {
+  if (!dtype_ok(g_dtype)) return E4B_ERR_ARG;
+  e4b::GluLaunch L{};
+  int st = glu_launch_of(rows, rows_dtype, row_scales, S, I, flags, g_rows, g_rows_dtype, &L);
+  if (st != E4B_OK) return st;
+  if (S == 0) return check_device();
+  if (!g) return E4B_ERR_ARG;
+  if ((st = check_glu(L)) != E4B_OK) return st;
+  if (!aligned16(g)) return E4B_ERR_ALIGN;
+  L.g = g;
+  L.g_dtype = g_dtype;
+  if ((st = check_device()) != E4B_OK) return st;
+  return launched(e4b::launch_glu(L, (hipStream_t)stream));
+}
+
+int e4b_quantize_act_mxfp4(const void* x, int32_t dtype, int64_t T, int64_t K, int32_t k, const int32_t* sorted_slots,
+                           uint8_t* blocks, uint8_t* scales, void* stream) {
+  if (!dtype_ok(dtype)) return E4B_ERR_ARG;
+  if (!sorted_slots && k != 1 && T != 0) return E4B_ERR_ARG;
+  int st = check_tokens(T, K, k);
+  if (st != E4B_OK) return st;
+  if (K % 32) return E4B_ERR_SHAPE;
+  if ((st = check_items(e4b::quantize_mxfp4_items(T * k, K))) != E4B_OK) return st;
+  if (T == 0) return check_device();
+  if (!x || !blocks || !scales) return E4B_ERR_ARG;
+  if (!aligned16(x) || !aligned16(sorted_slots) || !aligned16(blocks) || !aligned16(scales)) return E4B_ERR_ALIGN;
+  if ((st = check_device()) != E4B_OK) return st;
+  return launched(e4b::launch_quantize_mxfp4(x, dtype, T, K, k, sorted_slots, blocks, scales, (hipStream_t)stream));
+}
+
+int e4b_grouped_gemm_mxfp4(const e4b_mxfp4_gemm_args* a, void* stream) {
+  if (!a || a->reserved != 0 || !dtype_ok(a->out_dtype)) return E4B_ERR_ARG;
+  if (a->E <= 0 || a->N <= 0 || a->K <= 0 || a->S < 0) return E4B_ERR_ARG;
+  if (a->K % 32) return E4B_ERR_SHAPE;
+  const int64_t lim = int64_t(1) << 31, wide = int64_t(1) << 23;
+  if (a->S >= lim || a->K > wide || a->N > wide || a->E > e4b::kLoraGroups) return E4B_ERR_OVERFLOW;
+  e4b::MxGemmLaunch L{};
+  L.E = a->E;
+  L.N = a->N;
+  L.K = a->K;
+  L.S = a->S;
+  L.out_dtype = a->out_dtype;
+  L.x = a->x;
+  L.xs = a->x_scales;
+  L.w = a->w;
+  L.ws = a->w_scales;
+  L.bias = a->bias;
+  L.offsets = a->expert_offsets;
+  L.out = a->out;
+  int st = check_items(e4b::mxfp4_gemm_items(L));
+  if (st != E4B_OK) return st;
+  if (a->S == 0) return check_device();
+  if (!a->x || !a->x_scales || !a->w || !a->w_scales || !a->expert_offsets || !a->out) return E4B_ERR_ARG;
+  const void* ptrs[] = {a->x, a->x_scales, a->w, a->w_scales, a->bias, a->expert_offsets, a->out};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return E4B_ERR_ALIGN;
-  const size_t need = a->S > 0 ? e4b::lora_backward_ws_bytes(L) : 0;
-  if (need && !a->ws) return E4B_ERR_ARG;
-  if (need && a->ws_bytes < need) return E4B_ERR_WORKSPACE;
   if ((st = check_device()) != E4B_OK) return st;
-  return launched(e4b::launch_lora_backward(L, (hipStream_t)stream));
+  return launched(e4b::launch_mxfp4_gemm(L, (hipStream_t)stream));
 }
 
 int e4b_permute_workspace_bytes(int32_t dtype, int64_t T, int64_t H, int32_t k, size_t* bytes) {

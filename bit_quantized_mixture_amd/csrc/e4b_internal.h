@@ -222,6 +222,8 @@ struct LoraBackwardLaunch {
   int gx_dtype;
   const uint16_t* g;
   const uint16_t* x;
+  const int8_t* x8;        // in x's place: its 8-bit checkpoint
+  const uint8_t* x8_scales;
   const float* z;
   const uint16_t* a;
   const uint16_t* b;
@@ -239,6 +241,43 @@ int64_t lora_items(const LoraLaunch& L);
 int64_t lora_backward_items(const LoraBackwardLaunch& L);
 hipError_t launch_lora(const LoraLaunch& L, hipStream_t stream);
 hipError_t launch_lora_backward(const LoraBackwardLaunch& L, hipStream_t stream);
+
+// Rows in 8 bits and the gated activation (act.hip).  Row types: e4b_dtype values, 2 the 8-bit form.
+hipError_t launch_checkpoint(const void* x, int dtype, int64_t n, int8_t* codes, uint8_t* scales, hipStream_t stream);
+hipError_t launch_restore(const int8_t* codes, const uint8_t* scales, int64_t n, void* out, int out_dtype,
+                          hipStream_t stream);
+struct GluLaunch {
+  int64_t S, I;
+  int rows_dtype, g_dtype, out_dtype;
+  bool clamped, interleaved;
+  const void* rows;
+  const uint8_t* row_scales;  // of 8-bit rows
+  const void* g;              // nullable: the forward
+  void* out;
+  int8_t* codes;              // nullable
+  uint8_t* scales;
+};
+hipError_t launch_glu(const GluLaunch& L, hipStream_t stream);
+int64_t rows8_items(int64_t S, int64_t C, int dtype);
+int64_t glu_items(int64_t S, int64_t I, int rows_dtype, bool interleaved);
+
+// Rows in MXFP4 and their products with an MXFP4 stack (mxrows.hip).
+hipError_t launch_quantize_mxfp4(const void* x, int dtype, int64_t T, int64_t K, int k, const int32_t* slots,
+                                 uint8_t* blocks, uint8_t* scales, hipStream_t stream);
+int64_t quantize_mxfp4_items(int64_t S, int64_t K);
+struct MxGemmLaunch {
+  int64_t E, N, K, S;
+  int out_dtype;
+  const uint8_t* x;
+  const uint8_t* xs;
+  const uint8_t* w;
+  const uint8_t* ws;
+  const float* bias;          // nullable [E, N]
+  const int32_t* offsets;
+  void* out;
+};
+hipError_t launch_mxfp4_gemm(const MxGemmLaunch& L, hipStream_t stream);
+int64_t mxfp4_gemm_items(const MxGemmLaunch& L);
 
 // Streaming read (mode 0; dst: NULL or a 4-byte sink that is never written in practice) or
 // copy (mode 1) of `bytes` (a multiple of 16) with cus * 8 workgroups.

@@ -95,4 +95,58 @@ __device__ __forceinline__ void store_vec(float* p, const float (&v)[V]) {
     __builtin_nontemporal_store(f32x4{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]}, reinterpret_cast<f32x4_any*>(p + 4 * i));
 }
 
+// The same for a lane's 2, 4 or 8 columns (aligned to as many elements).
+template <int V>
+__device__ __forceinline__ void load_short(const uint16_t* p, float (&v)[V]) {
+  if constexpr (V == 8) {
+    load_once<8>(p, v);
+  } else {
+    uint32_t q[V / 2];
+    if constexpr (V == 4) {
+      const u32x2 w = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
+      q[0] = w[0];
+      q[1] = w[1];
+    } else {
+      q[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
+    }
+#pragma unroll
+    for (int i = 0; i < V / 2; ++i) {
+      v[2 * i] = __uint_as_float(q[i] << 16);
+      v[2 * i + 1] = __uint_as_float(q[i] & 0xFFFF0000u);
+    }
+  }
+}
+template <int V>
+__device__ __forceinline__ void load_short(const float* p, float (&v)[V]) {
+  if constexpr (V >= 4) {
+    load_once<V>(p, v);
+  } else {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    const f32x2 w = __builtin_nontemporal_load(reinterpret_cast<const f32x2*>(p));
+    v[0] = w[0];
+    v[1] = w[1];
+  }
+}
+template <int V>
+__device__ __forceinline__ void store_short(uint16_t* p, const float (&v)[V]) {
+  if constexpr (V >= 4) store_vec<V>(p, v);
+  else __builtin_nontemporal_store(bf16_rne2(v[0], v[1]), reinterpret_cast<uint32_t*>(p));
+}
+template <int V>
+__device__ __forceinline__ void store_short(float* p, const float (&v)[V]) {
+  if constexpr (V >= 4) {
+    store_vec<V>(p, v);
+  } else {
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    __builtin_nontemporal_store(f32x2{v[0], v[1]}, reinterpret_cast<f32x2*>(p));
+  }
+}
+
+// What a block of an 8-bit checkpoint multiplies its codes by: 2^(byte - 133), NaN for byte 255.  The
+// products with int8 codes are bf16 values.
+__device__ __forceinline__ float scale8(uint32_t byte) {
+  const float s = __uint_as_float(byte >= 7u ? (byte - 6u) << 23 : 0x10000u << byte);  // below 2^-126: subnormal
+  return byte == 255u ? __uint_as_float(0x7FC00000u) : s;
+}
+
 }  // namespace e4b

@@ -14,6 +14,7 @@
 // and u are float32 all the way: in expand each is cut into three bf16 parts (8 + 8 + 8 bits of
 // its 24-bit significand: no rounding) that stand behind one another in the contraction, and so in
 // grad.
+#include "e4b_groups.h"
 #include "e4b_internal.h"
 #include "e4b_rows.h"
 
@@ -25,64 +26,6 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kThreads = 256;
 constexpr int kWaves = kThreads / kWave;
-
-struct RowTile {
-  int adapter;     // -1: none
-  int64_t row0;
-  int rows;        // 1 .. bm; 0: no such tile
-};
-
-// Inclusive sum over the wave's lanes in six steps of the vector unit: shifts by 1, 2, 4 and 8 in
-// each row of 16 lanes, then a row's last lane onto the next row, and lane 31 onto the upper half.
-__device__ __forceinline__ int wave_scan(int x) {
-  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);
-  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
-  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
-  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
-  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);
-  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
-  return x;
-}
-
-// Rows lo .. hi of group g, clamped to the S rows there are and to ascending order.
-__device__ __forceinline__ void group_rows(const int32_t* __restrict__ offsets, int g, int S, int* lo, int* hi) {
-  const int a = offsets[g], b = offsets[g + 1];
-  *lo = a < 0 ? 0 : (a > S ? S : a);
-  *hi = b < *lo ? *lo : (b > S ? S : b);
-}
-
-__device__ __forceinline__ int adapter_of(const int32_t* __restrict__ ids, int group, int n) {
-  const int a = ids ? ids[group] : group;
-  return a >= 0 && a < n ? a : -1;
-}
-
-// Tile `tile` of the list that cuts every group into pieces of 1 << bm_log2 rows, found by each
-// wave from the offsets, 64 groups a step (their adapters are read beside them: one latency, not two).
-__device__ __forceinline__ RowTile find_tile(const int32_t* __restrict__ offsets, const int32_t* __restrict__ ids,
-                                             int n_adapters, int G, int S, int bm_log2, uint32_t tile) {
-  const int lane = threadIdx.x & (kWave - 1);
-  int base = 0;
-  for (int g0 = 0; g0 < G; g0 += kWave) {
-    int lo = 0, hi = 0, a = -1;
-    if (g0 + lane < G) {
-      group_rows(offsets, g0 + lane, S, &lo, &hi);
-      a = adapter_of(ids, g0 + lane, n_adapters);
-    }
-    const int n = int((int64_t(hi) - lo + (1 << bm_log2) - 1) >> bm_log2);
-    const int ni = wave_scan(n);
-    const int total = __builtin_amdgcn_readlane(ni, kWave - 1);
-    if (int(tile) - base < total) {
-      const int l = __ffsll((unsigned long long)__ballot(int(tile) - base < ni)) - 1;
-      const int at = int(tile) - base - (__builtin_amdgcn_readlane(ni, l) - __builtin_amdgcn_readlane(n, l));
-      if (at < 0 || at >= __builtin_amdgcn_readlane(n, l)) break;  // sums of offsets that descend can wrap
-      const int row0 = __builtin_amdgcn_readlane(lo, l) + (at << bm_log2);
-      const int left = __builtin_amdgcn_readlane(hi, l) - row0;
-      return RowTile{__builtin_amdgcn_readlane(a, l), row0, left < (1 << bm_log2) ? left : (1 << bm_log2)};
-    }
-    base += total;
-  }
-  return RowTile{-1, 0, 0};
-}
 
 // Loads and stores go through buffers that end with the tile's rows or the adapter's matrix: a
 // lane's offset is fixed for the tile, the step's offset is scalar, and what lies past the end
@@ -612,6 +555,8 @@ __device__ __forceinline__ GradTile find_grad_tile(const int32_t* __restrict__ o
 struct GradArgs {
   const float* v;         // [S, r]: z or u (read for grad)
   const uint16_t* m;      // [S, C]: g or x
+  const int8_t* m8;       // x in 8 bits, in m's place: [S, C] codes
+  const uint8_t* m8s;     // and [S, C/32] exponent bytes
   const uint16_t* w;      // [n, C, r]: B, for u
   const float* scale;     // nullable: 1; of grad and of u
   const int32_t* offsets;
@@ -660,7 +605,8 @@ __device__ __forceinline__ s16x4 lds_read_tr(const uint8_t* at) {
 // round of workgroups that ends with the longest group, four or five blocks one after the other.
 // One pass instead of two reads m once: 8192 rows of 28672 took 387 us for all gradients with a pass
 // each for u and grad (and float32 matrix instructions), 191 so.
-template <int RT, int NSUB, bool UP, bool BYCOL>
+// With M8 m comes as an 8-bit checkpoint: its blocks are bf16 values exactly, and are put into LDS as such.
+template <int RT, int NSUB, bool UP, bool BYCOL, bool M8>
 __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
   constexpr int kVStride = kGradRows + 8;               // v^T row in bf16
   constexpr int kWCols = kGradCols * NSUB, kWStride = kWCols + 8;
@@ -688,17 +634,49 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
   // The block's loads: thread i of row i / 32 takes piece i % 32 of every 8th row.  Offsets are
   // taken from the block's first row, so they stay small however long the tile is.
   const int prow = tid >> 5, piece = tid & 31;
-  auto load_block = [&](int row, int sub, u32x4 (&v)[8]) {
-    const uint16_t* at = p.m + (int64_t(t.row0) + row) * p.C;
+  struct Block {
+    u32x4 v[M8 ? 4 : 8];    // M8: the codes of passes 2 j and 2 j + 1
+    uint32_t s[M8 ? 8 : 1]; // and their bytes
+  };
+  auto load_block = [&](int row, int sub, Block& b) {
     const int left = t.rows - row;
-    const __amdgpu_buffer_rsrc_t res =
-        wave_rsrc(at, left > 0 ? uint32_t(left < kGradRows ? left : kGradRows) * p.C * 2u : 0u);
+    const uint32_t n = left > 0 ? uint32_t(left < kGradRows ? left : kGradRows) : 0u;
     const uint32_t col = col0 + kGradCols * sub + 8 * piece;
+    // read once, past the caches (gate_up gradients 199 us kept, 190 so)
+    if constexpr (M8) {
+      const int64_t first = int64_t(t.row0) + row;
+      const __amdgpu_buffer_rsrc_t res = wave_rsrc(p.m8 + first * p.C, n * p.C);
+      const __amdgpu_buffer_rsrc_t sres = wave_rsrc(p.m8s + first * (p.C >> 5), n * (p.C >> 5));
 #pragma unroll
-    for (int j = 0; j < 8; ++j)  // read once, past the caches (gate_up gradients 199 us kept, 190 so)
-      v[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
-                                           res, col < p.C ? (prow * p.C + col) * 2u : kNowhere, 16u * j * p.C,
-                                           kPastCaches));
+      for (int j = 0; j < 8; ++j) {
+        const u32x2 q = __builtin_bit_cast(u32x2, __builtin_amdgcn_raw_buffer_load_b64(
+                                                      res, col < p.C ? prow * p.C + col : kNowhere, 8u * j * p.C, kPastCaches));
+        b.v[j >> 1][2 * (j & 1)] = q[0];
+        b.v[j >> 1][2 * (j & 1) + 1] = q[1];
+        b.s[j] = __builtin_amdgcn_raw_buffer_load_b8(sres, col < p.C ? (prow * p.C + col) >> 5 : kNowhere, 8u * j * (p.C >> 5), 0);
+      }
+    } else {
+      const __amdgpu_buffer_rsrc_t res = wave_rsrc(p.m + (int64_t(t.row0) + row) * p.C, n * p.C * 2u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        b.v[j] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                               res, col < p.C ? (prow * p.C + col) * 2u : kNowhere, 16u * j * p.C,
+                                               kPastCaches));
+    }
+  };
+  auto block_piece = [&](const Block& b, int j) {
+    if constexpr (M8) {
+      const float sc8 = scale8(b.s[j] & 255u);
+      u32x4 o;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t q = b.v[j >> 1][2 * (j & 1) + (w >> 1)] >> (16 * (w & 1));
+        o[w] = hi2(__float_as_uint(float(int(int8_t(q))) * sc8), __float_as_uint(float(int(int8_t(q >> 8))) * sc8));
+      }
+      return o;
+    } else {
+      return b.v[j];
+    }
   };
   // v of a block: two rows of one rank a thread and turn.
   constexpr int kVTurns = kGradRows / 2 * 16 * RT / kThreads;
@@ -739,7 +717,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
   };
   constexpr int kUSteps = RT <= 2 ? 4 : (RT == 4 ? 2 : 1);  // steps of u whose fragments are read together
 
-  u32x4 mv[8];
+  Block mv;
   float vv[kVTurns][2];
   load_v(0, vv);
   load_block(0, 0, mv);
@@ -762,7 +740,7 @@ __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
     for (int sub = 0; sub < NSUB; ++sub) {
       __syncthreads();  // the last block has been read
 #pragma unroll
-      for (int j = 0; j < 8; ++j) *reinterpret_cast<u32x4*>(lds + block_at(prow + 8 * j, piece)) = mv[j];
+      for (int j = 0; j < 8; ++j) *reinterpret_cast<u32x4*>(lds + block_at(prow + 8 * j, piece)) = block_piece(mv, j);
       if (sub == 0 && grad) {
 #pragma unroll
         for (int j = 0; j < kVTurns; ++j) {
@@ -1152,21 +1130,29 @@ hipError_t expand(const LoraGroups& q, const float* z, int pieces, const uint16_
   return hipGetLastError();
 }
 
-template <bool UP, bool BYCOL>
+template <bool UP, bool BYCOL, bool M8>
 void grad_rt(const GradArgs& a, unsigned grid, hipStream_t s) {
-  if (a.r <= 16) hipLaunchKernelGGL((grad_kernel<1, UP ? 2 : 1, UP, BYCOL>), dim3(grid), dim3(kThreads), 0, s, a);
-  else if (a.r <= 32) hipLaunchKernelGGL((grad_kernel<2, 1, UP, BYCOL>), dim3(grid), dim3(kThreads), 0, s, a);
-  else if (a.r <= 64) hipLaunchKernelGGL((grad_kernel<4, 1, UP, BYCOL>), dim3(grid), dim3(kThreads), 0, s, a);
-  else hipLaunchKernelGGL((grad_kernel<8, 1, UP, BYCOL>), dim3(grid), dim3(kThreads), 0, s, a);
+  if (a.r <= 16) hipLaunchKernelGGL((grad_kernel<1, UP ? 2 : 1, UP, BYCOL, M8>), dim3(grid), dim3(kThreads), 0, s, a);
+  else if (a.r <= 32) hipLaunchKernelGGL((grad_kernel<2, 1, UP, BYCOL, M8>), dim3(grid), dim3(kThreads), 0, s, a);
+  else if (a.r <= 64) hipLaunchKernelGGL((grad_kernel<4, 1, UP, BYCOL, M8>), dim3(grid), dim3(kThreads), 0, s, a);
+  else hipLaunchKernelGGL((grad_kernel<8, 1, UP, BYCOL, M8>), dim3(grid), dim3(kThreads), 0, s, a);
 }
 
+// Rows as bf16, or in 8 bits.
+struct GradRows {
+  const uint16_t* m;
+  const int8_t* m8;
+  const uint8_t* m8s;
+};
 // The gradient pass over m: grad (nullable) from v, and with upart also u.
-hipError_t grad_pass(const LoraGroups& q, const float* v, const uint16_t* m, const uint16_t* w, const float* scale,
+hipError_t grad_pass(const LoraGroups& q, const float* v, const GradRows& m, const uint16_t* w, const float* scale,
                      int64_t C, bool by_column, float* grad, float* parts, float* upart, hipStream_t s) {
   const bool up = upart != nullptr;
   GradArgs a{};
   a.v = v;
-  a.m = m;
+  a.m = m.m;
+  a.m8 = m.m8;
+  a.m8s = m.m8s;
   a.w = w;
   a.scale = scale;
   a.offsets = q.offsets;
@@ -1184,9 +1170,10 @@ hipError_t grad_pass(const LoraGroups& q, const float* v, const uint16_t* m, con
   a.chunks = uint32_t(div_up(C, kGradCols * grad_subs(q.r, up)));
   const unsigned grid = unsigned(grad_tiles_bound(q, a.most) * a.chunks);
   if (grid) {
-    if (up) grad_rt<true, true>(a, grid, s);
-    else if (by_column) grad_rt<false, true>(a, grid, s);
-    else grad_rt<false, false>(a, grid, s);
+    if (up) grad_rt<true, true, false>(a, grid, s);
+    else if (by_column) grad_rt<false, true, false>(a, grid, s);
+    else if (a.m8) grad_rt<false, false, true>(a, grid, s);
+    else grad_rt<false, false, false>(a, grid, s);
     if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
   }
   return hipSuccess;
@@ -1316,7 +1303,7 @@ hipError_t launch_lora_backward(const LoraBackwardLaunch& L, hipStream_t stream)
   hipError_t e = hipSuccess;
   if (q.S > 0) {
     float* upart = need_u ? reinterpret_cast<float*>(ws + w.upart) : nullptr;
-    if ((e = grad_pass(q, L.z, L.g, L.b, L.scale, q.N, true, L.gb, parts_b, upart, stream)) != hipSuccess) return e;
+    if ((e = grad_pass(q, L.z, {L.g, nullptr, nullptr}, L.b, L.scale, q.N, true, L.gb, parts_b, upart, stream)) != hipSuccess) return e;
     if (need_u) {
       uint16_t* at = L.gx ? reinterpret_cast<uint16_t*>(ws + w.at) : nullptr;
       const int64_t u_blocks = between_u_blocks(q);
@@ -1330,7 +1317,7 @@ hipError_t launch_lora_backward(const LoraBackwardLaunch& L, hipStream_t stream)
         if (e != hipSuccess) return e;
       }
       if (L.ga) {
-        e = grad_pass(q, u, L.x, nullptr, nullptr, q.K, false, L.ga, parts_a, nullptr, stream);
+        e = grad_pass(q, u, {L.x, L.x8, L.x8_scales}, nullptr, nullptr, q.K, false, L.ga, parts_a, nullptr, stream);
         if (e != hipSuccess) return e;
       }
     }

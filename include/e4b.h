@@ -22,8 +22,11 @@
  * the grouped product on the same packed stacks (e4b_grouped_dgrad), an int4-b32
  * routed decode GEMV with exact integer block sums (e4b_pack_int4_b32, e4b_gemv_int4_b32),
  * token rows to expert order and back with their gradients (e4b_permute_tokens,
- * e4b_combine_tokens, e4b_combine_tokens_backward), and low-rank adapters on grouped rows with
- * theirs (e4b_grouped_lora, e4b_grouped_lora_backward).
+ * e4b_combine_tokens, e4b_combine_tokens_backward), low-rank adapters on grouped rows with
+ * theirs (e4b_grouped_lora, e4b_grouped_lora_backward), the rows of one MXFP4 projection
+ * (e4b_quantize_act_mxfp4, e4b_grouped_gemm_mxfp4), the activation on rows with its gradient (e4b_glu,
+ * e4b_glu_backward), and rows kept in 8 bits for the backward pass (e4b_checkpoint_rows,
+ * e4b_restore_rows).
  *
  * Conventions shared by every entry point
  *   - All tensor pointers are DEVICE pointers, owned by the caller, row-major and dense.
@@ -81,8 +84,9 @@ typedef enum e4b_status {
   E4B_ERR_TOO_LARGE = -8    /* more workspace than e4b_moe_forward_noalloc's fixed scratch */
 } e4b_status;
 
-/* Element type of a row matrix in the calls that take either. */
-typedef enum e4b_dtype { E4B_DT_BF16 = 0, E4B_DT_F32 = 1 } e4b_dtype;
+/* Element type of a row matrix in the calls that take either.  E4B_DT_I8, the codes of
+ * e4b_checkpoint_rows, only where a call says so. */
+typedef enum e4b_dtype { E4B_DT_BF16 = 0, E4B_DT_F32 = 1, E4B_DT_I8 = 2 } e4b_dtype;
 
 typedef enum e4b_fmt { E4B_FMT_NF4 = 0, E4B_FMT_MXFP4 = 1 } e4b_fmt;
 
@@ -472,6 +476,106 @@ int e4b_lora_backward_workspace_bytes(const e4b_lora_backward_args* a, size_t* b
  * Synchronous errors as e4b_moe_forward.
  */
 int e4b_grouped_lora_backward(const e4b_lora_backward_args* a, void* stream);
+
+/*
+ * e4b_grouped_lora_backward_x8 — e4b_grouped_lora_backward with x kept in 8 bits by
+ * e4b_checkpoint_rows.  The codes stand for bf16 values exactly and enter ga as those.
+ *   a         as for e4b_grouped_lora_backward, with a->x = NULL and K % 32 == 0; the same workspace.
+ *   x_codes   [S, K] int8, x_scales [S, K/32] uint8 (read for ga).
+ */
+int e4b_grouped_lora_backward_x8(const e4b_lora_backward_args* a, const int8_t* x_codes,
+                                 const uint8_t* x_scales, void* stream);
+
+/*
+ * e4b_checkpoint_rows — rows kept in 8 bits until the backward pass needs them.  Each 32 consecutive
+ * columns of a row share a power of two: with X = floor(log2(amax)), one more where the largest would
+ * round to 128 steps, q = rint(v * 2^(6 - X)) (ties to even) and v' = q * 2^(X - 6).
+ *   x       [S, C] of `dtype`.  C % 32 == 0.  S*C < 2^34 (bf16: 2^35).
+ *   codes   [S, C] int8 out, in [-127, 127].
+ *   scales  [S, C/32] uint8 out: X + 127 (0 for blocks below 2^-126).  255 for a block that holds a NaN or
+ *           an infinity: all of it is read as NaN.
+ * Off by half a step 2^(X - 7) at most, 1/127 of the block's largest; a block whose largest is
+ * 2^127 * 255/128 or more saturates at 127 * 2^121.  Bit-exact and deterministic.  No output overlaps an input, here and in the calls below.
+ */
+int e4b_checkpoint_rows(const void* x, int32_t dtype, int64_t S, int64_t C, int8_t* codes, uint8_t* scales,
+                        void* stream);
+
+/*
+ * e4b_restore_rows — the rows that e4b_checkpoint_rows has kept: out[s, c] = q * 2^(X - 6).
+ *   out     [S, C] of out_dtype out.  Exact in both types.
+ */
+int e4b_restore_rows(const int8_t* codes, const uint8_t* scales, int64_t S, int64_t C, void* out,
+                     int32_t out_dtype, void* stream);
+
+/*
+ * e4b_glu — the gated activation between the two products, on rows that carry both (bitsandbytes pull
+ * request #1984, Design: per-expert SwiGLU MLP): h = silu(G) * U, or with E4B_ACT_CLAMPED_GLU
+ * h = min(G,7) * sigmoid(1.702 * min(G,7)) * (clamp(U,-7,7) + 1).
+ *   rows        [S, 2I] of rows_dtype: I gates, then I ups; E4B_GU_INTERLEAVED: gate j at 2j, up j at
+ *               2j+1.  I % 32 == 0 (interleaved: I % 16).  S*I < 2^33.  E4B_DT_I8: codes of e4b_checkpoint_rows,
+ *   row_scales  and their scales [S, 2I/32]; NULL for the other types.
+ *   flags       E4B_ACT_CLAMPED_GLU | E4B_GU_INTERLEAVED, as for e4b_moe_forward.
+ *   h           [S, I] of h_dtype out, computed in float32 and rounded once.  NaN in a row's pair gives NaN.
+ *   codes, scales  NULL, or the checkpoint of `rows` as e4b_checkpoint_rows makes it, out (not with
+ *               E4B_DT_I8 rows).
+ */
+int e4b_glu(const void* rows, int32_t rows_dtype, const uint8_t* row_scales, int64_t S, int64_t I,
+            int32_t flags, void* h, int32_t h_dtype, int8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * e4b_glu_backward — the gradient of e4b_glu's rows, with s the logistic function:
+ *   silu      g_gate = g * U * s(G) * (1 + G * (1 - s(G))),   g_up = g * G * s(G)
+ *   clamped   with Gc = min(G,7), Uc = clamp(U,-7,7), t = 1.702 * Gc:
+ *             g_gate = g * (Uc + 1) * s(t) * (1 + t * (1 - s(t))) where G <= 7, else 0,
+ *             g_up = g * Gc * s(t) where |U| <= 7, else 0.
+ *   g        [S, I] of g_dtype: the gradient of h.
+ *   rows, row_scales, flags  as for e4b_glu; after e4b_glu with a checkpoint, its codes and scales.
+ *   g_rows   [S, 2I] of g_rows_dtype out, in the layout of `rows`.
+ */
+int e4b_glu_backward(const void* g, int32_t g_dtype, const void* rows, int32_t rows_dtype,
+                     const uint8_t* row_scales, int64_t S, int64_t I, int32_t flags, void* g_rows,
+                     int32_t g_rows_dtype, void* stream);
+
+/*
+ * e4b_quantize_act_mxfp4 — rows to MXFP4, the left operand of e4b_grouped_gemm_mxfp4, by the rule of
+ * e4b_pack_mxfp4; with sorted_slots gathered to expert order on the way.
+ *   x             [T, K] of `dtype`.  K % 32 == 0.  1 <= k <= 64, T*k < 2^31.  T*k*K < 2^35.
+ *   sorted_slots  [T*k] int32 from e4b_route_permute: row p comes from x[sorted_slots[p] / k]; a slot
+ *                 outside [0, T*k) leaves a row of zeros.  NULL: the rows as they are (k = 1).
+ *   blocks        [T*k, K/32, 16] uint8 out; scales [T*k, K/32] uint8 out, as e4b_pack_mxfp4 has them.
+ *                 A block that holds a NaN or an infinity gets scale 255 (e8m0's NaN).
+ * Bit-exact and deterministic.
+ */
+int e4b_quantize_act_mxfp4(const void* x, int32_t dtype, int64_t T, int64_t K, int32_t k,
+                           const int32_t* sorted_slots, uint8_t* blocks, uint8_t* scales, void* stream);
+
+/* Arguments of e4b_grouped_gemm_mxfp4.  K % 32 == 0; any N >= 1; E <= 65536; S < 2^31, K and N <= 2^23. */
+typedef struct e4b_mxfp4_gemm_args {
+  int32_t out_dtype;      /* e4b_dtype of out */
+  int32_t reserved;       /* must be 0 */
+  int64_t E, N, K;        /* MXFP4 stack [E, N, K] (e4b_pack_mxfp4) */
+  int64_t S;              /* grouped rows */
+  const uint8_t* x;       /* [S, K/32, 16] rows from e4b_quantize_act_mxfp4 */
+  const uint8_t* x_scales; /* [S, K/32] */
+  const uint8_t* w;       /* [E, N, K/32, 16] */
+  const uint8_t* w_scales; /* [E, N, K/32] */
+  const float* bias;      /* [E, N] float32, or NULL */
+  const int32_t* expert_offsets; /* [E+1]: rows of expert e are offsets[e] .. offsets[e+1]-1, ascending; clamped
+                           * to [0, S] */
+  void* out;              /* [S, N] of out_dtype out */
+} e4b_mxfp4_gemm_args;
+
+/*
+ * e4b_grouped_gemm_mxfp4 — the rows of one projection of an MXFP4 stack, for the adapters to add to
+ * and the activation to read: out[p, :] = W_e x[p] + bias[e] for every row p of expert e, both operands as
+ * their codes stand (grouped-nf4-gemm 0.25.0 project description, opening section: MXFP4 on the
+ * released bytes).  Products are exact, sums float32 (past its range infinite, below
+ * 2^-126 possibly 0), out is rounded once.  Deterministic.  A scale of 255 makes
+ * its row (or its column) NaN.  Rows outside every group are left as they were.  The gradient of the rows
+ * that were quantised is e4b_grouped_dgrad's (the rounding passed over).  A dense layer is E = 1.
+ * out overlaps no input.  Synchronous errors as e4b_moe_forward.
+ */
+int e4b_grouped_gemm_mxfp4(const e4b_mxfp4_gemm_args* a, void* stream);
 
 /*
  * e4b_pack_int4_b32 — round-to-nearest int4-b32 packing of bf16 stacks (grouped-nf4-gemm
