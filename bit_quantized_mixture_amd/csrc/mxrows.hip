@@ -150,22 +150,23 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t uniform_rsrc(const void* base,
 typedef u32x4 u32x4_byte __attribute__((aligned(1)));
 
 // 16 exponent bytes of a row from block `first` on, zeros behind its last (nb in all).  A row of bytes starts
-// anywhere; no byte outside it is read.
+// anywhere; no byte outside it is read: the last ones come with those before them, and are moved down.
 __device__ __forceinline__ u32x4 load_bytes16(const uint8_t* __restrict__ row, int first, int nb) {
-  if (first + 16 <= nb) return *reinterpret_cast<const u32x4_byte*>(row + first);
+  return *reinterpret_cast<const u32x4_byte*>(row + (first + 16 <= nb ? first : nb - 16));
+}
+__device__ __forceinline__ u32x4 bytes_from(u32x4 v, int first, int nb) {
+  const int down = first + 16 <= nb ? 0 : first + 16 - nb;
+  if (down & 8) v = u32x4{v[2], v[3], 0u, 0u};
+  if (down & 4) v = u32x4{v[1], v[2], v[3], 0u};
+  const uint32_t by = uint32_t(down & 3);
+  return u32x4{__builtin_amdgcn_alignbyte(v[1], v[0], by), __builtin_amdgcn_alignbyte(v[2], v[1], by),
+               __builtin_amdgcn_alignbyte(v[3], v[2], by), __builtin_amdgcn_alignbyte(0u, v[3], by)};
+}
+// The same for a row of fewer than 16.
+__device__ __forceinline__ u32x4 load_few_bytes(const uint8_t* __restrict__ row, int nb) {
   u32x4 v = {};
-  if (first >= nb) return v;
-  if (nb >= 16) {  // the row's last 16, moved down
-    v = *reinterpret_cast<const u32x4_byte*>(row + nb - 16);
-    const int down = first + 16 - nb;
-    if (down & 8) v = u32x4{v[2], v[3], 0u, 0u};
-    if (down & 4) v = u32x4{v[1], v[2], v[3], 0u};
-    const uint32_t by = uint32_t(down & 3);
-    return u32x4{__builtin_amdgcn_alignbyte(v[1], v[0], by), __builtin_amdgcn_alignbyte(v[2], v[1], by),
-                 __builtin_amdgcn_alignbyte(v[3], v[2], by), __builtin_amdgcn_alignbyte(0u, v[3], by)};
-  }
 #pragma unroll
-  for (int j = 0; j < 15; ++j)  // first is 0
+  for (int j = 0; j < 15; ++j)
     if (j < nb) v[j >> 2] |= uint32_t(row[j]) << (8 * (j & 3));
   return v;
 }
@@ -183,9 +184,9 @@ __global__ void __launch_bounds__(WR * WC * kWave) tile_kernel(GemmArgs p) {
   constexpr int kT = WR * WC * kWave, kW = WR * WC;
   constexpr int BM = 32 * RB * WR, BN = 32 * CB * WC, kRows = BM + BN;
   constexpr int kBmLog2 = BM == 256 ? 8 : (BM == 128 ? 7 : (BM == 64 ? 6 : 5));
-  constexpr int kStage = kRows * 128, kBytes = kRows * 16;
   constexpr int kUnits = kRows / 8 / kW;           // copies of a wave and chunk
-  constexpr int kTurns = (kRows + kT - 1) / kT;    // rows of bytes a thread has
+  constexpr int kTurns = (kRows + kT - 1) / kT;    // rows of bytes a thread has (some past the last)
+  constexpr int kStage = kRows * 128, kBytes = kTurns * kT * 16;
   static_assert((kRows / 8) % kW == 0 && BM % 16 == 0, "copies");
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage + 2 * kBytes];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -209,15 +210,12 @@ __global__ void __launch_bounds__(WR * WC * kWave) tile_kernel(GemmArgs p) {
     const int last = (r < BM ? t.rows : cols) - 1, own = r < BM ? r : r - BM;
     src[i] = uint32_t(own < last ? own : last) * rowb + 16u * piece_of(unit);
   }
-  const auto copy = [&](int chunk) {
-    uint8_t* dst = lds + (chunk & 1) * kStage;
+  // A copy of a chunk that does not exist reads one place again, into a stage that nothing reads.
+  const auto copy_unit = [&](int chunk, int i) {
     const int left = nb - 8 * chunk;  // blocks of the row from here on
-#pragma unroll
-    for (int i = 0; i < kUnits; ++i) {
-      const int unit = wave * kUnits + i, past = left < 8 ? piece_of(unit) - (left - 1) : 0;
-      const uint32_t at = src[i] - (past > 0 ? 16u * past : 0u);
-      dma16(8 * unit < BM ? xres : wres, at, 128u * chunk, dst + 1024 * unit);
-    }
+    const int unit = wave * kUnits + i, past = left < 8 ? piece_of(unit) - (left - 1) : 0;
+    const uint32_t at = left > 0 ? src[i] - (past > 0 ? 16u * past : 0u) : 0u;
+    dma16(8 * unit < BM ? xres : wres, at, left > 0 ? 128u * chunk : 0u, lds + (chunk & 1) * kStage + 1024 * unit);
   };
   const uint8_t* srow[kTurns];
 #pragma unroll
@@ -226,96 +224,135 @@ __global__ void __launch_bounds__(WR * WC * kWave) tile_kernel(GemmArgs p) {
     srow[i] = (r < BM ? p.xs + t.row0 * nb : p.ws + wrow0 * nb) + int64_t(own < last ? own : last) * nb;
   }
   u32x4 sreg[kTurns];
-  const auto load_scales = [&](int window) {
+  const auto load_scales = [&](int window) {  // past the last window: the last again, unused
+    const int first = 16 * window < nb ? 16 * window : (nb - 1) & ~15;
 #pragma unroll
-    for (int i = 0; i < kTurns; ++i)
-      if (tid + i * kT < kRows) sreg[i] = load_bytes16(srow[i], 16 * window, nb);
+    for (int i = 0; i < kTurns; ++i) sreg[i] = load_bytes16(srow[i], first, nb);
+  };
+  const auto put = [&](int window, int i, u32x4 v) {
+    *reinterpret_cast<u32x4*>(lds + 2 * kStage + (window & 1) * kBytes + 16 * (tid + i * kT)) =
+        u32x4{perm(v[1], v[0], 0x06040200u), perm(v[1], v[0], 0x07050301u), perm(v[3], v[2], 0x06040200u),
+              perm(v[3], v[2], 0x07050301u)};
   };
   const auto put_scales = [&](int window) {
-    uint8_t* dst = lds + 2 * kStage + (window & 1) * kBytes;
 #pragma unroll
-    for (int i = 0; i < kTurns; ++i) {
-      const u32x4 v = sreg[i];
-      if (tid + i * kT < kRows)
-        *reinterpret_cast<u32x4*>(dst + 16 * (tid + i * kT)) =
-            u32x4{perm(v[1], v[0], 0x06040200u), perm(v[1], v[0], 0x07050301u), perm(v[3], v[2], 0x06040200u),
-                  perm(v[3], v[2], 0x07050301u)};
-    }
+    for (int i = 0; i < kTurns; ++i) put(window, i, bytes_from(sreg[i], 16 * window, nb));
   };
 
   const int row_a = 32 * RB * (wave / WC), row_b = BM + 32 * CB * (wave % WC);
   struct Frags {
     u32x4 a[RB], b[CB];
   };
-  struct Scales {
+  struct Bytes {
     uint32_t a[RB], b[CB];
   };
   const auto frag = [&](const uint8_t* stage, int row, int s) {
     return *reinterpret_cast<const u32x4*>(stage + 128 * row + 16 * ((2 * s + half) ^ ((row >> 1) & 7)));
   };
-  const auto read = [&](int chunk, int s, Frags& f) {
+  // Part i of RB of a step's fragments, and of a chunk's bytes.
+  const auto read = [&](int chunk, int s, Frags& f, int i) {
     const uint8_t* stage = lds + (chunk & 1) * kStage;
+    f.a[i] = frag(stage, row_a + 32 * i + c, s);
 #pragma unroll
-    for (int i = 0; i < RB; ++i) f.a[i] = frag(stage, row_a + 32 * i + c, s);
-#pragma unroll
-    for (int i = 0; i < CB; ++i) f.b[i] = frag(stage, row_b + 32 * i + c, s);
+    for (int j = i * CB / RB; j < (i + 1) * CB / RB; ++j) f.b[j] = frag(stage, row_b + 32 * j + c, s);
   };
-  const auto read_scales = [&](int chunk, Scales& f) {
+  const auto read_bytes = [&](int chunk, Bytes& f, int i) {
     const uint8_t* from = lds + 2 * kStage + ((chunk >> 1) & 1) * kBytes + 8 * (chunk & 1) + 4 * half;
+    f.a[i] = *reinterpret_cast<const uint32_t*>(from + 16 * (row_a + 32 * i + c));
 #pragma unroll
-    for (int i = 0; i < RB; ++i) f.a[i] = *reinterpret_cast<const uint32_t*>(from + 16 * (row_a + 32 * i + c));
-#pragma unroll
-    for (int i = 0; i < CB; ++i) f.b[i] = *reinterpret_cast<const uint32_t*>(from + 16 * (row_b + 32 * i + c));
+    for (int j = i * CB / RB; j < (i + 1) * CB / RB; ++j)
+      f.b[j] = *reinterpret_cast<const uint32_t*>(from + 16 * (row_b + 32 * j + c));
   };
   f32x16 acc[RB][CB] = {};
-  const auto multiply = [&](auto step, const Frags& f, const Scales& sc) {
+  // The products of a step; `beside(i)` issues reads and copies before row i's, to run under them.
+  const auto multiply = [&](auto step, const Frags& f, const Bytes& by, auto&& beside) {
     constexpr int s = decltype(step)::value;
 #pragma unroll
-    for (int i = 0; i < RB; ++i)
+    for (int i = 0; i < RB; ++i) {
+      beside(i);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int j = 0; j < CB; ++j)
         acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand4(f.a[i]), operand4(f.b[j]), acc[i][j], 4, 4, s,
-                                                                    int(sc.a[i]), s, int(sc.b[j]));
+                                                                    int(by.a[i]), s, int(by.b[j]));
+      __builtin_amdgcn_sched_barrier(0);
+    }
   };
   using S0 = std::integral_constant<int, 0>;
   using S1 = std::integral_constant<int, 1>;
   using S2 = std::integral_constant<int, 2>;
   using S3 = std::integral_constant<int, 3>;
-
-  copy(0);
-  load_scales(0);
-  put_scales(0);
-  if (chunks > 2) load_scales(1);
-  Frags f0, f1;
-  Scales sc, before;
-  for (int k = 0; k < chunks; ++k) {
-    // chunk k has landed and everyone is done with the stage that chunk k + 1 goes to
+  constexpr int kPer = (kUnits + 2 * RB - 1) / (2 * RB);  // copies beside a row, over two steps
+  const auto copies = [&](int chunk, int part) {
+#pragma unroll
+    for (int u = part * kPer; u < (part + 1) * kPer; ++u)
+      if (u < kUnits) copy_unit(chunk, u);
+  };
+  const auto sync = [&] {  // a chunk has landed, and everyone is done with the stage of the one before
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-    if (k + 1 < chunks) copy(k + 1);
-    const int steps = (nb - 8 * k + 1) >> 1;  // 1 .. 4 in the last chunk, more before it
-    read(k, 0, f0);
-    read_scales(k, sc);
-    __builtin_amdgcn_sched_barrier(0);
-    if (k > 0) multiply(S3{}, f1, before);
-    if (steps > 1) read(k, 1, f1);
-    __builtin_amdgcn_sched_barrier(0);
-    multiply(S0{}, f0, sc);
-    if (steps > 2) read(k, 2, f0);
-    __builtin_amdgcn_sched_barrier(0);
-    if (steps > 1) multiply(S1{}, f1, sc);
-    if (steps > 3) read(k, 3, f1);
-    if ((k & 1) && k + 1 < chunks) {
-      put_scales((k + 1) >> 1);
-      if (k + 3 < chunks) load_scales((k + 3) >> 1);
-    }
-    __builtin_amdgcn_sched_barrier(0);
-    if (steps > 2) multiply(S2{}, f0, sc);
-    before = sc;
-    if (k + 1 == chunks && steps > 3) multiply(S3{}, f1, sc);
+  };
+  const auto nothing = [](int) {};
+
+#pragma unroll
+  for (int u = 0; u < kUnits; ++u) copy_unit(0, u);
+  if (nb >= 16) {
+    load_scales(0);
+    put_scales(0);
+    load_scales(1);
+  } else {
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) put(0, i, load_few_bytes(srow[i], nb));
   }
+  Frags f0, f1;
+  Bytes even, odd;
+  sync();
+#pragma unroll
+  for (int i = 0; i < RB; ++i) {
+    read(0, 0, f0, i);
+    read_bytes(0, even, i);
+    if (chunks > 1) copies(1, i);
+  }
+  // A chunk that is not the last, up to its last step, under which the next one's first fragments are read.  No
+  // branch inside: the compiler moves products over one.
+  const auto body = [&](auto is_odd, auto copy_on, int k, const Bytes& by, Bytes& next) {
+    multiply(S0{}, f0, by, [&](int i) {
+      read(k, 1, f1, i);
+      copies(k + 1, RB + i);
+    });
+    multiply(S1{}, f1, by, [&](int i) { read(k, 2, f0, i); });
+    multiply(S2{}, f0, by, [&](int i) {
+      read(k, 3, f1, i);
+      if (decltype(is_odd)::value && i == 0) put_scales((k + 1) >> 1);
+    });
+    sync();
+    multiply(S3{}, f1, by, [&](int i) {
+      read(k + 1, 0, f0, i);
+      read_bytes(k + 1, next, i);
+      if (decltype(copy_on)::value) copies(k + 2, i);
+      if (decltype(is_odd)::value && i == 0) load_scales((k + 3) >> 1);  // two chunks until it is put
+    });
+  };
+  using Yes = std::true_type;
+  using No = std::false_type;
+  int k = 0;
+  for (; k + 2 < chunks; k += 2) {
+    body(No{}, Yes{}, k, even, odd);
+    body(Yes{}, Yes{}, k + 1, odd, even);
+  }
+  if (k + 1 < chunks) {
+    body(No{}, No{}, k, even, odd);
+    even = odd;
+    ++k;
+  }
+  const int steps = (nb - 8 * k + 1) >> 1;  // of the last chunk
+  multiply(S0{}, f0, even, [&](int i) { read(k, 1, f1, i); });
+  if (steps > 1) multiply(S1{}, f1, even, [&](int i) { read(k, 2, f0, i); });
+  if (steps > 2) multiply(S2{}, f0, even, [&](int i) { read(k, 3, f1, i); });
+  if (steps > 3) multiply(S3{}, f1, even, nothing);
+  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));  // no copy is left when the LDS is given back
 
   // out: element r of a block is row 8 (r / 4) + 4 half + r % 4, column c
   typedef row_elem<ODT> out_t;
