@@ -77,17 +77,17 @@ struct GemmArgs {
 typedef int v8i __attribute__((ext_vector_type(8)));
 __device__ __forceinline__ v8i operand4(u32x4 a) { return v8i{int(a[0]), int(a[1]), int(a[2]), int(a[3]), 0, 0, 0, 0}; }
 
-// A wave's tile in a launch that cuts every expert's rows into pieces of 1 << bm_log2 and its columns into
-// `cols`: the row tiles of an expert stand in bands of up to kBand, a band's column after column, so that
-// neighbours share both operands.  The workgroups are dealt to the XCDs in contiguous stretches of that
-// list (workgroup b runs on XCD b % 8), each with an L2 cache of its own.
+// The tiles of a launch: every expert's rows cut into pieces of 1 << bm_log2 and its columns into `cols`.  The
+// row tiles of an expert stand in bands of up to kBand, a band's column after column, so that neighbours
+// share both operands.  The XCDs, each with an L2 cache of its own, have contiguous stretches of that list, and
+// the workgroups of an XCD (workgroup b runs on XCD b % 8) take its stretch in turn.
 struct GemmTile {
   int expert;
   int64_t row0;
   int rows;        // 0: no such tile
   uint32_t col;
 };
-constexpr int kBand = 4;
+constexpr int kBand = 8;
 
 __device__ __forceinline__ GemmTile find_gemm_tile(const int32_t* __restrict__ offsets, int E, int S, int bm_log2,
                                                    uint32_t cols, uint32_t block) {
@@ -103,11 +103,10 @@ __device__ __forceinline__ GemmTile find_gemm_tile(const int32_t* __restrict__ o
     int l, h;
     all += uint32_t(__builtin_amdgcn_readlane(wave_scan(tiles_at(g0, &l, &h)), kWave - 1));
   }
-  const uint64_t total = all * cols;
-  if (block >= total) return GemmTile{0, 0, 0, 0};
-  const uint32_t xcd = block & 7u, per = uint32_t(total >> 3), rest = uint32_t(total & 7u);
-  const uint32_t at = xcd * per + (xcd < rest ? xcd : rest) + (block >> 3);
-  const uint32_t row_tile = at / cols;
+  all *= cols;
+  if (block >= all) return GemmTile{0, 0, 0, 0};
+  const uint32_t xcd = block & 7u, per = uint32_t(all >> 3), rest = uint32_t(all & 7u);
+  const uint32_t id = xcd * per + (xcd < rest ? xcd : rest) + (block >> 3), row_tile = id / cols;
   uint32_t base = 0;
   for (int g0 = 0; g0 < E; g0 += kWave) {
     if (g0 > 0) {
@@ -116,17 +115,17 @@ __device__ __forceinline__ GemmTile find_gemm_tile(const int32_t* __restrict__ o
     }
     const uint32_t sum = uint32_t(__builtin_amdgcn_readlane(ni, kWave - 1));
     if (row_tile - base < sum) {
-      const int l = __ffsll((unsigned long long)__ballot(row_tile - base < uint32_t(ni))) - 1;
-      const uint32_t m = uint32_t(__builtin_amdgcn_readlane(n, l));
-      const uint32_t first = base + uint32_t(__builtin_amdgcn_readlane(ni, l)) - m;
-      const uint32_t within = at - first * cols, band = within / (kBand * cols);
+      const int k = __ffsll((unsigned long long)__ballot(row_tile - base < uint32_t(ni))) - 1;
+      const uint32_t m = uint32_t(__builtin_amdgcn_readlane(n, k));
+      const uint32_t first = base + uint32_t(__builtin_amdgcn_readlane(ni, k)) - m;
+      const uint32_t within = id - first * cols, band = within / (kBand * cols);
       if (m == 0 || band * kBand >= m) break;  // sums of offsets that descend can wrap
-      const uint32_t rows_of_band = m - band * kBand < kBand ? m - band * kBand : kBand;
-      const uint32_t in_band = within - band * kBand * cols, col = in_band / rows_of_band;
+      const uint32_t high = m - band * kBand < kBand ? m - band * kBand : kBand;
+      const uint32_t in_band = within - band * kBand * cols, col = in_band / high;
       if (col >= cols) break;
-      const uint32_t t = band * kBand + (in_band - col * rows_of_band);
-      const int row0 = __builtin_amdgcn_readlane(lo, l) + int(t << bm_log2), left = __builtin_amdgcn_readlane(hi, l) - row0;
-      return GemmTile{g0 + l, row0, left < bm ? left : bm, col};
+      const uint32_t t = band * kBand + (in_band - col * high);
+      const int row0 = __builtin_amdgcn_readlane(lo, k) + int(t << bm_log2), left = __builtin_amdgcn_readlane(hi, k) - row0;
+      return GemmTile{g0 + k, row0, left < bm ? left : bm, col};
     }
     base += sum;
   }
@@ -171,29 +170,44 @@ __device__ __forceinline__ u32x4 load_few_bytes(const uint8_t* __restrict__ row,
   return v;
 }
 
-// The tile form.  A workgroup has BM rows of an expert by BN columns, its WR by WC waves RB by CB blocks of
-// 32 by 32 each.  K goes in chunks of 8 blocks (128 bytes of a row), copied straight into LDS, one chunk
-// ahead: a copy instruction has 8 whole rows' pieces, a row's 16-byte piece p at place p ^ ((row >> 1) & 7),
-// so that the 16 rows of a read spread over all banks.  Step s of a chunk takes blocks 2 s and 2 s + 1, a
-// lane half one each.  Exponent bytes come for 16 blocks at a time through registers, sorted so that a
-// lane's four of a chunk are one word, whose byte s the instruction picks.  What stands behind the last
-// block is another block of the row under bytes of 0: 2^-254 times something finite.  Fragments are read one step ahead
-// of their products, over the chunk's barrier too.
+// Rows are stored past the caches (the instruction's non-temporal bit), which keeps the L2 caches for the
+// operands: 2048 tokens of the 32-expert layer's gate_up rows 169 us kept, 153 so; 8168 rows of 64 experts at
+// [4096, 1536] 74 and 62.
+constexpr int kPastCaches = 2;
+
+// Keeps the products of a row of blocks where they are written: without it the compiler gathers a loop's
+// products behind all its reads.  There is no instruction in it, so nothing reads the sums here.
+template <int N>
+__device__ __forceinline__ void hold(f32x16 (&v)[N]) {
+#if defined(__HIP_DEVICE_COMPILE__)
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+a"(v[i]));
+#endif
+}
+
+// The tile form.  A workgroup has up to 32 RB WR rows of an expert by 32 CB WC columns; its WR by WC waves have
+// every WR-th block of 32 rows and 32 CB columns each.  A tile of fewer rows runs the form for as many blocks as
+// it has: what is left of an expert's rows behind whole tiles costs little more than its columns' bytes.
+// K goes in chunks of 8 blocks (128 bytes of a row), copied straight into a ring of stages in LDS: a copy
+// instruction has 8 whole rows' pieces, and a row's 16-byte piece p is at place p ^ ((row >> 1) & 7), so that the
+// 16 rows of a read spread over all banks.  Step s of a chunk takes blocks 2 s and 2 s + 1, a lane half one
+// each.  Exponent bytes come through registers for a window of 16 blocks at a time, sorted so that a lane's eight
+// of a window are two words, whose bytes the instruction picks.  Fragments are read a step ahead of their
+// products, over the chunk's barrier too.
 template <int ODT, int RB, int CB, int WR, int WC>
-__global__ void __launch_bounds__(WR * WC * kWave) tile_kernel(GemmArgs p) {
-  constexpr int kT = WR * WC * kWave, kW = WR * WC;
-  constexpr int BM = 32 * RB * WR, BN = 32 * CB * WC, kRows = BM + BN;
-  constexpr int kBmLog2 = BM == 256 ? 8 : (BM == 128 ? 7 : (BM == 64 ? 6 : 5));
-  constexpr int kUnits = kRows / 8 / kW;           // copies of a wave and chunk
-  constexpr int kTurns = (kRows + kT - 1) / kT;    // rows of bytes a thread has (some past the last)
-  constexpr int kStage = kRows * 128, kBytes = kTurns * kT * 16;
-  static_assert((kRows / 8) % kW == 0 && BM % 16 == 0, "copies");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * kStage + 2 * kBytes];
+__global__ void __launch_bounds__(WR * WC * kWave, 2) tile_kernel(GemmArgs p) {
+  constexpr int kW = WR * WC, kT = kW * kWave, CH = 8;
+  constexpr int BM = 32 * RB * WR, BN = 32 * CB * WC, kRowBytes = 16 * CH, kEvery = 8 * kW;
+  constexpr int kBmLog2 = BM == 256 ? 8 : (BM == 128 ? 7 : 6);
+  constexpr int kRing = 2 * (BM + BN) * kRowBytes;
+  constexpr int kTurns = (BM + BN + kT - 1) / kT;  // rows of bytes a thread has (some past the last)
+  static_assert(BM % kEvery == 0 && BN % kEvery == 0 && kEvery % 32 == 0, "copies");
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kRing + kTurns * kT * 16];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, half = lane >> 5;
   const GemmTile t = find_gemm_tile(p.offsets, p.E, p.S, kBmLog2, p.col_tiles, blockIdx.x);
   if (t.rows == 0) return;
-  const int nb = int(p.K >> 5), chunks = (nb + 7) >> 3;
+  const int nb = int(p.K >> 5), windows = (nb + 15) >> 4;
   const uint32_t rowb = uint32_t(nb) * 16u;
   const int64_t n0 = int64_t(t.col) * BN;
   const int cols = p.N - n0 < BN ? int(p.N - n0) : BN;
@@ -201,202 +215,254 @@ __global__ void __launch_bounds__(WR * WC * kWave) tile_kernel(GemmArgs p) {
   const __amdgpu_buffer_rsrc_t xres = uniform_rsrc(p.x + t.row0 * rowb, uint32_t(t.rows) * rowb);
   const __amdgpu_buffer_rsrc_t wres = uniform_rsrc(p.w + wrow0 * rowb, uint32_t(cols) * rowb);
 
-  // copies: unit u has rows 8 u .. of x (then of w), lane l place l % 8 of row l / 8
-  uint32_t src[kUnits];
-  const auto piece_of = [&](int unit) { return (lane & 7) ^ ((4 * unit + (lane >> 4)) & 7); };
-#pragma unroll
-  for (int i = 0; i < kUnits; ++i) {
-    const int unit = wave * kUnits + i, r = 8 * unit + (lane >> 3);
-    const int last = (r < BM ? t.rows : cols) - 1, own = r < BM ? r : r - BM;
-    src[i] = uint32_t(own < last ? own : last) * rowb + 16u * piece_of(unit);
-  }
-  // A copy of a chunk that does not exist reads one place again, into a stage that nothing reads.
-  const auto copy_unit = [&](int chunk, int i) {
-    const int left = nb - 8 * chunk;  // blocks of the row from here on
-    const int unit = wave * kUnits + i, past = left < 8 ? piece_of(unit) - (left - 1) : 0;
-    const uint32_t at = left > 0 ? src[i] - (past > 0 ? 16u * past : 0u) : 0u;
-    dma16(8 * unit < BM ? xres : wres, at, left > 0 ? 128u * chunk : 0u, lds + (chunk & 1) * kStage + 1024 * unit);
+  // copies: unit u has LDS rows 8 u .. (w's, then x's), lane l place l % 8 of row l / 8; a wave takes every kW-th
+  // unit, so that a lane's units are whole numbers of rows apart.  A wave's 32 CB columns are dealt out to its
+  // blocks in turn, so that a lane ends with CB neighbouring columns.
+  const auto col_of = [](int r) { return (r & ~(32 * CB - 1)) + CB * (r & 31) + ((r >> 5) & (CB - 1)); };
+  const int own_row = 8 * wave + (lane >> 3);
+  const uint32_t own = 16u * ((lane & 7) ^ ((own_row >> 1) & 7));
+  const uint32_t x_own = uint32_t(own_row) * rowb + own, w_own = uint32_t(col_of(own_row)) * rowb + own;
+  constexpr int kUnitsW = BN / kEvery;
+  // Copy i of a chunk into the stage at `stage`.  The buffers end with the tile's rows: nothing is fetched for what
+  // stands behind them, nor for a chunk that does not exist (a row's blocks behind its last are the next
+  // row's, under bytes of 0: 2^-254 times something finite).
+  const auto copy_unit = [&](int chunk, int stage, int i) {
+    const uint32_t from = chunk * CH < nb ? uint32_t(kRowBytes * chunk) : 0x80000000u;
+    const uint32_t rows = i < kUnitsW ? col_of(i * kEvery) : (i - kUnitsW) * kEvery;
+    dma16(i < kUnitsW ? wres : xres, (i < kUnitsW ? w_own : x_own) + (from + rows * rowb), 0u,
+          lds + stage + 1024 * (i * kW + wave));
   };
   const uint8_t* srow[kTurns];
+  u32x4 sreg[kTurns];
 #pragma unroll
   for (int i = 0; i < kTurns; ++i) {
-    const int r = tid + i * kT, last = (r < BM ? t.rows : cols) - 1, own = r < BM ? r : r - BM;
-    srow[i] = (r < BM ? p.xs + t.row0 * nb : p.ws + wrow0 * nb) + int64_t(own < last ? own : last) * nb;
+    const int r = tid + i * kT < BM + BN ? tid + i * kT : 0;
+    const int last = (r < BN ? cols : t.rows) - 1, row = r < BN ? col_of(r) : r - BN;
+    srow[i] = (r < BN ? p.ws + wrow0 * nb : p.xs + t.row0 * nb) + int64_t(row < last ? row : last) * nb;
   }
-  u32x4 sreg[kTurns];
   const auto load_scales = [&](int window) {  // past the last window: the last again, unused
     const int first = 16 * window < nb ? 16 * window : (nb - 1) & ~15;
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) sreg[i] = load_bytes16(srow[i], first, nb);
   };
-  const auto put = [&](int window, int i, u32x4 v) {
-    *reinterpret_cast<u32x4*>(lds + 2 * kStage + (window & 1) * kBytes + 16 * (tid + i * kT)) =
-        u32x4{perm(v[1], v[0], 0x06040200u), perm(v[1], v[0], 0x07050301u), perm(v[3], v[2], 0x06040200u),
+  const auto put = [&](int i, u32x4 v) {  // even blocks' bytes, then odd blocks'
+    *reinterpret_cast<u32x4*>(lds + kRing + 16 * (tid + i * kT)) =
+        u32x4{perm(v[1], v[0], 0x06040200u), perm(v[3], v[2], 0x06040200u), perm(v[1], v[0], 0x07050301u),
               perm(v[3], v[2], 0x07050301u)};
   };
   const auto put_scales = [&](int window) {
 #pragma unroll
-    for (int i = 0; i < kTurns; ++i) put(window, i, bytes_from(sreg[i], 16 * window, nb));
+    for (int i = 0; i < kTurns; ++i) put(i, bytes_from(sreg[i], 16 * window, nb));
   };
 
-  const int row_a = 32 * RB * (wave / WC), row_b = BM + 32 * CB * (wave % WC);
-  struct Frags {
-    u32x4 a[RB], b[CB];
-  };
-  struct Bytes {
-    uint32_t a[RB], b[CB];
-  };
-  const auto frag = [&](const uint8_t* stage, int row, int s) {
-    return *reinterpret_cast<const u32x4*>(stage + 128 * row + 16 * ((2 * s + half) ^ ((row >> 1) & 7)));
-  };
-  // Part i of RB of a step's fragments, and of a chunk's bytes.
-  const auto read = [&](int chunk, int s, Frags& f, int i) {
-    const uint8_t* stage = lds + (chunk & 1) * kStage;
-    f.a[i] = frag(stage, row_a + 32 * i + c, s);
-#pragma unroll
-    for (int j = i * CB / RB; j < (i + 1) * CB / RB; ++j) f.b[j] = frag(stage, row_b + 32 * j + c, s);
-  };
-  const auto read_bytes = [&](int chunk, Bytes& f, int i) {
-    const uint8_t* from = lds + 2 * kStage + ((chunk >> 1) & 1) * kBytes + 8 * (chunk & 1) + 4 * half;
-    f.a[i] = *reinterpret_cast<const uint32_t*>(from + 16 * (row_a + 32 * i + c));
-#pragma unroll
-    for (int j = i * CB / RB; j < (i + 1) * CB / RB; ++j)
-      f.b[j] = *reinterpret_cast<const uint32_t*>(from + 16 * (row_b + 32 * j + c));
-  };
-  f32x16 acc[RB][CB] = {};
-  // The products of a step; `beside(i)` issues reads and copies before row i's, to run under them.
-  const auto multiply = [&](auto step, const Frags& f, const Bytes& by, auto&& beside) {
-    constexpr int s = decltype(step)::value;
-#pragma unroll
-    for (int i = 0; i < RB; ++i) {
-      beside(i);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int j = 0; j < CB; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand4(f.a[i]), operand4(f.b[j]), acc[i][j], 4, 4, s,
-                                                                    int(by.a[i]), s, int(by.b[j]));
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  };
-  using S0 = std::integral_constant<int, 0>;
-  using S1 = std::integral_constant<int, 1>;
-  using S2 = std::integral_constant<int, 2>;
-  using S3 = std::integral_constant<int, 3>;
-  constexpr int kPer = (kUnits + 2 * RB - 1) / (2 * RB);  // copies beside a row, over two steps
-  const auto copies = [&](int chunk, int part) {
-#pragma unroll
-    for (int u = part * kPer; u < (part + 1) * kPer; ++u)
-      if (u < kUnits) copy_unit(chunk, u);
-  };
-  const auto sync = [&] {  // a chunk has landed, and everyone is done with the stage of the one before
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-  };
-  const auto nothing = [](int) {};
+  const int wave_row = wave / WC, wave_col = wave % WC;
+  // (2 s + half) ^ swap = (half ^ swap) ^ 2 s, and a row's place is a multiple of 128.
+  const uint32_t place = kRowBytes * c + 16u * (half ^ ((c >> 1) & 7));
+  const uint32_t b_place = place + 32 * CB * kRowBytes * wave_col, a_place = place + (BN + 32 * wave_row) * kRowBytes;
 
+  // The sums of R blocks for each wave, and their way out.
+  const auto run = [&](auto blocks_of) {
+    constexpr int R = decltype(blocks_of)::value;
+    constexpr int kStage = (BN + 32 * WR * R) * kRowBytes, ST = kRing / kStage < 3 ? 2 : 3, kUnits = kUnitsW + 32 * WR * R / kEvery;
+    struct Frags {
+      u32x4 a[R], b[CB];
+    };
+    f32x16 acc[R][CB];
+    Frags f0, f1;
+    uint32_t bytes_a[2][R], bytes_b[2][CB];
+    // Part i of R of a step's fragments, and of half a window's bytes.  Rows 32 apart have their pieces alike.
+    const auto read = [&](int stage, int s, Frags& f, int i) {
+      const uint8_t* from = lds + stage;
+      f.a[i] = *reinterpret_cast<const u32x4*>(from + (a_place ^ (32u * s)) + 32 * WR * kRowBytes * i);
 #pragma unroll
-  for (int u = 0; u < kUnits; ++u) copy_unit(0, u);
-  if (nb >= 16) {
-    load_scales(0);
-    put_scales(0);
-    load_scales(1);
-  } else {
+      for (int j = i * CB / R; j < (i + 1) * CB / R; ++j)
+        f.b[j] = *reinterpret_cast<const u32x4*>(from + (b_place ^ (32u * s)) + 32 * kRowBytes * j);
+    };
+    const auto read_bytes = [&](int word, int i) {
+      const uint8_t* from = lds + kRing + 8 * half + 4 * word + 16 * c;
+      bytes_a[word][i] = *reinterpret_cast<const uint32_t*>(from + 16 * (BN + 32 * wave_row) + 512 * WR * i);
 #pragma unroll
-    for (int i = 0; i < kTurns; ++i) put(0, i, load_few_bytes(srow[i], nb));
-  }
-  Frags f0, f1;
-  Bytes even, odd;
-  sync();
+      for (int j = i * CB / R; j < (i + 1) * CB / R; ++j)
+        bytes_b[word][j] = *reinterpret_cast<const uint32_t*>(from + 512 * CB * wave_col + 512 * j);
+    };
+    // The products of step `T` of a window; `beside(i)` issues reads and copies before row i's, to run under them.
+    const auto multiply = [&](auto T, const Frags& f, auto&& beside) {
+      constexpr int s = decltype(T)::value & 3, word = decltype(T)::value >> 2;
 #pragma unroll
-  for (int i = 0; i < RB; ++i) {
-    read(0, 0, f0, i);
-    read_bytes(0, even, i);
-    if (chunks > 1) copies(1, i);
-  }
-  // A chunk that is not the last, up to its last step, under which the next one's first fragments are read.  No
-  // branch inside: the compiler moves products over one.
-  const auto body = [&](auto is_odd, auto copy_on, int k, const Bytes& by, Bytes& next) {
-    multiply(S0{}, f0, by, [&](int i) {
-      read(k, 1, f1, i);
-      copies(k + 1, RB + i);
-    });
-    multiply(S1{}, f1, by, [&](int i) { read(k, 2, f0, i); });
-    multiply(S2{}, f0, by, [&](int i) {
-      read(k, 3, f1, i);
-      if (decltype(is_odd)::value && i == 0) put_scales((k + 1) >> 1);
-    });
-    sync();
-    multiply(S3{}, f1, by, [&](int i) {
-      read(k + 1, 0, f0, i);
-      read_bytes(k + 1, next, i);
-      if (decltype(copy_on)::value) copies(k + 2, i);
-      if (decltype(is_odd)::value && i == 0) load_scales((k + 3) >> 1);  // two chunks until it is put
-    });
-  };
-  using Yes = std::true_type;
-  using No = std::false_type;
-  int k = 0;
-  for (; k + 2 < chunks; k += 2) {
-    body(No{}, Yes{}, k, even, odd);
-    body(Yes{}, Yes{}, k + 1, odd, even);
-  }
-  if (k + 1 < chunks) {
-    body(No{}, No{}, k, even, odd);
-    even = odd;
-    ++k;
-  }
-  const int steps = (nb - 8 * k + 1) >> 1;  // of the last chunk
-  multiply(S0{}, f0, even, [&](int i) { read(k, 1, f1, i); });
-  if (steps > 1) multiply(S1{}, f1, even, [&](int i) { read(k, 2, f0, i); });
-  if (steps > 2) multiply(S2{}, f0, even, [&](int i) { read(k, 3, f1, i); });
-  if (steps > 3) multiply(S3{}, f1, even, nothing);
-  __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));  // no copy is left when the LDS is given back
-
-  // out: element r of a block is row 8 (r / 4) + 4 half + r % 4, column c
-  typedef row_elem<ODT> out_t;
-  constexpr int kSize = sizeof(out_t);
+      for (int i = 0; i < R; ++i) {
+        beside(i);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int i = 0; i < RB; ++i) {
-    const int first = row_a + 32 * i, rows = t.rows - first < 32 ? t.rows - first : 32;
-    if (rows <= 0) break;
-    const uint32_t pitch = uint32_t(p.N) * kSize;
-    const __amdgpu_buffer_rsrc_t ores =
-        uniform_rsrc(static_cast<out_t*>(p.out) + (t.row0 + first) * p.N + n0, uint32_t(rows - 1) * pitch + uint32_t(cols) * kSize);
-#pragma unroll
-    for (int j = 0; j < CB; ++j) {
-      const int col = row_b - BM + 32 * j + c;
-      const bool in = col < cols;
-      const float bias = p.bias && in ? p.bias[wrow0 + col] : 0.f;
-      const uint32_t off = in ? uint32_t(4 * half) * pitch + uint32_t(col) * kSize : 0x80000000u;
-#pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const uint32_t row = (8 * (r >> 2) + (r & 3)) * pitch;
-        const float v = acc[i][j][r] + bias;
-        if constexpr (ODT == 0) __builtin_amdgcn_raw_buffer_store_b16(bf16_rne(v), ores, off + row, 0, 0);
-        else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ores, off + row, 0, 0);
+        for (int j = 0; j < CB; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(operand4(f.a[i]), operand4(f.b[j]), acc[i][j], 4, 4, s,
+                                                                      int(bytes_a[word][i]), s, int(bytes_b[word][j]));
+        hold<CB>(acc[i]);
+        __builtin_amdgcn_sched_barrier(0);
       }
+    };
+    constexpr int kPer = (kUnits + 2 * R - 1) / (2 * R);  // copies beside a row, over two steps
+    const auto copies = [&](int chunk, int stage, int part) {
+#pragma unroll
+      for (int u = part * kPer; u < (part + 1) * kPer; ++u)
+        if (u < kUnits) copy_unit(chunk, stage, u);
+    };
+    // All copies but the last `behind` have landed, and everyone is done with the stage before.
+    const auto sync = [&](auto behind) {
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(decltype(behind)::value));
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+    };
+    // Stages go round with the chunks: the one that the current chunk is in, and the n-th after it.
+    int at = 0;
+    const auto after = [](int stage, int n) {
+      const int to = stage + n * kStage;
+      return to >= ST * kStage ? to - ST * kStage : to;
+    };
+    // Step `T` of a window.  With MORE windows behind it, nothing in it is a branch: the compiler moves
+    // products over one.
+    const auto step = [&](auto T, auto more, int window) {
+      constexpr int kT8 = decltype(T)::value, s = kT8 & 3, kChunk = kT8 >> 2;
+      constexpr bool kMore = decltype(more)::value;
+      const int chunk = 2 * window + kChunk;
+      Frags& f = kT8 & 1 ? f1 : f0;
+      Frags& g = kT8 & 1 ? f0 : f1;
+      // the last chunk that is copied before this one ends: of the last window no more than it has
+      constexpr int kCopied = kMore || kChunk + ST - 1 < 2 ? kChunk + ST - 1 : 1;
+      if constexpr (s == 3) {
+        constexpr bool kLast = !kMore && kT8 == 7;
+        if (!kLast) sync(std::integral_constant<int, kCopied - kChunk - 1 < 0 ? 0 : (kCopied - kChunk - 1) * kUnits>{});
+        const int here = at;
+        at = after(at, 1);
+        multiply(T, f, [&](int i) {
+          if (!kLast) read(at, 0, g, i);
+          if (kMore && kT8 == 7) read_bytes(0, i);
+          if (kMore || kChunk + ST < 2) copies(chunk + ST, here, i);
+        });
+      } else {
+        multiply(T, f, [&](int i) {
+          read(at, s + 1, g, i);
+          if (kT8 == 0) read_bytes(1, i);
+          if (s == 0 && (kMore || kChunk + ST - 1 < 2)) copies(chunk + ST - 1, after(at, ST - 1), R + i);
+          if (kMore && kT8 == 4 && i == 0) {
+            put_scales(window + 1);
+            load_scales(window + 2);
+          }
+        });
+      }
+    };
+    using Yes = std::true_type;
+    using No = std::false_type;
+#pragma unroll
+    for (int k = 0; k < ST - 1; ++k)
+#pragma unroll
+      for (int u = 0; u < kUnits; ++u) copy_unit(k, k * kStage, u);
+    if (nb >= 16) {
+      load_scales(0);
+      put_scales(0);
+      load_scales(1);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) put(i, load_few_bytes(srow[i], nb));
     }
-  }
+    sync(std::integral_constant<int, 0>{});
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+#pragma unroll
+      for (int j = 0; j < CB; ++j) acc[i][j] = f32x16{};
+      read(0, 0, f0, i);
+      read_bytes(0, i);
+      copies(ST - 1, (ST - 1) * kStage, i);
+    }
+    int w = 0;
+    for (; w + 1 < windows; ++w) {
+      step(std::integral_constant<int, 0>{}, Yes{}, w);
+      step(std::integral_constant<int, 1>{}, Yes{}, w);
+      step(std::integral_constant<int, 2>{}, Yes{}, w);
+      step(std::integral_constant<int, 3>{}, Yes{}, w);
+      step(std::integral_constant<int, 4>{}, Yes{}, w);
+      step(std::integral_constant<int, 5>{}, Yes{}, w);
+      step(std::integral_constant<int, 6>{}, Yes{}, w);
+      step(std::integral_constant<int, 7>{}, Yes{}, w);
+    }
+    const int steps = (nb - 16 * w + 1) >> 1;  // 1 .. 8 of the last window
+    step(std::integral_constant<int, 0>{}, No{}, w);
+    if (steps > 1) step(std::integral_constant<int, 1>{}, No{}, w);
+    if (steps > 2) step(std::integral_constant<int, 2>{}, No{}, w);
+    if (steps > 3) step(std::integral_constant<int, 3>{}, No{}, w);
+    if (steps > 4) step(std::integral_constant<int, 4>{}, No{}, w);
+    if (steps > 5) step(std::integral_constant<int, 5>{}, No{}, w);
+    if (steps > 6) step(std::integral_constant<int, 6>{}, No{}, w);
+    if (steps > 7) step(std::integral_constant<int, 7>{}, No{}, w);
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));  // no copy is left when the LDS is given back
+
+    // out: element r of a block is row 8 (r / 4) + 4 half + r % 4; a lane's columns are CB c ..
+    typedef row_elem<ODT> out_t;
+    constexpr int kSize = sizeof(out_t);
+    const int lane_col = CB * (32 * wave_col + c);
+    float bias[CB];
+#pragma unroll
+    for (int j = 0; j < CB; ++j) bias[j] = p.bias && lane_col + j < cols ? p.bias[wrow0 + lane_col + j] : 0.f;
+    const uint32_t pitch = uint32_t(p.N) * kSize;
+    const auto store = [&](auto together) {
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int first = 32 * (WR * i + wave_row), rows = t.rows - first < 32 ? t.rows - first : 32;
+        if (rows <= 0) break;
+        const __amdgpu_buffer_rsrc_t ores = uniform_rsrc(static_cast<out_t*>(p.out) + (t.row0 + first) * p.N + n0,
+                                                         uint32_t(rows - 1) * pitch + uint32_t(cols) * kSize);
+        uint32_t to[CB];
+#pragma unroll
+        for (int j = 0; j < CB; ++j)
+          to[j] = lane_col + j < cols ? uint32_t(4 * half) * pitch + uint32_t(lane_col + j) * kSize : 0x80000000u;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const uint32_t row = uint32_t(8 * (r >> 2) + (r & 3)) * pitch;
+          if constexpr (decltype(together)::value) {
+            static_assert(CB == 2, "columns of a lane");
+            const float v0 = acc[i][0][r] + bias[0], v1 = acc[i][1][r] + bias[1];
+            if constexpr (ODT == 0) __builtin_amdgcn_raw_buffer_store_b32(bf16_rne2(v0, v1), ores, to[0] + row, 0, kPastCaches);
+            else __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(v0), __float_as_uint(v1)}, ores, to[0] + row, 0, kPastCaches);
+          } else {
+#pragma unroll
+            for (int j = 0; j < CB; ++j) {
+              const float v = acc[i][j][r] + bias[j];
+              if constexpr (ODT == 0) __builtin_amdgcn_raw_buffer_store_b16(bf16_rne(v), ores, to[j] + row, 0, kPastCaches);
+              else __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(v), ores, to[j] + row, 0, kPastCaches);
+            }
+          }
+          if ((r & 3) == 3) __builtin_amdgcn_sched_barrier(0);  // a few sums in registers at a time
+        }
+      }
+    };
+    if (CB == 2 && p.N % CB == 0) store(std::integral_constant<bool, CB == 2>{});  // rows begin at the pair's alignment
+    else store(std::false_type{});
+  };
+  const int blocks = (t.rows + 32 * WR - 1) / (32 * WR);
+  if (RB > 2 && blocks > 2) run(std::integral_constant<int, RB>{});
+  else if (RB > 1 && blocks > 1) run(std::integral_constant<int, RB < 2 ? RB : 2>{});
+  else run(std::integral_constant<int, 1>{});
 }
 
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Rows and columns of a tile, by the mean number of an expert's rows.
+int64_t row_tiles(const MxGemmLaunch& L, int bm) {
+  const int64_t used = L.E < L.S ? L.E : L.S;
+  return (L.S + used * (bm - 1)) / bm;
+}
+
+// Rows and columns of a tile.  256 x 256 where an expert has about a hundred rows and more and there is such a
+// tile for every CU, 128 x 128 below, 64 x 128 where an expert has few.  us with 256 x 256, 128 x 128 and 64 x 128,
+// [5760, 2880] of 32 experts: 8192 rows 150, 157, 186; 4096 95, 105, 113; 2048 74, 72, 81; 1024 60, 59, 64;
+// [1536, 2048] of 128 experts, 512 and 2048 rows: 38, 35, 33 and 41, 36, 34; of one expert [14336, 4096], 256 rows
+// (56, 224 and 448 tiles): 26, 17, 16; of 8 [4096, 14336], 512 rows (128 large tiles): 66, 52, 60.
 struct TileForm {
   int bm, bn, threads;
 };
 TileForm tile_form(const MxGemmLaunch& L) {
-  const int64_t mean = L.S / L.E;
-  if (mean >= 192) return {256, 256, 256};
-  if (mean >= 96) return {128, 128, 256};
-  if (mean >= 48) return {64, 128, 256};
-  return {32, 128, 256};
-}
-int64_t row_tiles(const MxGemmLaunch& L, int bm) {
-  const int64_t used = L.E < L.S ? L.E : L.S;
-  return (L.S + used * (bm - 1)) / bm;
+  const int64_t mean = L.S / (L.E < L.S ? L.E : (L.S > 0 ? L.S : 1));
+  if (mean >= 96 && row_tiles(L, 256) * div_up(L.N, 256) >= cu_count()) return {256, 256, 512};
+  return mean > 24 ? TileForm{128, 128, 256} : TileForm{64, 128, 256};
 }
 int64_t gemm_blocks(const MxGemmLaunch& L) {
   const TileForm f = tile_form(L);
@@ -429,10 +495,9 @@ hipError_t launch_mxfp4_gemm(const MxGemmLaunch& L, hipStream_t stream) {
   const TileForm f = tile_form(L);
   const GemmArgs a{L.x, L.xs, L.w, L.ws, L.bias, L.offsets, L.out, L.N, L.K, int(L.S), int(L.E), uint32_t(div_up(L.N, f.bn))};
   const unsigned grid = unsigned(gemm_blocks(L));
-  if (f.bm == 256) tile<4, 4, 2, 2>(L, a, grid, stream);
+  if (f.bm == 256) tile<4, 2, 2, 4>(L, a, grid, stream);
   else if (f.bm == 128) tile<2, 2, 2, 2>(L, a, grid, stream);
-  else if (f.bm == 64) tile<2, 1, 1, 4>(L, a, grid, stream);
-  else tile<1, 1, 1, 4>(L, a, grid, stream);
+  else tile<2, 1, 1, 4>(L, a, grid, stream);
   return hipGetLastError();
 }
 
