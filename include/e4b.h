@@ -539,7 +539,8 @@ int e4b_glu_backward(const void* g, int32_t g_dtype, const void* rows, int32_t r
 /*
  * e4b_quantize_act_mxfp4 — rows to MXFP4, the left operand of e4b_grouped_gemm_mxfp4, by the rule of
  * e4b_pack_mxfp4; with sorted_slots gathered to expert order on the way.
- *   x             [T, K] of `dtype`.  K % 32 == 0.  1 <= k <= 64, T*k < 2^31.  T*k*K < 2^35.
+ *   x             [T, K] of `dtype`.  K % 32 == 0.  1 <= k <= 64, T*k < 2^31.  Fewer than 2^26
+ *                 pieces of up to 2048 columns.
  *   sorted_slots  [T*k] int32 from e4b_route_permute: row p comes from x[sorted_slots[p] / k]; a slot
  *                 outside [0, T*k) leaves a row of zeros.  NULL: the rows as they are (k = 1).
  *   blocks        [T*k, K/32, 16] uint8 out; scales [T*k, K/32] uint8 out, as e4b_pack_mxfp4 has them.

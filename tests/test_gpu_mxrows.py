@@ -36,7 +36,7 @@ def _offsets(lengths):
 # ---- quantise
 
 
-@pytest.mark.parametrize("T,K", [(1, 32), (1, 2880), (3, 96), (70, 2880), (513, 1312)])
+@pytest.mark.parametrize("T,K", [(1, 32), (1, 2880), (3, 96), (70, 2880), (513, 1312), (1000, 32), (333, 160), (9, 1024), (31, 1056), (2, 14336)])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_quantize_as_the_packer(e4b, T, K, dtype):
     x = _normal(T, K, dtype=dtype, seed=T) * torch.exp2(_normal(1, K, seed=1, std=3.0).round()).to(dtype)
