@@ -191,8 +191,9 @@ __device__ __forceinline__ u32x4 bytes_from(u32x4 v, int first, int nb) {
   if (down & 8) v = u32x4{v[2], v[3], 0u, 0u};
   if (down & 4) v = u32x4{v[1], v[2], v[3], 0u};
   const uint32_t by = uint32_t(down & 3);
-  return u32x4{__builtin_amdgcn_alignbyte(v[1], v[0], by), __builtin_amdgcn_alignbyte(v[2], v[1], by),
-               __builtin_amdgcn_alignbyte(v[3], v[2], by), __builtin_amdgcn_alignbyte(0u, v[3], by)};
+  v = u32x4{__builtin_amdgcn_alignbyte(v[1], v[0], by), __builtin_amdgcn_alignbyte(v[2], v[1], by),
+            __builtin_amdgcn_alignbyte(v[3], v[2], by), __builtin_amdgcn_alignbyte(0u, v[3], by)};
+  return down < 16 ? v : u32x4{0u, 0u, 0u, 0u};
 }
 // The same for a row of fewer than 16.
 __device__ __forceinline__ u32x4 load_few_bytes(const uint8_t* __restrict__ row, int nb) {
@@ -233,9 +234,10 @@ __global__ void __launch_bounds__(WR * WC * kWave, 2) tile_kernel(GemmArgs p) {
   constexpr int BM = 32 * RB * WR, BN = 32 * CB * WC, kRowBytes = 16 * CH, kEvery = 8 * kW;
   constexpr int kBmLog2 = BM == 256 ? 8 : (BM == 128 ? 7 : 6);
   constexpr int kRing = RING * (BM + BN) * kRowBytes;
-  constexpr int kTurns = (BM + BN + kT - 1) / kT;  // rows of bytes a thread has (some past the last)
+  constexpr int kTurnRows = kT / 2, kTurns = (BM + BN + kTurnRows - 1) / kTurnRows;  // rows of bytes, two lanes each
+  constexpr int kHalf = kTurns * kTurnRows * 16;   // a window's bytes in LDS
   static_assert(BM % kEvery == 0 && BN % kEvery == 0 && kEvery % 32 == 0, "copies");
-  __shared__ __attribute__((aligned(16))) uint8_t lds[kRing + kTurns * kT * 16];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[kRing + 2 * kHalf];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, half = lane >> 5;
   const GemmTile t = find_gemm_tile(p.offsets, p.E, p.S, kBmLog2, p.col_tiles, blockIdx.x);
@@ -265,30 +267,31 @@ __global__ void __launch_bounds__(WR * WC * kWave, 2) tile_kernel(GemmArgs p) {
     dma16(i < kUnitsW ? wres : xres, (i < kUnitsW ? w_own : x_own) + (from + rows * rowb), 0u,
           lds + stage + 1024 * (i * kW + wave));
   };
+  // Exponent bytes come for two windows at a time, a lane for each row and window.
   const uint8_t* sbase[kTurns];  // the same for a wave: its rows are all of w or all of x
   uint32_t soff[kTurns];
   u32x4 sreg[kTurns];
 #pragma unroll
   for (int i = 0; i < kTurns; ++i) {
-    const int r = tid + i * kT < BM + BN ? tid + i * kT : 0;
+    const int r = (tid >> 1) + i * kTurnRows < BM + BN ? (tid >> 1) + i * kTurnRows : 0;
     const bool of_w = __builtin_amdgcn_readfirstlane(r) < BN;
     const int last = (of_w ? cols : t.rows) - 1, row = of_w ? col_of(r) : r - BN;
     sbase[i] = of_w ? p.ws + wrow0 * nb : p.xs + t.row0 * nb;
     soff[i] = uint32_t(row < last ? row : last) * uint32_t(nb);
   }
-  const auto load_scales = [&](int window) {  // past the last window: the last again, unused
-    const int first = 16 * window < nb ? 16 * window : (nb - 1) & ~15;
+  const auto load_scales = [&](int pair) {  // past the last window: the last again, unused
+    const int first = 32 * pair + 16 * (tid & 1);
 #pragma unroll
     for (int i = 0; i < kTurns; ++i) sreg[i] = load_bytes16(sbase[i], soff[i], first, nb);
   };
   const auto put = [&](int i, u32x4 v) {  // even blocks' bytes, then odd blocks'
-    *reinterpret_cast<u32x4*>(lds + kRing + 16 * (tid + i * kT)) =
+    *reinterpret_cast<u32x4*>(lds + kRing + kHalf * (tid & 1) + 16 * ((tid >> 1) + i * kTurnRows)) =
         u32x4{perm(v[1], v[0], 0x06040200u), perm(v[3], v[2], 0x06040200u), perm(v[1], v[0], 0x07050301u),
               perm(v[3], v[2], 0x07050301u)};
   };
-  const auto put_scales = [&](int window) {
+  const auto put_scales = [&](int pair) {
 #pragma unroll
-    for (int i = 0; i < kTurns; ++i) put(i, bytes_from(sreg[i], 16 * window, nb));
+    for (int i = 0; i < kTurns; ++i) put(i, bytes_from(sreg[i], 32 * pair + 16 * (tid & 1), nb));
   };
 
   const int wave_row = wave / WC, wave_col = wave % WC;
@@ -314,8 +317,8 @@ __global__ void __launch_bounds__(WR * WC * kWave, 2) tile_kernel(GemmArgs p) {
       for (int j = i * CB / R; j < (i + 1) * CB / R; ++j)
         f.b[j] = *reinterpret_cast<const u32x4*>(from + (b_place ^ (32u * s)) + 32 * kRowBytes * j);
     };
-    const auto read_bytes = [&](int word, int i) {
-      const uint8_t* from = lds + kRing + 8 * half + 4 * word + 16 * c;
+    const auto read_bytes = [&](int odd, int word, int i) {
+      const uint8_t* from = lds + kRing + kHalf * odd + 8 * half + 4 * word + 16 * c;
       bytes_a[word][i] = *reinterpret_cast<const uint32_t*>(from + 16 * (BN + 32 * wave_row) + 512 * WR * i);
 #pragma unroll
       for (int j = i * CB / R; j < (i + 1) * CB / R; ++j)
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(WR * WC * kWave, 2) tile_kernel(GemmArgs p) {
     };
     // Step `T` of a window.  With MORE windows behind it, nothing in it is a branch: the compiler moves
     // products over one.
-    const auto step = [&](auto T, auto more, int window) {
+    const auto step = [&](auto T, auto more, int odd, int window) {
       constexpr int kT8 = decltype(T)::value, s = kT8 & 3, kChunk = kT8 >> 2;
       constexpr bool kMore = decltype(more)::value;
       const int chunk = 2 * window + kChunk;
@@ -372,64 +375,70 @@ __global__ void __launch_bounds__(WR * WC * kWave, 2) tile_kernel(GemmArgs p) {
         at = after(at, 1);
         multiply(T, f, [&](int i) {
           if (!kLast) read(at, 0, g, i);
-          if (kMore && kT8 == 7) read_bytes(0, i);
+          if (kMore && kT8 == 7) read_bytes(odd ^ 1, 0, i);
           if (kMore || kChunk + ST < 2) copies(chunk + ST, here, i);
         });
       } else {
         multiply(T, f, [&](int i) {
           read(at, s + 1, g, i);
-          if (kT8 == 0) read_bytes(1, i);
+          if (kT8 == 0) read_bytes(odd, 1, i);
           if (s == 0 && (kMore || kChunk + ST - 1 < 2)) copies(chunk + ST - 1, after(at, ST - 1), R + i);
-          if (kMore && kT8 == 4 && i == 0) {
-            put_scales(window + 1);
-            load_scales(window + 2);
+          if (kMore && kT8 == 4 && i == 0 && odd) {
+            put_scales((window + 1) >> 1);
+            load_scales((window + 3) >> 1);
           }
         });
       }
     };
     using Yes = std::true_type;
     using No = std::false_type;
+    // The first window's bytes are asked for before the copies (loads come back in order), the next one's after.
+    if (nb >= 16) load_scales(0);
 #pragma unroll
     for (int k = 0; k < ST - 1; ++k)
 #pragma unroll
       for (int u = 0; u < kUnits; ++u) copy_unit(k, k * kStage, u);
     if (nb >= 16) {
-      load_scales(0);
       put_scales(0);
-      load_scales(1);
     } else {
 #pragma unroll
-      for (int i = 0; i < kTurns; ++i) put(i, load_few_bytes(sbase[i] + soff[i], nb));
+      for (int i = 0; i < kTurns; ++i) put(i, load_few_bytes(sbase[i] + soff[i], tid & 1 ? 0 : nb));
     }
     sync(std::integral_constant<int, 0>{});
+    if (nb >= 16) load_scales(1);
 #pragma unroll
     for (int i = 0; i < R; ++i) {
 #pragma unroll
       for (int j = 0; j < CB; ++j) acc[i][j] = f32x16{};
       read(0, 0, f0, i);
-      read_bytes(0, i);
+      read_bytes(0, 0, i);
       copies(ST - 1, (ST - 1) * kStage, i);
     }
+    const auto window = [&](int odd, int w) {
+      step(std::integral_constant<int, 0>{}, Yes{}, odd, w);
+      step(std::integral_constant<int, 1>{}, Yes{}, odd, w);
+      step(std::integral_constant<int, 2>{}, Yes{}, odd, w);
+      step(std::integral_constant<int, 3>{}, Yes{}, odd, w);
+      step(std::integral_constant<int, 4>{}, Yes{}, odd, w);
+      step(std::integral_constant<int, 5>{}, Yes{}, odd, w);
+      step(std::integral_constant<int, 6>{}, Yes{}, odd, w);
+      step(std::integral_constant<int, 7>{}, Yes{}, odd, w);
+    };
     int w = 0;
-    for (; w + 1 < windows; ++w) {
-      step(std::integral_constant<int, 0>{}, Yes{}, w);
-      step(std::integral_constant<int, 1>{}, Yes{}, w);
-      step(std::integral_constant<int, 2>{}, Yes{}, w);
-      step(std::integral_constant<int, 3>{}, Yes{}, w);
-      step(std::integral_constant<int, 4>{}, Yes{}, w);
-      step(std::integral_constant<int, 5>{}, Yes{}, w);
-      step(std::integral_constant<int, 6>{}, Yes{}, w);
-      step(std::integral_constant<int, 7>{}, Yes{}, w);
+    for (; w + 2 < windows; w += 2) {
+      window(0, w);
+      window(1, w + 1);
     }
-    const int steps = (nb - 16 * w + 1) >> 1;  // 1 .. 8 of the last window
-    step(std::integral_constant<int, 0>{}, No{}, w);
-    if (steps > 1) step(std::integral_constant<int, 1>{}, No{}, w);
-    if (steps > 2) step(std::integral_constant<int, 2>{}, No{}, w);
-    if (steps > 3) step(std::integral_constant<int, 3>{}, No{}, w);
-    if (steps > 4) step(std::integral_constant<int, 4>{}, No{}, w);
-    if (steps > 5) step(std::integral_constant<int, 5>{}, No{}, w);
-    if (steps > 6) step(std::integral_constant<int, 6>{}, No{}, w);
-    if (steps > 7) step(std::integral_constant<int, 7>{}, No{}, w);
+    if (w + 1 < windows) window(0, w++);
+    const int steps = (nb - 16 * w + 1) >> 1, odd = w & 1;  // 1 .. 8 of the last window
+    step(std::integral_constant<int, 0>{}, No{}, odd, w);
+    if (steps > 1) step(std::integral_constant<int, 1>{}, No{}, odd, w);
+    if (steps > 2) step(std::integral_constant<int, 2>{}, No{}, odd, w);
+    if (steps > 3) step(std::integral_constant<int, 3>{}, No{}, odd, w);
+    if (steps > 4) step(std::integral_constant<int, 4>{}, No{}, odd, w);
+    if (steps > 5) step(std::integral_constant<int, 5>{}, No{}, odd, w);
+    if (steps > 6) step(std::integral_constant<int, 6>{}, No{}, odd, w);
+    if (steps > 7) step(std::integral_constant<int, 7>{}, No{}, odd, w);
     __builtin_amdgcn_s_waitcnt(waitcnt_vm_lgkm0(0));  // no copy is left when the LDS is given back
 
     // out: element r of a block is row 8 (r / 4) + 4 half + r % 4; a lane's columns are CB c ..

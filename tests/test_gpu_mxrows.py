@@ -122,12 +122,13 @@ def _lengths(S, E, seed):
     return rng.multinomial(S, p / p.sum())
 
 
-# rows, experts: a token, few rows of many experts, about 16, 32, 64, 128 and 256 rows an expert and their neighbours, one expert alone
+# rows, experts: a token, few rows of many experts, about 16, 32, 64, 128 and 256 rows an expert and their neighbours, one expert alone;
+# K of one block to six windows of 16 blocks, whole and not, even and odd numbers of windows and blocks
 COUNTS = [(1, 1), (1, 32), (4, 32), (15, 1), (16, 1), (17, 1), (31, 2), (33, 1), (64, 128), (130, 5), (200, 3), (257, 1), (700, 4), (1100, 2)]
 
 
 @pytest.mark.parametrize("S,E", COUNTS)
-@pytest.mark.parametrize("N,K", [(64, 32), (5, 64), (96, 96), (257, 544), (1000, 2880), (320, 2048)])
+@pytest.mark.parametrize("N,K", [(64, 32), (5, 64), (96, 96), (64, 512), (257, 544), (48, 1024), (130, 1056), (65, 2592), (1000, 2880), (320, 2048)])
 @pytest.mark.parametrize("out_t,biased", [(F32, False), (BF16, True)])
 def test_product(e4b, S, E, N, K, out_t, biased):
     x, w = _codes((S,), K, seed=S + K), _codes((E, N), K, seed=E + N)
