@@ -59,7 +59,7 @@ def test_quantize_refuses(e4b):
     assert f(x=None) == ERR_ARG and f(blocks=None) == ERR_ARG and f(scales=None) == ERR_ARG
     assert f(K=48) == ERR_SHAPE and f(k=65) == ERR_SHAPE
     assert f(x=FAKE + 8) == ERR_ALIGN and f(slots=FAKE + 4) == ERR_ALIGN and f(scales=FAKE + 2) == ERR_ALIGN
-    assert f(T=1 << 30) == ERR_OVERFLOW and f(T=1 << 26, K=512, k=1) == ERR_OVERFLOW
+    assert f(T=1 << 30) == ERR_OVERFLOW and f(T=1 << 26, K=2048, k=1) == ERR_OVERFLOW
 
 
 def _gemm(e4b, **kw):
