@@ -139,13 +139,16 @@ struct GluArgs {
   uint32_t items, per;    // of the call, of a row
 };
 
-// s(t) and 1 - s(t), the logistic function.  Below -87 it stays at 1.6e-38, so that no infinity
-// enters; NaN stays NaN.
+// s(t) and 1 - s(t), the logistic function, from e^-|t|, which cannot overflow: below -87.3 it is 0 as e is.
+// NaN stays NaN.
 __device__ __forceinline__ void logistic(float t, float* s, float* rest) {
-  const float e = __expf(t < -87.f ? 87.f : -t);
-  *s = __builtin_amdgcn_rcpf(1.f + e);
-  *rest = e * *s;
+  const float e = __expf(-fabsf(t)), near = __builtin_amdgcn_rcpf(1.f + e), far = e * near;
+  *s = t < 0.f ? far : near;
+  *rest = t < 0.f ? near : far;
 }
+// The clamped form's t.  Far below, where s(t) is 0, t stays finite, so that t s(t) is 0 too.
+__device__ __forceinline__ float steep(float gc) { return gc < -128.f ? -128.f : 1.702f * gc; }
+
 template <bool CLAMPED>
 __device__ __forceinline__ float glu(float g, float u) {
   float s, rest;
@@ -154,22 +157,24 @@ __device__ __forceinline__ float glu(float g, float u) {
     return g * s * u;
   }
   const float gc = g > 7.f ? 7.f : g, uc = u > 7.f ? 7.f : (u < -7.f ? -7.f : u);  // NaN stays NaN
-  logistic(1.702f * gc, &s, &rest);
+  logistic(steep(gc), &s, &rest);
   return gc * s * (uc + 1.f);
 }
+// The factor of the gate's gradient is taken first: it lies in [-0.1, 1.1] whatever the gate.
 template <bool CLAMPED>
 __device__ __forceinline__ void glu_grad(float g, float gate, float up, float* d_gate, float* d_up) {
   float s, rest;
   if (!CLAMPED) {
     logistic(gate, &s, &rest);
-    *d_gate = g * up * s * (1.f + gate * rest);
-    *d_up = g * gate * s;
+    *d_gate = (s + gate * s * rest) * up * g;
+    *d_up = gate * s * g;
     return;
   }
   const float gc = gate > 7.f ? 7.f : gate, uc = up > 7.f ? 7.f : (up < -7.f ? -7.f : up);
-  logistic(1.702f * gc, &s, &rest);
-  *d_gate = gate > 7.f ? 0.f : g * (uc + 1.f) * s * (1.f + 1.702f * gc * rest);
-  *d_up = up > 7.f || up < -7.f ? 0.f : g * gc * s;
+  const float t = steep(gc);
+  logistic(t, &s, &rest);
+  *d_gate = gate > 7.f ? 0.f : (s + t * s * rest) * (uc + 1.f) * g;
+  *d_up = up > 7.f || up < -7.f ? 0.f : gc * s * g;
 }
 
 // An item is V elements of gates and V of ups (halves), or V elements of pairs (interleaved).  Its h

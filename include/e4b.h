@@ -515,7 +515,8 @@ int e4b_restore_rows(const int8_t* codes, const uint8_t* scales, int64_t S, int6
  *               2j+1.  I % 32 == 0 (interleaved: I % 16).  S*I < 2^33.  E4B_DT_I8: codes of e4b_checkpoint_rows,
  *   row_scales  and their scales [S, 2I/32]; NULL for the other types.
  *   flags       E4B_ACT_CLAMPED_GLU | E4B_GU_INTERLEAVED, as for e4b_moe_forward.
- *   h           [S, I] of h_dtype out, computed in float32 and rounded once.  NaN in a row's pair gives NaN.
+ *   h           [S, I] of h_dtype out, computed in float32 and rounded once.  NaN in a row's pair gives NaN;
+ *               the logistic function is 0 below 2^-126.
  *   codes, scales  NULL, or the checkpoint of `rows` as e4b_checkpoint_rows makes it, out (not with
  *               E4B_DT_I8 rows).
  */

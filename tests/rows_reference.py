@@ -53,7 +53,7 @@ def _parts(rows, act, interleaved):
 # The kernels take e = 2^(t log2 e) and 1 / (1 + e) from the hardware.  t (a product for the clamped form, with a
 # rounded constant), its product with a rounded log2 e: at most 4 |t| 2^-24 relative in e; the two
 # instructions an ulp each, the sum and the two to four products half an ulp each: under 12 * 2^-24 more.  Below
-# t = -87 the logistic stays at 1.7e-38.
+# t = -87.3 the logistic, there under 1.2e-38, counts as 0.
 def _rel(t):
     return (4 * t.abs().clamp(max=88) + 12) * 2.0 ** -24
 

@@ -161,6 +161,29 @@ def test_values_at_the_clamps_and_far_out(e4b, act, interleaved):
 
 
 @pytest.mark.parametrize("act,interleaved", ACTS)
+def test_values_at_the_ends_of_float32(e4b, act, interleaved):
+    """A gate far below zero shuts its pair, whatever the ups and gradients: the logistic function there is under
+    2^-126 and counts as 0.  Far above zero it is 1."""
+    top = torch.finfo(F32).max
+    gate = torch.tensor([-top, -1e38, -1e30, -1e4, -200.0, -128.0, -105.0], device=DEV).repeat_interleave(32)[None]
+    up = torch.tensor([top, -top, 1e38, 1.0, -1.0, 0.0, 7.0, -7.0], device=DEV).repeat(28)[None]
+    g = torch.tensor([top, 1.0, -top, -1.0], device=DEV).repeat_interleave(8).repeat(7)[None]
+    rows = ref.joined(gate, up, interleaved).contiguous()
+    zero = torch.zeros_like(gate)
+    assert torch.equal(e4b.e4b_glu(rows, act=act, interleaved=interleaved, dtype=F32)[0], zero)
+    d = e4b.e4b_glu_backward(g, rows, act=act, interleaved=interleaved, dtype=F32)
+    assert torch.equal(d, torch.zeros_like(d))
+    high = ref.joined(-gate, torch.ones_like(gate), interleaved).contiguous()
+    h = e4b.e4b_glu(high, act=act, interleaved=interleaved, dtype=F32)[0]
+    d_gate, d_up = ref.halves(e4b.e4b_glu_backward(torch.ones_like(g), high, act=act, interleaved=interleaved, dtype=F32), interleaved)
+    if act == "swiglu":
+        assert torch.equal(h, -gate) and torch.equal(d_gate, torch.ones_like(gate)) and torch.equal(d_up, -gate)
+    else:
+        ref.assert_within(h, *ref.glu(high, act, interleaved), "h")
+        assert torch.equal(d_gate, zero) and torch.equal(d_up, h / 2)
+
+
+@pytest.mark.parametrize("act,interleaved", ACTS)
 def test_gradient_against_differences(e4b, act, interleaved):
     """Central differences of the float64 forward with steps of 2^-10: a third derivative of a few units times
     step^2 / 6 is under 1e-5."""
