@@ -491,6 +491,153 @@ __global__ void __launch_bounds__(WR * WC * kWave, 2) tile_kernel(GemmArgs p) {
   else run(std::integral_constant<int, 1>{});
 }
 
+// The form of few tiles, where the tile form would leave CUs without one.  A workgroup has up to 16 RB rows of an
+// expert by 16 CB columns; its WK waves take chunks of 16 blocks in turn, straight from memory into the
+// instruction's registers, and their sums meet in LDS in a fixed order.  Step s of a chunk takes blocks 4 s to
+// 4 s + 3, sixteen lanes each: half a line of a row, so w's lines are kept for the next step (past the caches 29.4 us
+// for two experts' row at [28672, 4096], 27.9 so).  Bound: the latency of a chunk's loads and the join, and for many
+// rows the rows of x that every column tile reads anew.  Two chunks under way where registers allow it (one row
+// at [4096, 14336] 10.0 us, one chunk 13.7; for 2 x 2 blocks two take the second workgroup of a CU its registers).
+template <int ODT, int WK, int RB, int CB>
+__global__ void __launch_bounds__(WK * kWave, RB * CB == 1 ? 4 : 2) few_kernel(GemmArgs p) {
+  constexpr int BM = 16 * RB, BN = 16 * CB, kBmLog2 = RB == 1 ? 4 : 5, CH = 16;
+  __shared__ f32x4 part[WK][RB][CB][kWave];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, q = lane >> 4;
+  const GemmTile t = find_gemm_tile(p.offsets, p.E, p.S, kBmLog2, p.col_tiles, blockIdx.x);
+  if (t.rows == 0) return;
+  const int nb = int(p.K >> 5), chunks = (nb + CH - 1) / CH;
+  const uint32_t rowb = uint32_t(nb) * 16u;
+  const int64_t n0 = int64_t(t.col) * BN;
+  const int cols = p.N - n0 < BN ? int(p.N - n0) : BN;
+  const int64_t wrow0 = int64_t(t.expert) * p.N + n0;
+  const __amdgpu_buffer_rsrc_t xres = uniform_rsrc(p.x + t.row0 * rowb, uint32_t(t.rows) * rowb);
+  const __amdgpu_buffer_rsrc_t wres = uniform_rsrc(p.w + wrow0 * rowb, uint32_t(cols) * rowb);
+  const uint8_t *wsb = p.ws + wrow0 * nb, *xsb = p.xs + t.row0 * nb;
+  const uint32_t own = uint32_t(c) * rowb + 16u * q;
+  // Rows behind the last have no codes (the buffers end) and the last one's bytes, which nothing reads outside.
+  uint32_t w_bytes[CB], x_bytes[RB];
+#pragma unroll
+  for (int j = 0; j < CB; ++j) w_bytes[j] = uint32_t(16 * j + c < cols ? 16 * j + c : cols - 1) * uint32_t(nb);
+#pragma unroll
+  for (int i = 0; i < RB; ++i) x_bytes[i] = uint32_t(16 * i + c < t.rows ? 16 * i + c : t.rows - 1) * uint32_t(nb);
+
+  struct Chunk {
+    u32x4 w[CB][4], x[RB][4], ws[CB], xs[RB];
+  };
+  const auto load_codes = [&](int chunk, Chunk& k) {
+    const uint32_t at = own + uint32_t(16 * CH * chunk);
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+#pragma unroll
+      for (int j = 0; j < CB; ++j)
+        k.w[j][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(wres, at + 64u * s + 16u * j * rowb, 0, 0));
+#pragma unroll
+      for (int i = 0; i < RB; ++i)
+        k.x[i][s] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(xres, at + 64u * s + 16u * i * rowb, 0, 0));
+    }
+  };
+  const auto load = [&](int chunk, Chunk& k) {
+#pragma unroll
+    for (int j = 0; j < CB; ++j) k.ws[j] = load_bytes16(wsb, w_bytes[j], CH * chunk, nb);
+#pragma unroll
+    for (int i = 0; i < RB; ++i) k.xs[i] = load_bytes16(xsb, x_bytes[i], CH * chunk, nb);
+    load_codes(chunk, k);
+  };
+  f32x4 acc[RB][CB];
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < CB; ++j) acc[i][j] = f32x4{};
+  const uint32_t low = 0x0C0C0400u + 0x0101u * q, high = 0x04000C0Cu + 0x01010000u * q;  // byte q of each word
+  const auto bytes_of = [&](u32x4 v) {
+    return int(perm(v[1], v[0], low) | perm(v[3], v[2], high));
+  };
+  const auto multiply = [&](const Chunk& k) {
+    int wb[CB], xb[RB];
+#pragma unroll
+    for (int j = 0; j < CB; ++j) wb[j] = bytes_of(k.ws[j]);
+#pragma unroll
+    for (int i = 0; i < RB; ++i) xb[i] = bytes_of(k.xs[i]);
+    const auto step = [&](auto S) {
+      constexpr int s = decltype(S)::value;
+#pragma unroll
+      for (int i = 0; i < RB; ++i)
+#pragma unroll
+        for (int j = 0; j < CB; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(operand4(k.x[i][s]), operand4(k.w[j][s]), acc[i][j], 4, 4,
+                                                                       s, xb[i], s, wb[j]);
+    };
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+    step(std::integral_constant<int, 2>{});
+    step(std::integral_constant<int, 3>{});
+  };
+  const auto use = [&](int chunk, Chunk& k) {
+#pragma unroll
+    for (int j = 0; j < CB; ++j) k.ws[j] = bytes_from(k.ws[j], CH * chunk, nb);
+#pragma unroll
+    for (int i = 0; i < RB; ++i) k.xs[i] = bytes_from(k.xs[i], CH * chunk, nb);
+    multiply(k);
+  };
+  if (nb >= 16) {
+    int at = wave;
+    if constexpr (RB * CB == 1) {
+      // A chunk is loaded before the last is used.  The loop goes on only where both are there: the compiler waits
+      // for every load behind a branch that may or may not have had some.
+      Chunk k0, k1;
+      if (at < chunks) load(at, k0);
+      while (at < chunks) {
+        if (at + WK >= chunks) {
+          use(at, k0);
+          break;
+        }
+        load(at + WK, k1);
+        use(at, k0);
+        at += WK;
+        if (at + WK >= chunks) {
+          use(at, k1);
+          break;
+        }
+        load(at + WK, k0);
+        use(at, k1);
+        at += WK;
+      }
+    } else {
+      for (; at < chunks; at += WK) {
+        Chunk k;
+        load(at, k);
+        use(at, k);
+      }
+    }
+  } else if (wave == 0) {
+    Chunk k;
+    load_codes(0, k);
+#pragma unroll
+    for (int j = 0; j < CB; ++j) k.ws[j] = load_few_bytes(wsb + w_bytes[j], nb);
+#pragma unroll
+    for (int i = 0; i < RB; ++i) k.xs[i] = load_few_bytes(xsb + x_bytes[i], nb);
+    multiply(k);
+  }
+#pragma unroll
+  for (int i = 0; i < RB; ++i)
+#pragma unroll
+    for (int j = 0; j < CB; ++j) part[wave][i][j][lane] = acc[i][j];
+  __syncthreads();
+  // element r of lane l is row 4 (l / 16) + r, column l % 16
+  for (int o = tid; o < BM * BN; o += WK * kWave) {
+    const int col = o & (BN - 1), row = o / BN, from = 16 * ((row & 15) >> 2) + (col & 15);
+    if (row >= t.rows || col >= cols) continue;
+    float sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < WK; ++w) sum += reinterpret_cast<const float*>(&part[w][row >> 4][col >> 4][from])[row & 3];
+    if (p.bias) sum += p.bias[wrow0 + col];
+    row_elem<ODT>* to = static_cast<row_elem<ODT>*>(p.out) + (t.row0 + row) * p.N + n0 + col;
+    if constexpr (ODT == 0) *to = bf16_rne(sum);
+    else *to = sum;
+  }
+}
+
 int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 int64_t row_tiles(const MxGemmLaunch& L, int bm) {
@@ -503,12 +650,19 @@ int64_t row_tiles(const MxGemmLaunch& L, int bm) {
 // [5760, 2880] of 32 experts: 8192 rows 150, 157, 186; 4096 95, 105, 113; 2048 74, 72, 81; 1024 60, 59, 64;
 // [1536, 2048] of 128 experts, 512 and 2048 rows: 38, 35, 33 and 41, 36, 34; of one expert [14336, 4096], 256 rows
 // (56, 224 and 448 tiles): 26, 17, 16; of 8 [4096, 14336], 512 rows (128 large tiles): 66, 52, 60.
+// Where those leave CUs without a tile, tiles of 16 x 16 whose waves share K, or for more rows of 32 x 32.  us with
+// 64 x 128 or 128 x 128, 16 x 16 and 32 x 32 of one expert, a row at [4096, 14336] 30, 10, -; [2880, 2880] 7.5, 4.1, -; 32 rows
+// at [4096, 14336] 51, 19, 24; 64: 51, 32, 23; 128: 56, 59, 34; 256: 55, 114, 63; 64 rows at [2880, 2880] 11, 6.6, 6.4; of 4
+// experts' rows at [5760, 2880] (180 tiles) 13.4, 12.7, -; of 8 with 4 rows each at [4096, 14336] (256 tiles) 52, 57, -.
 struct TileForm {
   int bm, bn, threads;
 };
 TileForm tile_form(const MxGemmLaunch& L) {
   const int64_t mean = L.S / (L.E < L.S ? L.E : (L.S > 0 ? L.S : 1));
   if (mean >= 96 && row_tiles(L, 256) * div_up(L.N, 256) >= cu_count()) return {256, 256, 512};
+  const int64_t small = row_tiles(L, 32) * div_up(L.N, 32);  // tiles of the larger few form
+  if (mean <= 16 ? row_tiles(L, 64) * div_up(L.N, 128) < cu_count() : small <= 2 * cu_count())
+    return mean <= 16 || small < cu_count() ? TileForm{16, 16, 256} : TileForm{32, 32, 256};
   return mean > 24 ? TileForm{128, 128, 256} : TileForm{64, 128, 256};
 }
 int64_t gemm_blocks(const MxGemmLaunch& L) {
@@ -519,6 +673,12 @@ template <int RB, int CB, int WR, int WC, int RING>
 void tile(const MxGemmLaunch& L, const GemmArgs& a, unsigned grid, hipStream_t s) {
   if (L.out_dtype == 0) hipLaunchKernelGGL((tile_kernel<0, RB, CB, WR, WC, RING>), dim3(grid), dim3(WR * WC * kWave), 0, s, a);
   else hipLaunchKernelGGL((tile_kernel<1, RB, CB, WR, WC, RING>), dim3(grid), dim3(WR * WC * kWave), 0, s, a);
+}
+
+template <int RB, int CB>
+void few(const MxGemmLaunch& L, const GemmArgs& a, unsigned grid, hipStream_t s) {
+  if (L.out_dtype == 0) hipLaunchKernelGGL((few_kernel<0, 4, RB, CB>), dim3(grid), dim3(4 * kWave), 0, s, a);
+  else hipLaunchKernelGGL((few_kernel<1, 4, RB, CB>), dim3(grid), dim3(4 * kWave), 0, s, a);
 }
 
 }  // namespace
@@ -557,7 +717,9 @@ hipError_t launch_mxfp4_gemm(const MxGemmLaunch& L, hipStream_t stream) {
   const unsigned grid = unsigned(gemm_blocks(L));
   if (f.bm == 256) tile<4, 2, 2, 4, 2>(L, a, grid, stream);
   else if (f.bm == 128) tile<2, 2, 2, 2, 2>(L, a, grid, stream);
-  else tile<2, 1, 1, 4, 3>(L, a, grid, stream);
+  else if (f.bm == 64) tile<2, 1, 1, 4, 3>(L, a, grid, stream);
+  else if (f.bm == 32) few<2, 2>(L, a, grid, stream);
+  else few<1, 1>(L, a, grid, stream);
   return hipGetLastError();
 }
 

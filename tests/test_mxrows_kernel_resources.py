@@ -13,7 +13,7 @@ pytestmark = pytest.mark.skipif(shutil.which("hipcc") is None and not os.path.ex
 
 
 @pytest.mark.parametrize("source,kernels", [
-    ("mxrows.hip", ["quantize_kernel", "tile_kernel"]),
+    ("mxrows.hip", ["quantize_kernel", "tile_kernel", "few_kernel"]),
     ("act.hip", ["checkpoint_kernel", "restore_kernel", "glu_kernel", "glu_backward_kernel"])])
 def test_no_spills(source, kernels):
     spec = importlib.util.spec_from_file_location("e4b_build", os.path.join(ROOT, "bit_quantized_mixture_amd", "build.py"))
