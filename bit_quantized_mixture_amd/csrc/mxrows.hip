@@ -228,6 +228,12 @@ __device__ __forceinline__ void hold(f32x16 (&v)[N]) {
 // each.  Exponent bytes come through registers for a window of 16 blocks at a time, sorted so that a lane's eight
 // of a window are two words, whose bytes the instruction picks.  Fragments are read a step ahead of their
 // products, over the chunk's barrier too.
+// Bound: for few rows memory (512 rows of 128 experts at [1536, 2048] 35 us, 6.1 TB/s); for whole tiles the L2
+// caches' requests (a workgroup reads 64 KB for 256 matrix instructions) and the clock under the matrix unit's
+// power, and at K = 2880 the start and end of a tile, 15000 of 60000 cycles (8192 rows at [28672, 4096] 540 us,
+// 3.6 PFLOP/s; at [5760, 2880] of 32 experts 164 us, 1.7).  Two stages of 128-byte rows fill the LDS at 256 x 256; chunks of
+// half that with four stages, and 128 x 256 with two workgroups a CU, were slower (762 us against 660 of that
+// state), so was a grid of one workgroup a CU that went through its tiles (660 against 552).
 template <int ODT, int RB, int CB, int WR, int WC, int RING>
 __global__ void __launch_bounds__(WR * WC * kWave, 2) tile_kernel(GemmArgs p) {
   constexpr int kW = WR * WC, kT = kW * kWave, CH = 8;

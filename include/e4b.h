@@ -495,7 +495,8 @@ int e4b_grouped_lora_backward_x8(const e4b_lora_backward_args* a, const int8_t* 
  *   scales  [S, C/32] uint8 out: X + 127 (0 for blocks below 2^-126).  255 for a block that holds a NaN or
  *           an infinity: all of it is read as NaN.
  * Off by half a step 2^(X - 7) at most, 1/127 of the block's largest; a block whose largest is
- * 2^127 * 255/128 or more saturates at 127 * 2^121.  Bit-exact and deterministic.  No output overlaps an input, here and in the calls below.
+ * 2^127 * 255/128 or more saturates at 127 * 2^121.  Bit-exact and deterministic.  No output
+ * overlaps an input, here and in the calls below.
  */
 int e4b_checkpoint_rows(const void* x, int32_t dtype, int64_t S, int64_t C, int8_t* codes, uint8_t* scales,
                         void* stream);
