@@ -112,8 +112,10 @@ __device__ __forceinline__ v8i operand4(u32x4 a) { return v8i{int(a[0]), int(a[1
 
 // The tiles of a launch: every expert's rows cut into pieces of 1 << bm_log2 and its columns into `cols`.  The
 // row tiles of an expert stand in bands of up to kBand, a band's column after column, so that neighbours
-// share both operands.  The XCDs, each with an L2 cache of its own, have contiguous stretches of that list, and
-// the workgroups of an XCD (workgroup b runs on XCD b % 8) take its stretch in turn.
+// share both operands.  In the larger forms last pieces of half the rows and fewer are a list of their own behind all
+// others, so that the launch ends with short tiles (8192 rows of 32 experts at [5760, 2880] 165 us in one list, 147 so; 4096 of 8 at
+// [4096, 14336] 185 and 155).  The XCDs, each with an L2 cache of its own, have contiguous stretches of either list, and
+// the workgroups of an XCD (workgroup b runs on XCD b % 8) take its stretches in turn.
 struct GemmTile {
   int expert;
   int64_t row0;
@@ -122,41 +124,62 @@ struct GemmTile {
 };
 constexpr int kBand = 8;
 
+template <bool SHORTS>
 __device__ __forceinline__ GemmTile find_gemm_tile(const int32_t* __restrict__ offsets, int E, int S, int bm_log2,
                                                    uint32_t cols, uint32_t block) {
   const int lane = threadIdx.x & (kWave - 1), bm = 1 << bm_log2;
-  const auto tiles_at = [&](int g0, int* lo, int* hi) {
+  // Tiles of an expert's rows, and whether a short one follows.
+  const auto tiles_at = [&](int g0, int* lo, int* hi, int* rest) {
     *lo = *hi = 0;
     if (g0 + lane < E) group_rows(offsets, g0 + lane, S, lo, hi);
-    return int((int64_t(*hi) - *lo + bm - 1) >> bm_log2);
+    const int n = *hi - *lo, left = n & (bm - 1);
+    *rest = SHORTS && left > 0 && left <= bm / 2;
+    return (n >> bm_log2) + (left > (SHORTS ? bm / 2 : 0));
   };
-  int lo, hi, n = tiles_at(0, &lo, &hi), ni = wave_scan(n);
-  uint64_t all = uint32_t(__builtin_amdgcn_readlane(ni, kWave - 1));
+  int lo, hi, rest, n = tiles_at(0, &lo, &hi, &rest), ni = wave_scan(n), ri = SHORTS ? wave_scan(rest) : 0;
+  uint64_t whole = uint32_t(__builtin_amdgcn_readlane(ni, kWave - 1)), shorts = uint32_t(__builtin_amdgcn_readlane(ri, kWave - 1));
   for (int g0 = kWave; g0 < E; g0 += kWave) {
-    int l, h;
-    all += uint32_t(__builtin_amdgcn_readlane(wave_scan(tiles_at(g0, &l, &h)), kWave - 1));
+    int l, h, r;
+    whole += uint32_t(__builtin_amdgcn_readlane(wave_scan(tiles_at(g0, &l, &h, &r)), kWave - 1));
+    if (SHORTS) shorts += uint32_t(__builtin_amdgcn_readlane(wave_scan(r), kWave - 1));
   }
-  all *= cols;
-  if (block >= all) return GemmTile{0, 0, 0, 0};
-  const uint32_t xcd = block & 7u, per = uint32_t(all >> 3), rest = uint32_t(all & 7u);
-  const uint32_t id = xcd * per + (xcd < rest ? xcd : rest) + (block >> 3), row_tile = id / cols;
+  const uint32_t xcd = block & 7u;
+  uint32_t id = block >> 3;
+  // an XCD's stretch of a list of `all`
+  const auto take = [&](uint64_t all) {
+    const uint32_t per = uint32_t(all >> 3), over = uint32_t(all & 7u), mine = per + (xcd < over);
+    if (id >= mine) {
+      id -= mine;
+      return false;
+    }
+    id += xcd * per + (xcd < over ? xcd : over);
+    return true;
+  };
+  bool is_short = false;
+  if (!take(whole * cols)) {
+    if (!take(shorts * cols)) return GemmTile{0, 0, 0, 0};
+    is_short = true;
+  }
+  const uint32_t row_tile = id / cols;
   uint32_t base = 0;
   for (int g0 = 0; g0 < E; g0 += kWave) {
     if (g0 > 0) {
-      n = tiles_at(g0, &lo, &hi);
+      n = tiles_at(g0, &lo, &hi, &rest);
       ni = wave_scan(n);
+      if (SHORTS) ri = wave_scan(rest);
     }
-    const uint32_t sum = uint32_t(__builtin_amdgcn_readlane(ni, kWave - 1));
+    const int count = is_short ? rest : n, ci = is_short ? ri : ni;
+    const uint32_t sum = uint32_t(__builtin_amdgcn_readlane(ci, kWave - 1));
     if (row_tile - base < sum) {
-      const int k = __ffsll((unsigned long long)__ballot(row_tile - base < uint32_t(ni))) - 1;
-      const uint32_t m = uint32_t(__builtin_amdgcn_readlane(n, k));
-      const uint32_t first = base + uint32_t(__builtin_amdgcn_readlane(ni, k)) - m;
+      const int k = __ffsll((unsigned long long)__ballot(row_tile - base < uint32_t(ci))) - 1;
+      const uint32_t m = uint32_t(__builtin_amdgcn_readlane(count, k));
+      const uint32_t first = base + uint32_t(__builtin_amdgcn_readlane(ci, k)) - m;
       const uint32_t within = id - first * cols, band = within / (kBand * cols);
       if (m == 0 || band * kBand >= m) break;  // sums of offsets that descend can wrap
       const uint32_t high = m - band * kBand < kBand ? m - band * kBand : kBand;
       const uint32_t in_band = within - band * kBand * cols, col = in_band / high;
       if (col >= cols) break;
-      const uint32_t t = band * kBand + (in_band - col * high);
+      const uint32_t t = band * kBand + (in_band - col * high) + (is_short ? uint32_t(__builtin_amdgcn_readlane(n, k)) : 0u);
       const int row0 = __builtin_amdgcn_readlane(lo, k) + int(t << bm_log2), left = __builtin_amdgcn_readlane(hi, k) - row0;
       return GemmTile{g0 + k, row0, left < bm ? left : bm, col};
     }
@@ -246,7 +269,7 @@ __global__ void __launch_bounds__(WR * WC * kWave, 2) tile_kernel(GemmArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kRing + 2 * kHalf];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, half = lane >> 5;
-  const GemmTile t = find_gemm_tile(p.offsets, p.E, p.S, kBmLog2, p.col_tiles, blockIdx.x);
+  const GemmTile t = find_gemm_tile<(BM >= 128)>(p.offsets, p.E, p.S, kBmLog2, p.col_tiles, blockIdx.x);
   if (t.rows == 0) return;
   const int nb = int(p.K >> 5), windows = (nb + 15) >> 4;
   const uint32_t rowb = uint32_t(nb) * 16u;
@@ -510,7 +533,7 @@ __global__ void __launch_bounds__(WK * kWave, RB * CB == 1 ? 4 : 2) few_kernel(G
   __shared__ f32x4 part[WK][RB][CB][kWave];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, q = lane >> 4;
-  const GemmTile t = find_gemm_tile(p.offsets, p.E, p.S, kBmLog2, p.col_tiles, blockIdx.x);
+  const GemmTile t = find_gemm_tile<false>(p.offsets, p.E, p.S, kBmLog2, p.col_tiles, blockIdx.x);
   if (t.rows == 0) return;
   const int nb = int(p.K >> 5), chunks = (nb + CH - 1) / CH;
   const uint32_t rowb = uint32_t(nb) * 16u;
@@ -673,7 +696,7 @@ TileForm tile_form(const MxGemmLaunch& L) {
 }
 int64_t gemm_blocks(const MxGemmLaunch& L) {
   const TileForm f = tile_form(L);
-  return row_tiles(L, f.bm) * div_up(L.N, f.bn);
+  return row_tiles(L, f.bm) * div_up(L.N, f.bn) + 16;  // an XCD has up to one tile of either list more than an eighth
 }
 template <int RB, int CB, int WR, int WC, int RING>
 void tile(const MxGemmLaunch& L, const GemmArgs& a, unsigned grid, hipStream_t s) {
