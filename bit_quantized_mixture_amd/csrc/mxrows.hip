@@ -675,10 +675,11 @@ int64_t row_tiles(const MxGemmLaunch& L, int bm) {
 }
 
 // Rows and columns of a tile.  256 x 256 where an expert has about a hundred rows and more and there is such a
-// tile for every CU, 128 x 128 below, 64 x 128 where an expert has few.  us with 256 x 256, 128 x 128 and 64 x 128,
-// [5760, 2880] of 32 experts: 8192 rows 150, 157, 186; 4096 95, 105, 113; 2048 74, 72, 81; 1024 60, 59, 64;
-// [1536, 2048] of 128 experts, 512 and 2048 rows: 38, 35, 33 and 41, 36, 34; of one expert [14336, 4096], 256 rows
-// (56, 224 and 448 tiles): 26, 17, 16; of 8 [4096, 14336], 512 rows (128 large tiles): 66, 52, 60.
+// tile for most CUs, 128 x 128 below, 64 x 128 where an expert has few.  us with 256 x 256, 128 x 128 and 64 x 128,
+// [5760, 2880] of 32 experts: 8192 rows 149, 176, 217; 4096 97, 114, 130; 2048 85, 81, 91; 1024 70, 70, 67;
+// [4096, 14336] of 8: 4096 rows 159, 190, 224; 2048 (at most 240 large tiles) 112, 127, 134; 1024 (at most 176) 97, 72, 95;
+// [1536, 2048] of 128, 512 and 2048 rows: 38, 35, 33 and 41, 36, 34; of one expert [14336, 4096], 256 rows
+// (56, 224 and 448 tiles): 26, 17, 16.
 // Where those leave CUs without a tile, tiles of 16 x 16 whose waves share K, or for more rows of 32 x 32.  us with
 // 64 x 128 or 128 x 128, 16 x 16 and 32 x 32 of one expert, a row at [4096, 14336] 30, 10, -; [2880, 2880] 7.5, 4.1, -; 32 rows
 // at [4096, 14336] 51, 19, 24; 64: 51, 32, 23; 128: 56, 59, 34; 256: 55, 114, 63; 64 rows at [2880, 2880] 11, 6.6, 6.4; of 4
@@ -688,7 +689,7 @@ struct TileForm {
 };
 TileForm tile_form(const MxGemmLaunch& L) {
   const int64_t mean = L.S / (L.E < L.S ? L.E : (L.S > 0 ? L.S : 1));
-  if (mean >= 96 && row_tiles(L, 256) * div_up(L.N, 256) >= cu_count()) return {256, 256, 512};
+  if (mean >= 96 && row_tiles(L, 256) * div_up(L.N, 256) >= cu_count() * 7 / 8) return {256, 256, 512};
   const int64_t small = row_tiles(L, 32) * div_up(L.N, 32);  // tiles of the larger few form
   if (mean <= 16 ? row_tiles(L, 64) * div_up(L.N, 128) < cu_count() : small <= 2 * cu_count())
     return mean <= 16 || small < cu_count() ? TileForm{16, 16, 256} : TileForm{32, 32, 256};
