@@ -105,6 +105,7 @@ struct GemmArgs {
   int64_t N, K;
   int S, E;
   uint32_t col_tiles;
+  bool two_lists;
 };
 
 typedef int v8i __attribute__((ext_vector_type(8)));
@@ -112,10 +113,12 @@ __device__ __forceinline__ v8i operand4(u32x4 a) { return v8i{int(a[0]), int(a[1
 
 // The tiles of a launch: every expert's rows cut into pieces of 1 << bm_log2 and its columns into `cols`.  The
 // row tiles of an expert stand in bands of up to kBand, a band's column after column, so that neighbours
-// share both operands.  In the larger forms last pieces of half the rows and fewer are a list of their own behind all
-// others, so that the launch ends with short tiles (8192 rows of 32 experts at [5760, 2880] 165 us in one list, 147 so; 4096 of 8 at
-// [4096, 14336] 185 and 155).  The XCDs, each with an L2 cache of its own, have contiguous stretches of either list, and
-// the workgroups of an XCD (workgroup b runs on XCD b % 8) take its stretches in turn.
+// share both operands.  In the larger forms, where a launch is few rounds of tiles, last pieces of half the rows
+// and fewer are a list of their own behind all others, so that it ends with short tiles (8192 rows of 32 experts at
+// [5760, 2880], at most 6 tiles a CU, 165 us in one list, 148 so; 4096 of 8 at [4096, 14336], 2, 185 and 155; 16384
+// of 32, 8, 249 and 241; but 8192 of 8 at [28672, 4096], 17, 558 and 563: their columns are fetched twice).  The
+// XCDs, each with an L2 cache of its own, have contiguous stretches of either list, and the workgroups of an XCD
+// (workgroup b runs on XCD b % 8) take its stretches in turn.
 struct GemmTile {
   int expert;
   int64_t row0;
@@ -124,24 +127,23 @@ struct GemmTile {
 };
 constexpr int kBand = 8;
 
-template <bool SHORTS>
 __device__ __forceinline__ GemmTile find_gemm_tile(const int32_t* __restrict__ offsets, int E, int S, int bm_log2,
-                                                   uint32_t cols, uint32_t block) {
+                                                   uint32_t cols, bool two_lists, uint32_t block) {
   const int lane = threadIdx.x & (kWave - 1), bm = 1 << bm_log2;
   // Tiles of an expert's rows, and whether a short one follows.
   const auto tiles_at = [&](int g0, int* lo, int* hi, int* rest) {
     *lo = *hi = 0;
     if (g0 + lane < E) group_rows(offsets, g0 + lane, S, lo, hi);
     const int n = *hi - *lo, left = n & (bm - 1);
-    *rest = SHORTS && left > 0 && left <= bm / 2;
-    return (n >> bm_log2) + (left > (SHORTS ? bm / 2 : 0));
+    *rest = two_lists && left > 0 && left <= bm / 2;
+    return (n >> bm_log2) + (left > (two_lists ? bm / 2 : 0));
   };
-  int lo, hi, rest, n = tiles_at(0, &lo, &hi, &rest), ni = wave_scan(n), ri = SHORTS ? wave_scan(rest) : 0;
+  int lo, hi, rest, n = tiles_at(0, &lo, &hi, &rest), ni = wave_scan(n), ri = two_lists ? wave_scan(rest) : 0;
   uint64_t whole = uint32_t(__builtin_amdgcn_readlane(ni, kWave - 1)), shorts = uint32_t(__builtin_amdgcn_readlane(ri, kWave - 1));
   for (int g0 = kWave; g0 < E; g0 += kWave) {
     int l, h, r;
     whole += uint32_t(__builtin_amdgcn_readlane(wave_scan(tiles_at(g0, &l, &h, &r)), kWave - 1));
-    if (SHORTS) shorts += uint32_t(__builtin_amdgcn_readlane(wave_scan(r), kWave - 1));
+    if (two_lists) shorts += uint32_t(__builtin_amdgcn_readlane(wave_scan(r), kWave - 1));
   }
   const uint32_t xcd = block & 7u;
   uint32_t id = block >> 3;
@@ -166,7 +168,7 @@ __device__ __forceinline__ GemmTile find_gemm_tile(const int32_t* __restrict__ o
     if (g0 > 0) {
       n = tiles_at(g0, &lo, &hi, &rest);
       ni = wave_scan(n);
-      if (SHORTS) ri = wave_scan(rest);
+      if (two_lists) ri = wave_scan(rest);
     }
     const int count = is_short ? rest : n, ci = is_short ? ri : ni;
     const uint32_t sum = uint32_t(__builtin_amdgcn_readlane(ci, kWave - 1));
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(WR * WC * kWave, 2) tile_kernel(GemmArgs p) {
   __shared__ __attribute__((aligned(16))) uint8_t lds[kRing + 2 * kHalf];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 31, half = lane >> 5;
-  const GemmTile t = find_gemm_tile<(BM >= 128)>(p.offsets, p.E, p.S, kBmLog2, p.col_tiles, blockIdx.x);
+  const GemmTile t = find_gemm_tile(p.offsets, p.E, p.S, kBmLog2, p.col_tiles, BM >= 128 && p.two_lists, blockIdx.x);
   if (t.rows == 0) return;
   const int nb = int(p.K >> 5), windows = (nb + 15) >> 4;
   const uint32_t rowb = uint32_t(nb) * 16u;
@@ -533,7 +535,7 @@ __global__ void __launch_bounds__(WK * kWave, RB * CB == 1 ? 4 : 2) few_kernel(G
   __shared__ f32x4 part[WK][RB][CB][kWave];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, q = lane >> 4;
-  const GemmTile t = find_gemm_tile<false>(p.offsets, p.E, p.S, kBmLog2, p.col_tiles, blockIdx.x);
+  const GemmTile t = find_gemm_tile(p.offsets, p.E, p.S, kBmLog2, p.col_tiles, false, blockIdx.x);
   if (t.rows == 0) return;
   const int nb = int(p.K >> 5), chunks = (nb + CH - 1) / CH;
   const uint32_t rowb = uint32_t(nb) * 16u;
@@ -743,7 +745,8 @@ hipError_t launch_quantize_mxfp4(const void* x, int dtype, int64_t T, int64_t K,
 hipError_t launch_mxfp4_gemm(const MxGemmLaunch& L, hipStream_t stream) {
   if (L.S == 0) return hipSuccess;
   const TileForm f = tile_form(L);
-  const GemmArgs a{L.x, L.xs, L.w, L.ws, L.bias, L.offsets, L.out, L.N, L.K, int(L.S), int(L.E), uint32_t(div_up(L.N, f.bn))};
+  const GemmArgs a{L.x, L.xs, L.w, L.ws, L.bias, L.offsets, L.out, L.N, L.K, int(L.S), int(L.E), uint32_t(div_up(L.N, f.bn)),
+                   gemm_blocks(L) <= 12 * cu_count()};
   const unsigned grid = unsigned(gemm_blocks(L));
   if (f.bm == 256) tile<4, 2, 2, 4, 2>(L, a, grid, stream);
   else if (f.bm == 128) tile<2, 2, 2, 2, 2>(L, a, grid, stream);

@@ -29,6 +29,16 @@ def test_every_row_and_column(e4b, name, N):
     _check(out, x, w, off, None, K, before=torch.full((S, N), 9.0, device=DEV))
 
 
+def test_many_rounds_of_large_tiles(e4b):
+    """More than twelve tiles of 256 x 256 for each of 256 compute units: one list."""
+    counts = COUNTS["large"]
+    S, E, N, K = sum(counts) + 3, len(counts), 16650, 32
+    x, w, off = _codes((S,), K, seed=E), _codes((E, N), K, seed=N), _offsets(counts)
+    out = torch.full((S, N), 9.0, device=DEV)
+    e4b.e4b_grouped_gemm_mxfp4(*x, *w, off, out=out)
+    _check(out, x, w, off, None, K, before=torch.full((S, N), 9.0, device=DEV))
+
+
 @pytest.mark.parametrize("S", [40, 3000])
 def test_offsets_that_descend_stay_in_bounds(e4b, S):
     """Not a call that the documentation allows: nothing outside the rows is written, and rows of proper groups are whole."""
