@@ -255,8 +255,9 @@ __device__ __forceinline__ void hold(f32x16 (&v)[N]) {
 // products, over the chunk's barrier too.
 // Bound: for few rows memory (512 rows of 128 experts at [1536, 2048] 35 us, 6.1 TB/s); for whole tiles the L2
 // caches' requests (a workgroup reads 64 KB for 256 matrix instructions) and the clock under the matrix unit's
-// power, and at K = 2880 the start and end of a tile, 15000 of 60000 cycles (8192 rows at [28672, 4096] 540 us,
-// 3.6 PFLOP/s; at [5760, 2880] of 32 experts 164 us, 1.7).  Two stages of 128-byte rows fill the LDS at 256 x 256; chunks of
+// power, and at K = 2880 the start and end of a tile, 15000 of 60000 cycles (8192 rows of 8 experts at [28672, 4096] 540 us,
+// 3.6 PFLOP/s; of 32 at [5760, 2880] 148 us, 1.8; of one at [8192, 8192] 254 us, 4.3; the unit alone, from registers, 6.3
+// on random codes).  Two stages of 128-byte rows fill the LDS at 256 x 256; chunks of
 // half that with four stages, and 128 x 256 with two workgroups a CU, were slower (762 us against 660 of that
 // state), so was a grid of one workgroup a CU that went through its tiles (660 against 552).
 template <int ODT, int RB, int CB, int WR, int WC, int RING>
