@@ -529,10 +529,10 @@ __global__ void __launch_bounds__(WR * WC * kWave, 2) tile_kernel(GemmArgs p) {
 // 4 s + 3, sixteen lanes each: half a line of a row, so w's lines are kept for the next step (past the caches 29.4 us
 // for two experts' row at [28672, 4096], 27.9 so).  Bound: the latency of a chunk's loads and the join, and for many
 // rows the rows of x that every column tile reads anew.  Two chunks under way where registers allow it (one row
-// at [4096, 14336] 10.0 us, one chunk 13.7; for 2 x 2 blocks two take the second workgroup of a CU its registers).
+// at [4096, 14336] 10.0 us, one chunk 13.7; for 2 x 2 blocks two take the second workgroup of a CU its registers, for 4 x 4 there is no room).
 template <int ODT, int WK, int RB, int CB>
 __global__ void __launch_bounds__(WK * kWave, RB * CB == 1 ? 4 : 2) few_kernel(GemmArgs p) {
-  constexpr int BM = 16 * RB, BN = 16 * CB, kBmLog2 = RB == 1 ? 4 : 5, CH = 16;
+  constexpr int BM = 16 * RB, BN = 16 * CB, kBmLog2 = RB == 1 ? 4 : (RB == 2 ? 5 : 6), CH = 16;
   __shared__ f32x4 part[WK][RB][CB][kWave];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, q = lane >> 4;
@@ -683,19 +683,22 @@ int64_t row_tiles(const MxGemmLaunch& L, int bm) {
 // [4096, 14336] of 8: 4096 rows 159, 190, 224; 2048 (at most 240 large tiles) 112, 127, 134; 1024 (at most 176) 97, 72, 95;
 // [1536, 2048] of 128, 512 and 2048 rows: 38, 35, 33 and 41, 36, 34; of one expert [14336, 4096], 256 rows
 // (56, 224 and 448 tiles): 26, 17, 16.
-// Where those leave CUs without a tile, tiles of 16 x 16 whose waves share K, or for more rows of 32 x 32.  us with
-// 64 x 128 or 128 x 128, 16 x 16 and 32 x 32 of one expert, a row at [4096, 14336] 30, 10, -; [2880, 2880] 7.5, 4.1, -; 32 rows
-// at [4096, 14336] 51, 19, 24; 64: 51, 32, 23; 128: 56, 59, 34; 256: 55, 114, 63; 64 rows at [2880, 2880] 11, 6.6, 6.4; of 4
-// experts' rows at [5760, 2880] (180 tiles) 13.4, 12.7, -; of 8 with 4 rows each at [4096, 14336] (256 tiles) 52, 57, -.
+// Where those leave CUs without a tile, tiles of 16 x 16 whose waves share K, or for more rows of 32 x 32 and 64 x 64.
+// us with 64 x 128 or 128 x 128, 16 x 16, 32 x 32 and 64 x 64 of one expert, a row at [4096, 14336] 30, 10, -, -; [2880, 2880]
+// 7.5, 4.1, -, -; 32 rows at [4096, 14336] 51, 19, 24, 38; 64: 51, 32, 23, 41; 128: 56, 59, 35, 41; 256: 55, 114, 63, 41; 384: 55,
+// -, 91, 64; 64 rows at [2880, 2880] 11, 6.6, 6.4, 11; at [14336, 4096] 18, 37, 23, 17; of 4 experts' rows at [5760, 2880]
+// (180 tiles) 13.4, 12.7, -, -; 4 experts' 32 rows at [2880, 2880] (at most 630 of 32 x 32) 16, -, 12, 13; of 8 with 4 rows each
+// at [4096, 14336] (256 tiles) 52, 57, -, -.
 struct TileForm {
   int bm, bn, threads;
 };
 TileForm tile_form(const MxGemmLaunch& L) {
   const int64_t mean = L.S / (L.E < L.S ? L.E : (L.S > 0 ? L.S : 1));
   if (mean >= 96 && row_tiles(L, 256) * div_up(L.N, 256) >= cu_count() * 7 / 8) return {256, 256, 512};
-  const int64_t small = row_tiles(L, 32) * div_up(L.N, 32);  // tiles of the larger few form
-  if (mean <= 16 ? row_tiles(L, 64) * div_up(L.N, 128) < cu_count() : small <= 2 * cu_count())
+  const int64_t small = row_tiles(L, 32) * div_up(L.N, 32);
+  if (mean <= 16 ? row_tiles(L, 64) * div_up(L.N, 128) < cu_count() : small <= cu_count() * 5 / 2)
     return mean <= 16 || small < cu_count() ? TileForm{16, 16, 256} : TileForm{32, 32, 256};
+  if (mean > 16 && row_tiles(L, 64) * div_up(L.N, 64) <= cu_count()) return {64, 64, 256};
   return mean > 24 ? TileForm{128, 128, 256} : TileForm{64, 128, 256};
 }
 int64_t gemm_blocks(const MxGemmLaunch& L) {
@@ -751,7 +754,8 @@ hipError_t launch_mxfp4_gemm(const MxGemmLaunch& L, hipStream_t stream) {
   const unsigned grid = unsigned(gemm_blocks(L));
   if (f.bm == 256) tile<4, 2, 2, 4, 2>(L, a, grid, stream);
   else if (f.bm == 128) tile<2, 2, 2, 2, 2>(L, a, grid, stream);
-  else if (f.bm == 64) tile<2, 1, 1, 4, 3>(L, a, grid, stream);
+  else if (f.bm == 64 && f.bn == 128) tile<2, 1, 1, 4, 3>(L, a, grid, stream);
+  else if (f.bm == 64) few<4, 4>(L, a, grid, stream);
   else if (f.bm == 32) few<2, 2>(L, a, grid, stream);
   else few<1, 1>(L, a, grid, stream);
   return hipGetLastError();

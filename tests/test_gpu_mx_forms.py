@@ -1,4 +1,4 @@
-"""Products of MXFP4 rows at sizes that reach each form of the kernel (tiles of 16 x 16 and 32 x 32 whose waves share
+"""Products of MXFP4 rows at sizes that reach each form of the kernel (tiles of 16 x 16 to 64 x 64 whose waves share
 K, of 64 x 128, 128 x 128 and 256 x 256), with every length of K that its loop treats differently, against float64."""
 import pytest
 import torch
@@ -14,7 +14,8 @@ BF16, F32 = torch.bfloat16, torch.float32
 FORMS = {
     "16 x 16": (9, 3, 333),          # few rows an expert, and fewer than 256 tiles of 64 x 128
     "16 x 16, more rows": (75, 2, 70),
-    "32 x 32": (190, 2, 1001),       # 256 to 512 tiles of 32 x 32
+    "32 x 32": (190, 2, 1201),       # 256 to 640 tiles of 32 x 32
+    "64 x 64": (200, 1, 4061),       # more of those, but no more than 256 tiles of 64 x 64
     "64 x 128": (300, 150, 259),
     "128 x 128": (1200, 30, 645),
     "256 x 256": (6500, 64, 1027),
