@@ -1029,7 +1029,7 @@ def e4b_checkpoint_rows(x, codes=None, scales=None, stream=None):
     """Rows kept in 8 bits: x [S, C] bf16 or float32 -> (codes int8 [S, C], scales uint8 [S, C/32]).
 
     Each 32 columns of a row share a power of two; a value is off by at most 1/127 of its block's
-    largest.  C % 32 == 0.  Read back by e4b_restore_rows, e4b_glu, e4b_glu_backward and
+    largest, or by 2^-134 where that largest is below 2^-127.  C % 32 == 0.  Read back by e4b_restore_rows, e4b_glu, e4b_glu_backward and
     e4b_grouped_lora_backward (x_scales).
     """
     dt = _need_rows(x, "x")

@@ -492,11 +492,12 @@ int e4b_grouped_lora_backward_x8(const e4b_lora_backward_args* a, const int8_t* 
  * round to 128 steps, q = rint(v * 2^(6 - X)) (ties to even) and v' = q * 2^(X - 6).
  *   x       [S, C] of `dtype`.  C % 32 == 0.  S*C < 2^34 (bf16: 2^35).
  *   codes   [S, C] int8 out, in [-127, 127].
- *   scales  [S, C/32] uint8 out: X + 127 (0 for blocks below 2^-126).  255 for a block that holds a NaN or
- *           an infinity: all of it is read as NaN.
- * Off by half a step 2^(X - 7) at most, 1/127 of the block's largest; a block whose largest is
- * 2^127 * 255/128 or more saturates at 127 * 2^121.  Bit-exact and deterministic.  No output
- * overlaps an input, here and in the calls below.
+ *   scales  [S, C/32] uint8 out: X + 127, with X no less than -127 (byte 0: a block whose largest is below
+ *           127.5 * 2^-133).  255 for a block that holds a NaN or an infinity: all of it is read as NaN.
+ * Off by half a step 2^(X - 7) at most: 1/127 of the block's largest where that is 2^-127 or more; below,
+ * half a step stays 2^-134, and a block whose largest is 2^-134 or less is read back as zeros.  A block
+ * whose largest is 2^127 * 255/128 or more saturates at 127 * 2^121, 1/127 of its largest off at
+ * most.  Bit-exact and deterministic.  No output overlaps an input, here and in the calls below.
  */
 int e4b_checkpoint_rows(const void* x, int32_t dtype, int64_t S, int64_t C, int8_t* codes, uint8_t* scales,
                         void* stream);
