@@ -150,7 +150,8 @@ __device__ __forceinline__ void logistic(float t, float* s, float* rest) {
   *s = t < 0.f ? far : near;
   *rest = t < 0.f ? near : far;
 }
-// The clamped form's t.  Far below, where s(t) is 0, t stays finite, so that t s(t) is 0 too.
+// The clamped form's t.  Far below, where s(t) is 0, t stays finite, so that t s(t) is 0 too, for a gate of -inf as
+// well (the gate itself times s(t) is NaN there, as the formula has it).
 __device__ __forceinline__ float steep(float gc) { return gc < -128.f ? -128.f : 1.702f * gc; }
 
 template <bool CLAMPED>
@@ -164,7 +165,8 @@ __device__ __forceinline__ float glu(float g, float u) {
   logistic(steep(gc), &s, &rest);
   return gc * s * (uc + 1.f);
 }
-// The factor of the gate's gradient is taken first: it lies in [-0.1, 1.1] whatever the gate.
+// The factor of the gate's gradient is taken first: it lies in [-0.1, 1.1] for every finite gate.  For an infinite one it
+// is NaN in the silu form; in the clamped form 0.
 template <bool CLAMPED>
 __device__ __forceinline__ void glu_grad(float g, float gate, float up, float* d_gate, float* d_up) {
   float s, rest;

@@ -518,7 +518,9 @@ int e4b_restore_rows(const int8_t* codes, const uint8_t* scales, int64_t S, int6
  *   row_scales  and their scales [S, 2I/32]; NULL for the other types.
  *   flags       E4B_ACT_CLAMPED_GLU | E4B_GU_INTERLEAVED, as for e4b_moe_forward.
  *   h           [S, I] of h_dtype out, computed in float32 and rounded once.  NaN in a row's pair gives NaN;
- *               the logistic function is 0 below 2^-126.
+ *               the logistic function is 0 below 2^-126.  Infinities go through the formula: a gate of
+ *               -inf gives NaN (-inf * 0, as in e4b_moe_forward), silu of +inf and an infinite unclamped up
+ *               an infinite h, or NaN where the other factor is 0.
  *   codes, scales  NULL, or the checkpoint of `rows` as e4b_checkpoint_rows makes it, out (not with
  *               E4B_DT_I8 rows).
  */
@@ -531,6 +533,10 @@ int e4b_glu(const void* rows, int32_t rows_dtype, const uint8_t* row_scales, int
  *   clamped   with Gc = min(G,7), Uc = clamp(U,-7,7), t = 1.702 * Gc:
  *             g_gate = g * (Uc + 1) * s(t) * (1 + t * (1 - s(t))) where G <= 7, else 0,
  *             g_up = g * Gc * s(t) where |U| <= 7, else 0.
+ * NaN in G reaches both, NaN in U g_gate; what the clamped form sets to 0 (g_gate past G = 7, g_up past
+ * |U| = 7) stays 0.  Infinities: silu's g_gate is NaN for an infinite G, its g_up NaN for G = -inf and
+ * infinite for +inf, and an infinite U enters its g_gate as it is; clamped, g_gate is 0 for either
+ * infinite G and g_up NaN for G = -inf.
  *   g        [S, I] of g_dtype: the gradient of h.
  *   rows, row_scales, flags  as for e4b_glu; after e4b_glu with a checkpoint, its codes and scales.
  *   g_rows   [S, 2I] of g_rows_dtype out, in the layout of `rows`.
