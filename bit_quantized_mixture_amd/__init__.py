@@ -489,7 +489,8 @@ def e4b_grouped_dgrad(fmt, g, w, s, expert_offsets, out_f32=None, out=False, ws=
     g: [S, N] bf16 (rows grouped by expert); w, s: a packed stack as returned by
     e4b_pack_nf4 / e4b_pack_mxfp4 ([E, N, K/2] | [E, N, K/32, 16] and its scales);
     expert_offsets [E+1] int32.  Returns (out_f32 [S, K], out bf16 [S, K] or None); pass
-    out=True to get the bf16 copy.
+    out=True to get the bf16 copy.  N % 64 == 0, K % 64 == 0; operands are fp16 (MXFP4 scale bytes
+    in [104, 140], |g| <= 65504: what lies outside is not refused but comes out infinite or rounded).
     """
     _need(g, "g", _BF16)
     if g.dim() != 2:
@@ -1159,7 +1160,8 @@ def e4b_grouped_gemm_mxfp4(x, x_scales, w, w_scales, expert_offsets, bias=None, 
 
     x [S, K/32, 16] and x_scales [S, K/32] from e4b_quantize_act_mxfp4; w [E, N, K/32, 16] and w_scales
     [E, N, K/32] from e4b_pack_mxfp4; expert_offsets [E+1] int32; bias [E, N] float32 or None.  Returns
-    out [S, N] of `dtype` (bf16 or float32); rows outside every group are not written.
+    out [S, N] of `dtype` (bf16 or float32); rows outside every group are not written.  Any N and any
+    scale bytes; a layer that wants the rows' gradient keeps to what e4b_grouped_dgrad takes.
     """
     u8 = (torch.uint8,)
     _need(w, "w", u8)

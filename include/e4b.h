@@ -368,7 +368,8 @@ int e4b_moe_decode_step(const e4b_decode_args* a, void* stream);
 typedef struct e4b_dgrad_args {
   int32_t fmt;            /* e4b_fmt */
   int32_t reserved;       /* must be 0 */
-  int64_t E, N, K;        /* packed stack [E, N, K] (as packed by e4b_pack_*); N % 64 == 0, K % 64 == 0 */
+  int64_t E, N, K;        /* packed stack [E, N, K] (as packed by e4b_pack_*); N % 64 == 0, K % 64 == 0;
+                           * S*N, S*K and N*K/2 below 2^31, E <= 2^20 */
   int64_t S;              /* grouped rows: expert_offsets[E] */
   const uint16_t* g;      /* [S, N] bf16 bits, rows grouped by expert; values in fp16 range */
   const uint8_t* w;       /* NF4 [E, N, K/2] | MXFP4 [E, N, K/32, 16] */
@@ -582,7 +583,10 @@ typedef struct e4b_mxfp4_gemm_args {
  * released bytes).  Products are exact, sums float32 (past its range infinite, below
  * 2^-126 possibly 0), out is rounded once.  Deterministic.  A scale of 255 makes
  * its row (or its column) NaN.  Rows outside every group are left as they were.  The gradient of the rows
- * that were quantised is e4b_grouped_dgrad's (the rounding passed over).  A dense layer is E = 1.
+ * that were quantised is e4b_grouped_dgrad's (the rounding passed over), which takes less than this call:
+ * N and K in multiples of 64, S*N, S*K and N*K/2 below 2^31, and, as it works in fp16, weights whose scale
+ * bytes lie in [104, 140] (exponents -23 to 13); past those it gives infinite or rounded weights and no
+ * error (see Operand ranges).  A dense layer is E = 1.
  * out overlaps no input.  Synchronous errors as e4b_moe_forward.
  */
 int e4b_grouped_gemm_mxfp4(const e4b_mxfp4_gemm_args* a, void* stream);
