@@ -7,6 +7,7 @@
 
 #include "e4b_groups.h"
 #include "e4b_internal.h"
+#include "e4b_mx_forms.h"
 #include "e4b_rows.h"
 
 namespace e4b {
@@ -670,41 +671,6 @@ __global__ void __launch_bounds__(WK * kWave, RB * CB == 1 ? 4 : 2) few_kernel(G
   }
 }
 
-int64_t div_up(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-int64_t row_tiles(const MxGemmLaunch& L, int bm) {
-  const int64_t used = L.E < L.S ? L.E : L.S;
-  return (L.S + used * (bm - 1)) / bm;
-}
-
-// Rows and columns of a tile.  256 x 256 where an expert has about a hundred rows and more and there is such a
-// tile for most CUs, 128 x 128 below, 64 x 128 where an expert has few.  us with 256 x 256, 128 x 128 and 64 x 128,
-// [5760, 2880] of 32 experts: 8192 rows 149, 176, 217; 4096 97, 114, 130; 2048 85, 81, 91; 1024 70, 70, 67;
-// [4096, 14336] of 8: 4096 rows 159, 190, 224; 2048 (at most 240 large tiles) 112, 127, 134; 1024 (at most 176) 97, 72, 95;
-// [1536, 2048] of 128, 512 and 2048 rows: 38, 35, 33 and 41, 36, 34; of one expert [14336, 4096], 256 rows
-// (56, 224 and 448 tiles): 26, 17, 16.
-// Where those leave CUs without a tile, tiles of 16 x 16 whose waves share K, or for more rows of 32 x 32 and 64 x 64.
-// us with 64 x 128 or 128 x 128, 16 x 16, 32 x 32 and 64 x 64 of one expert, a row at [4096, 14336] 30, 10, -, -; [2880, 2880]
-// 7.5, 4.1, -, -; 32 rows at [4096, 14336] 51, 19, 24, 38; 64: 51, 32, 23, 41; 128: 56, 59, 35, 41; 256: 55, 114, 63, 41; 384: 55,
-// -, 91, 64; 64 rows at [2880, 2880] 11, 6.6, 6.4, 11; at [14336, 4096] 18, 37, 23, 17; of 4 experts' rows at [5760, 2880]
-// (180 tiles) 13.4, 12.7, -, -; 4 experts' 32 rows at [2880, 2880] (at most 630 of 32 x 32) 16, -, 12, 13; of 8 with 4 rows each
-// at [4096, 14336] (256 tiles) 52, 57, -, -.
-struct TileForm {
-  int bm, bn, threads;
-};
-TileForm tile_form(const MxGemmLaunch& L) {
-  const int64_t mean = L.S / (L.E < L.S ? L.E : (L.S > 0 ? L.S : 1));
-  if (mean >= 96 && row_tiles(L, 256) * div_up(L.N, 256) >= cu_count() * 7 / 8) return {256, 256, 512};
-  const int64_t small = row_tiles(L, 32) * div_up(L.N, 32);
-  if (mean <= 16 ? row_tiles(L, 64) * div_up(L.N, 128) < cu_count() : small <= cu_count() * 5 / 2)
-    return mean <= 16 || small < cu_count() ? TileForm{16, 16, 256} : TileForm{32, 32, 256};
-  if (mean > 16 && row_tiles(L, 64) * div_up(L.N, 64) <= cu_count()) return {64, 64, 256};
-  return mean > 24 ? TileForm{128, 128, 256} : TileForm{64, 128, 256};
-}
-int64_t gemm_blocks(const MxGemmLaunch& L) {
-  const TileForm f = tile_form(L);
-  return row_tiles(L, f.bm) * div_up(L.N, f.bn) + 16;  // an XCD has up to one tile of either list more than an eighth
-}
 template <int RB, int CB, int WR, int WC, int RING>
 void tile(const MxGemmLaunch& L, const GemmArgs& a, unsigned grid, hipStream_t s) {
   if (L.out_dtype == 0) hipLaunchKernelGGL((tile_kernel<0, RB, CB, WR, WC, RING>), dim3(grid), dim3(WR * WC * kWave), 0, s, a);
@@ -724,13 +690,16 @@ struct QuantShape {
   int64_t per, pieces, together, waves;
 };
 QuantShape quant_shape(int64_t S, int64_t K) {
-  QuantShape q{K / 8, div_up(K / 8, kWave * kQuantTurns), 1, 0};
+  QuantShape q{K / 8, mx_div_up(K / 8, kWave * kQuantTurns), 1, 0};
   if (q.per <= kWave * kQuantTurns / 2) q.together = kWave * kQuantTurns / q.per;
-  q.waves = div_up(S, q.together) * q.pieces;
+  q.waves = mx_div_up(S, q.together) * q.pieces;
   return q;
 }
-int64_t quantize_mxfp4_items(int64_t S, int64_t K) { return div_up(quant_shape(S, K).waves * kWave, kThreads) * kThreads; }
-int64_t mxfp4_gemm_items(const MxGemmLaunch& L) { return gemm_blocks(L) * tile_form(L).threads; }
+int64_t quantize_mxfp4_items(int64_t S, int64_t K) { return mx_div_up(quant_shape(S, K).waves * kWave, kThreads) * kThreads; }
+int64_t mxfp4_gemm_items(const MxGemmLaunch& L) {
+  const MxTileForm f = mx_tile_form(L.E, L.N, L.S, cu_count());
+  return mx_gemm_blocks(f, L.E, L.N, L.S) * f.threads;
+}
 
 hipError_t launch_quantize_mxfp4(const void* x, int dtype, int64_t T, int64_t K, int k, const int32_t* slots,
                                  uint8_t* blocks, uint8_t* scales, hipStream_t stream) {
@@ -739,7 +708,7 @@ hipError_t launch_quantize_mxfp4(const void* x, int dtype, int64_t T, int64_t K,
   const QuantShape q = quant_shape(S, K);
   const QuantArgs a{x, slots, blocks, scales, K, uint32_t(S), uint32_t(q.per), uint32_t(q.pieces), uint32_t(q.together),
                     uint32_t(q.waves), k};
-  const dim3 grid(unsigned(div_up(q.waves * kWave, kThreads)));
+  const dim3 grid(unsigned(mx_div_up(q.waves * kWave, kThreads)));
   const auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, stream, a); };
   if (q.together > 1) dtype == 0 ? go(quantize_kernel<0, true>) : go(quantize_kernel<1, true>);
   else dtype == 0 ? go(quantize_kernel<0, false>) : go(quantize_kernel<1, false>);
@@ -748,10 +717,11 @@ hipError_t launch_quantize_mxfp4(const void* x, int dtype, int64_t T, int64_t K,
 
 hipError_t launch_mxfp4_gemm(const MxGemmLaunch& L, hipStream_t stream) {
   if (L.S == 0) return hipSuccess;
-  const TileForm f = tile_form(L);
-  const GemmArgs a{L.x, L.xs, L.w, L.ws, L.bias, L.offsets, L.out, L.N, L.K, int(L.S), int(L.E), uint32_t(div_up(L.N, f.bn)),
-                   gemm_blocks(L) <= 12 * cu_count()};
-  const unsigned grid = unsigned(gemm_blocks(L));
+  const MxTileForm f = mx_tile_form(L.E, L.N, L.S, cu_count());
+  const int64_t blocks = mx_gemm_blocks(f, L.E, L.N, L.S);
+  const GemmArgs a{L.x, L.xs, L.w, L.ws, L.bias, L.offsets, L.out, L.N, L.K, int(L.S), int(L.E), uint32_t(mx_div_up(L.N, f.bn)),
+                   mx_two_lists(blocks, cu_count())};
+  const unsigned grid = unsigned(blocks);
   if (f.bm == 256) tile<4, 2, 2, 4, 2>(L, a, grid, stream);
   else if (f.bm == 128) tile<2, 2, 2, 2, 2>(L, a, grid, stream);
   else if (f.bm == 64 && f.bn == 128) tile<2, 1, 1, 4, 3>(L, a, grid, stream);
