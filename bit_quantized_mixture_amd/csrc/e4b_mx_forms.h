@@ -26,6 +26,11 @@ inline int64_t mx_row_tiles(int64_t E, int64_t S, int64_t bm) {
 // -, 91, 64; 64 rows at [2880, 2880] 11, 6.6, 6.4, 11; at [14336, 4096] 18, 37, 23, 17; of 4 experts' rows at [5760, 2880]
 // (180 tiles) 13.4, 12.7, -, -; 4 experts' 32 rows at [2880, 2880] (at most 630 of 32 x 32) 16, -, 12, 13; of 8 with 4 rows each
 // at [4096, 14336] (256 tiles) 52, 57, -, -.
+// The rule sees how many rows and experts there are, not how the rows fall on them, and all of the above are even.  Where
+// the rows of 128 experts fall on 8, us with 256 x 256, 128 x 128 and, the choice there, 64 x 128 (repeated calls, operands
+// in the caches): 512 rows at [4096, 1536] 13, 11, 12, at [1536, 2048] 10, 8.4, 8.4, at [2880, 2880] 18, 14, 12; 1024 rows 14, 14, 15;
+// 14, 8.5, 8.4; 20, 19, 17; 2048 rows 17, 18, 20; 15, 9.2, 10; 23, 21, 25: a sixth lost at most, where 1024 rows spread
+// over all 128 lose a twentieth in the other form.
 struct MxTileForm {
   int bm, bn, threads;
 };
@@ -43,7 +48,10 @@ inline int64_t mx_gemm_blocks(const MxTileForm& f, int64_t E, int64_t N, int64_t
   // an XCD has up to one tile of either list more than an eighth
   return mx_row_tiles(E, S, f.bm) * mx_div_up(N, f.bn) + 16;
 }
-// Short last tiles in a list of their own (find_gemm_tile).
+// Short last tiles in a list of their own (find_gemm_tile) up to 12 tiles a CU.  us in one list and in two:
+// 8192 rows of 8 experts at [N, 4096], 9.8 to 17.1 tiles a CU at most: 308, 297; 346, 342; 377, 373; 455, 452; 537, 538.  Of
+// 32 experts at [5760, 2880], 16384 rows (8.5) 208, 205; 24576 (11.4) 300, 285; 32768 (14.3) 381, 384.  16384 rows of 64 at
+// [8192, 2048] (15.9) 238, 241.  So two lists gain up to a twentieth below and lose a hundredth above.
 inline bool mx_two_lists(int64_t blocks, int cus) { return blocks <= 12 * int64_t(cus); }
 
 }  // namespace e4b

@@ -606,8 +606,9 @@ __device__ __forceinline__ s16x4 lds_read_tr(const uint8_t* at) {
 // One pass instead of two reads m once: 8192 rows of 28672 took 387 us for all gradients with a pass
 // each for u and grad (and float32 matrix instructions), 191 so.
 // With M8 m comes as an 8-bit checkpoint: its blocks are bf16 values exactly, and are put into LDS as such.  Half
-// the bytes, the same time (8192 rows of 4096 in 8 groups 16.8 us, bf16 16): one round of workgroups either way,
-// as long as its longest group; what is saved is the memory that x took until then.
+// the bytes, the same time (8192 rows of 4096 in 8 groups 16.8 us, bf16 16): one round of workgroups either way, each a
+// chain of load, wait and multiply with one block under way, and eight loads of a single exponent byte beside
+// the eight of codes.  More blocks under way have not been built; what is saved is the memory that x took until then.
 template <int RT, int NSUB, bool UP, bool BYCOL, bool M8>
 __global__ void __launch_bounds__(kThreads) grad_kernel(GradArgs p) {
   constexpr int kVStride = kGradRows + 8;               // v^T row in bf16

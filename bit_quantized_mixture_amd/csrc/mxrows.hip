@@ -117,7 +117,8 @@ __device__ __forceinline__ v8i operand4(u32x4 a) { return v8i{int(a[0]), int(a[1
 // share both operands.  In the larger forms, where a launch is few rounds of tiles, last pieces of half the rows
 // and fewer are a list of their own behind all others, so that it ends with short tiles (8192 rows of 32 experts at
 // [5760, 2880], at most 6 tiles a CU, 165 us in one list, 148 so; 4096 of 8 at [4096, 14336], 2, 185 and 155; 16384
-// of 32, 8, 249 and 241; but 8192 of 8 at [28672, 4096], 17, 558 and 563: their columns are fetched twice).  The
+// of 32, 8, 249 and 241; but 8192 of 8 at [28672, 4096], 17, 558 and 563: their columns are fetched twice; where the
+// limit lies is measured at mx_two_lists).  The
 // XCDs, each with an L2 cache of its own, have contiguous stretches of either list, and the workgroups of an XCD
 // (workgroup b runs on XCD b % 8) take its stretches in turn.
 struct GemmTile {

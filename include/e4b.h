@@ -580,8 +580,8 @@ typedef struct e4b_mxfp4_gemm_args {
  * e4b_grouped_gemm_mxfp4 — the rows of one projection of an MXFP4 stack, for the adapters to add to
  * and the activation to read: out[p, :] = W_e x[p] + bias[e] for every row p of expert e, both operands as
  * their codes stand (grouped-nf4-gemm 0.25.0 project description, opening section: MXFP4 on the
- * released bytes).  Products are exact, sums float32 (past its range infinite, below
- * 2^-126 possibly 0), out is rounded once.  Deterministic.  A scale of 255 makes
+ * released bytes).  Products are exact, sums float32 (past its range infinite, or NaN
+ * where sums of both signs pass it; below 2^-126 possibly 0), out is rounded once.  Deterministic.  A scale of 255 makes
  * its row (or its column) NaN.  Rows outside every group are left as they were.  The gradient of the rows
  * that were quantised is e4b_grouped_dgrad's (the rounding passed over), which takes less than this call:
  * N and K in multiples of 64, S*N, S*K and N*K/2 below 2^31, and, as it works in fp16, weights whose scale
